@@ -1,8 +1,9 @@
-"""Python binding of the MI355X sum all-reduce over R simulated ranks.
+"""Python binding of the MI355X sum all-reduce over R simulated ranks, and of
+the operators around it in a tensor-parallel layer.
 
-The functions named ``ar*`` are the C ABI of ``include/ar_allreduce.h``, one
-for one, over ctypes: arguments are marshalled and the result code is
-returned, nothing else happens here.  :class:`Comm` and :func:`rank_buffers`
+The functions named ``ar*`` are the C ABI of ``include/ar_allreduce.h`` and
+``include/ar_block.h``, one for one, over ctypes: arguments are marshalled and
+the result code is returned, nothing else happens here.  :class:`Comm` and :func:`rank_buffers`
 are conveniences on top for torch tensors; torch supplies device memory and
 streams only.  Every step of the all-reduce runs in the HIP kernels of
 ``libar_allreduce.so``; there is no other implementation to fall back to, so a
@@ -17,6 +18,7 @@ from typing import Sequence
 
 LIBRARY = Path(__file__).resolve().parent / "_lib" / "libar_allreduce.so"
 HEADER = Path(__file__).resolve().parent.parent / "include" / "ar_allreduce.h"
+BLOCK_HEADER = HEADER.with_name("ar_block.h")
 
 
 class arResult(IntEnum):
@@ -64,6 +66,14 @@ class arOption(IntEnum):
     arOptLLDense = 15
 
 
+class arActivation(IntEnum):
+    arActNone = 0
+    arActSiLU = 1
+
+
+AR_SCALE_BLOCK = 128
+AR_NORM_MAX_COLS = 32768
+
 AR_MAX_RANKS = 32
 AR_NOALLOC_SCRATCH_BYTES = 64 << 20
 
@@ -101,6 +111,7 @@ def library() -> ctypes.CDLL:
         raise RuntimeError(f"{LIBRARY} is missing: build it with `python -m all_reduce_amd.build`")
     lib = ctypes.CDLL(str(LIBRARY))
     vp, i32, i64, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
+    pvp = ctypes.POINTER(vp)
     sig = {
         "arCommCreate": ([ctypes.POINTER(vp), i32, i32, sz], i32),
         "arCommDestroy": ([vp], i32),
@@ -115,6 +126,10 @@ def library() -> ctypes.CDLL:
         "arCommSetWorkspace": ([vp, vp, sz], i32),
         "arAllReduceNoAlloc": ([ctypes.POINTER(vp), ctypes.POINTER(vp), sz, i32, i32, i32, i32,
                                 vp], i32),
+        "arAllReduceNorm": ([pvp, vp, vp, ctypes.c_float, pvp, pvp, pvp, sz, sz, i32, i32, vp, vp],
+                            i32),
+        "arGateQuant": ([pvp, pvp, pvp, sz, sz, i32, i32, i32, vp, vp], i32),
+        "arMatmulScaled": ([pvp, pvp, pvp, pvp, pvp, sz, sz, sz, i32, i32, i32, vp, vp], i32),
         "arGetErrorString": ([i32], ctypes.c_char_p),
         "arGetVersion": ([], i32),
     }
@@ -221,6 +236,36 @@ def arAllReduceNoAlloc(sendbufs: Sequence[int] | None, recvbufs: Sequence[int] |
                                         int(node_ranks), stream)
 
 
+def arAllReduceNorm(sendbufs, residual, weight, eps: float, residual_out, outbufs, scalebufs,
+                    rows: int, cols: int, dtype: int, nranks: int, comm, stream) -> int:
+    """Device pointers as integers, sequences of them for the rank tables;
+    ``None`` passes NULL."""
+    return library().arAllReduceNorm(
+        _pointer_array(sendbufs, nranks), residual, weight, eps,
+        _pointer_array(residual_out, nranks), _pointer_array(outbufs, nranks),
+        _pointer_array(scalebufs, nranks), rows, cols, int(dtype), nranks, comm, stream)
+
+
+def arGateQuant(inbufs, outbufs, scalebufs, rows: int, cols: int, dtype: int, act: int,
+                nranks: int, comm, stream) -> int:
+    """Device pointers as integers, sequences of them for the rank tables;
+    ``None`` passes NULL."""
+    return library().arGateQuant(
+        _pointer_array(inbufs, nranks), _pointer_array(outbufs, nranks),
+        _pointer_array(scalebufs, nranks), rows, cols, int(dtype), int(act), nranks, comm, stream)
+
+
+def arMatmulScaled(abufs, ascales, bbufs, bscales, outbufs, rows: int, n: int, k: int,
+                   out_dtype: int, reduce: int, nranks: int, comm, stream) -> int:
+    """Device pointers as integers, sequences of them for the rank tables;
+    ``None`` passes NULL."""
+    return library().arMatmulScaled(
+        _pointer_array(abufs, nranks), _pointer_array(ascales, nranks),
+        _pointer_array(bbufs, nranks), _pointer_array(bscales, nranks),
+        _pointer_array(outbufs, nranks), rows, n, k, int(out_dtype), int(reduce), nranks, comm,
+        stream)
+
+
 # ---- torch conveniences ---------------------------------------------------
 def _torch():
     import torch
@@ -241,6 +286,18 @@ def protocol_code(protocol) -> arProtocol:
         return {"ll": arProtocol.arProtoLL, "hb": arProtocol.arProtoHB,
                 "auto": arProtocol.arProtoAuto}[protocol.lower()]
     return arProtocol(protocol)
+
+
+def activation_code(act) -> arActivation:
+    if isinstance(act, str):
+        return {"none": arActivation.arActNone, "silu": arActivation.arActSiLU}[act.lower()]
+    return arActivation(act)
+
+
+def scale_blocks(cols: int) -> int:
+    """Scales that `cols` columns (or a weight's rows) have: one for each 128, the
+    last block shorter."""
+    return -(-cols // AR_SCALE_BLOCK)
 
 
 def rank_buffers(nranks: int, count: int, dtype, device, align: int = 256):
@@ -393,6 +450,116 @@ class Comm:
         send, recv = self._check_ranks(send, recv)
         return PreparedAllReduce(self, send, recv, protocol_code(protocol), self._stream(stream))
 
+    def all_reduce_norm(self, send, weight, eps: float, residual=None, residual_out=None,
+                        out=None, scales=None, stream=None):
+        """All-reduce, residual addition and root-mean-square norm in one pass
+        (see arAllReduceNorm).  ``send``, ``residual_out`` (or None: not kept) and
+        ``out`` are lists of one [rows, cols] tensor a rank, ``residual`` (or
+        None) one such tensor, ``weight`` [cols].  ``out`` has the element type,
+        or torch.float8_e4m3fn with ``scales`` a list of float32
+        [scale_blocks(cols), rows].  Returns ``out``."""
+        self.prepare_all_reduce_norm(send, weight, eps, residual, residual_out, out, scales,
+                                     stream)()
+        return out
+
+    def prepare_all_reduce_norm(self, send, weight, eps: float, residual=None,
+                                residual_out=None, out=None, scales=None,
+                                stream=None) -> "PreparedCall":
+        """``all_reduce_norm`` with its arguments marshalled once (see ``prepare``)."""
+        torch = _torch()
+        rows, cols, dtype = self._matrix(send)
+        if out is None:
+            raise ValueError("need one output tensor per rank")
+        n = len(send)
+        eight = scales is not None
+        self._check("send", send, n, (rows, cols), dtype)
+        self._check("weight", [weight], 1, (cols,), dtype)
+        if residual is not None:
+            self._check("residual", [residual], 1, (rows, cols), dtype)
+        if residual_out is not None:
+            self._check("residual_out", residual_out, n, (rows, cols), dtype)
+        self._check("out", out, n, (rows, cols), torch.float8_e4m3fn if eight else dtype)
+        if eight:
+            self._check("scales", scales, n, (scale_blocks(cols), rows), torch.float32)
+        return PreparedCall(self, "arAllReduceNorm", (
+            _rank_table(send), None if residual is None else residual.data_ptr(),
+            weight.data_ptr(), float(eps), _rank_table(residual_out), _rank_table(out),
+            _rank_table(scales), rows, cols, int(dtype_code(dtype)), n), self._stream(stream),
+            (send, weight, residual, residual_out, out, scales))
+
+    def gate_quant(self, x, out, scales, act="silu", stream=None):
+        """Activation and quantisation to 8 bits for every rank (see arGateQuant).
+        ``x`` is a list of one [rows, cols] tensor a rank, or [rows, 2 * cols]
+        with ``act`` "silu" (gate, then up); ``out`` of [rows, cols]
+        torch.float8_e4m3fn, ``scales`` of float32 [scale_blocks(cols), rows].
+        Returns ``out``."""
+        self.prepare_gate_quant(x, out, scales, act, stream)()
+        return out
+
+    def prepare_gate_quant(self, x, out, scales, act="silu", stream=None) -> "PreparedCall":
+        """``gate_quant`` with its arguments marshalled once (see ``prepare``)."""
+        torch = _torch()
+        rows, wide, dtype = self._matrix(x)
+        code = activation_code(act)
+        n, cols = len(x), wide // 2 if code == arActivation.arActSiLU else wide
+        if code == arActivation.arActSiLU and wide % 2 != 0:
+            raise ValueError("gated inputs need an even number of columns")
+        self._check("x", x, n, (rows, wide), dtype)
+        self._check("out", out, n, (rows, cols), torch.float8_e4m3fn)
+        self._check("scales", scales, n, (scale_blocks(cols), rows), torch.float32)
+        return PreparedCall(self, "arGateQuant", (
+            _rank_table(x), _rank_table(out), _rank_table(scales), rows, cols,
+            int(dtype_code(dtype)), int(code), n), self._stream(stream), (x, out, scales))
+
+    def matmul_scaled(self, a, a_scales, b, b_scales, out, reduce: bool = False, stream=None):
+        """The product of 8-bit activations and weights with a scale per block of
+        128 (see arMatmulScaled).  Lists of one tensor a rank: ``a`` [rows, k] and
+        ``b`` [n, k] torch.float8_e4m3fn, ``a_scales`` float32
+        [scale_blocks(k), rows], ``b_scales`` float32
+        [scale_blocks(n), scale_blocks(k)], ``out`` [rows, n] bfloat16, float16 or
+        float32: each rank's own product, or with ``reduce`` the sum of all of
+        them in every rank's output.  Returns ``out``."""
+        self.prepare_matmul_scaled(a, a_scales, b, b_scales, out, reduce, stream)()
+        return out
+
+    def prepare_matmul_scaled(self, a, a_scales, b, b_scales, out, reduce: bool = False,
+                              stream=None) -> "PreparedCall":
+        """``matmul_scaled`` with its arguments marshalled once (see ``prepare``)."""
+        torch = _torch()
+        eight = torch.float8_e4m3fn
+        rows, k, _ = self._matrix(a)
+        cols, _, _ = self._matrix(b)
+        _, _, dtype = self._matrix(out)
+        n = len(a)
+        self._check("a", a, n, (rows, k), eight)
+        self._check("a_scales", a_scales, n, (scale_blocks(k), rows), torch.float32)
+        self._check("b", b, n, (cols, k), eight)
+        self._check("b_scales", b_scales, n, (scale_blocks(cols), scale_blocks(k)), torch.float32)
+        self._check("out", out, n, (rows, cols), dtype)
+        return PreparedCall(self, "arMatmulScaled", (
+            _rank_table(a), _rank_table(a_scales), _rank_table(b), _rank_table(b_scales),
+            _rank_table(out), rows, cols, k, int(dtype_code(dtype)), int(bool(reduce)), n),
+            self._stream(stream), (a, a_scales, b, b_scales, out))
+
+    @staticmethod
+    def _matrix(tensors):
+        """(rows, columns, dtype) of the first of a list of matrices."""
+        if not tensors or tensors[0].dim() != 2:
+            raise ValueError("need one two-dimensional tensor per rank")
+        return (*tensors[0].shape, tensors[0].dtype)
+
+    def _check(self, name, tensors, count, shape, dtype):
+        if len(tensors) != count:
+            raise ValueError(f"{name}: need {count} tensors, got {len(tensors)}")
+        for t in tensors:
+            if t.device != self.device:
+                raise ValueError(f"{name}: tensor on {t.device}, communicator on {self.device}")
+            if tuple(t.shape) != shape or t.dtype != dtype:
+                raise ValueError(f"{name}: need {shape} of {dtype}, got {tuple(t.shape)} of "
+                                 f"{t.dtype}")
+            if not t.is_contiguous():
+                raise ValueError(f"{name}: tensors must be contiguous")
+
     def _check_ranks(self, send, recv):
         if recv is None:
             recv = send
@@ -437,3 +604,34 @@ class PreparedAllReduce:
         r = self._fn(*self._head, h, self._tail)
         if r != 0:
             raise ArError(r, "arAllReduce")
+
+
+def _rank_table(tensors):
+    """The pointer array of one tensor a rank; None passes NULL."""
+    return None if tensors is None else \
+        (ctypes.c_void_p * len(tensors))(*[t.data_ptr() for t in tensors])
+
+
+class PreparedCall:
+    """One call of an operator of ``ar_block.h`` whose arguments were marshalled
+    once: calling it is a single foreign call.  Made by the ``Comm.prepare_*``
+    methods; the tensors are kept alive.  As with ``PreparedAllReduce``, the
+    communicator's handle is read at each call."""
+
+    __slots__ = ("_fn", "_name", "_head", "_tail", "_comm", "_keep")
+
+    def __init__(self, comm, name, head, stream, keep):
+        self._fn = getattr(library(), name)
+        self._name = name
+        self._head = head
+        self._tail = stream
+        self._comm = comm
+        self._keep = keep
+
+    def __call__(self):
+        h = self._comm.handle
+        if h is None:
+            raise ValueError("the communicator of this prepared call was closed")
+        r = self._fn(*self._head, h, self._tail)
+        if r != 0:
+            raise ArError(r, self._name)

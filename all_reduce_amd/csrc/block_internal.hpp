@@ -1,0 +1,58 @@
+// block_internal.hpp -- what the entry points of ar_block.h and their kernel
+// files share.
+#pragma once
+
+#include "ar_allreduce.h"
+#include "ar_block.h"
+#include "ar_internal.hpp"
+
+namespace ar {
+
+// Rank tables of the block operators, passed by value in the kernel arguments
+// and indexed at run time: the index is the same in every lane, so a pointer
+// is one scalar load, and one kernel serves every rank count.
+struct NormArgs {
+    const char *send[AR_MAX_RANKS];
+    char *res_out[AR_MAX_RANKS];  // unused where has_res_out is 0
+    char *out[AR_MAX_RANKS];
+    float *scales[AR_MAX_RANKS];  // unused for an output in the element type
+    const char *residual;         // nullptr: none
+    const char *weight;
+    uint64_t rows;
+    uint32_t cols;
+    uint32_t nranks;
+    uint32_t has_res_out;
+    float eps;
+};
+
+struct GateArgs {
+    const char *in[AR_MAX_RANKS];
+    char *out[AR_MAX_RANKS];
+    float *scales[AR_MAX_RANKS];
+    uint64_t rows;
+    uint64_t cols;
+};
+
+struct MatmulArgs {
+    const char *a[AR_MAX_RANKS];
+    const float *sa[AR_MAX_RANKS];
+    const char *b[AR_MAX_RANKS];
+    const float *sb[AR_MAX_RANKS];
+    char *out[AR_MAX_RANKS];
+    uint32_t rows;
+    uint32_t n;
+    uint32_t k;
+    uint32_t kblocks;  // ceil(k / 128)
+    uint32_t nranks;
+};
+
+// Launchers: validate nothing (the entry points did), pick the kernel and
+// enqueue it on `stream`.
+hipError_t launch_norm(const NormArgs &args, int dtype, bool eight, int cu_count,
+                       hipStream_t stream);
+hipError_t launch_gate(const GateArgs &args, int dtype, int act, int nranks, int cu_count,
+                       hipStream_t stream);
+hipError_t launch_matmul(const MatmulArgs &args, int out_dtype, bool reduce, int cu_count,
+                         hipStream_t stream);
+
+}  // namespace ar
