@@ -257,6 +257,8 @@ arResult_t arMatmulScaled(const void *const *abufs, const float *const *ascales,
     const size_t most = (size_t)1 << 30;
     if (rows > most || n > most || k > most)
         return reject(arInvalidArgument, "rows, n and k must be at most 2^30");
+    if (rows * n > ((size_t)1 << 40))
+        return reject(arInvalidArgument, "rows * n must be at most 2^40");
     Ranges mem;
     if (!mem.add_ranks(abufs, nranks, rows * k, false) ||
         !mem.add_ranks((const void *const *)ascales, nranks,

@@ -54,5 +54,10 @@ hipError_t launch_gate(const GateArgs &args, int dtype, int act, int nranks, int
                        hipStream_t stream);
 hipError_t launch_matmul(const MatmulArgs &args, int out_dtype, bool reduce, int cu_count,
                          hipStream_t stream);
+// Its kernel for many rows (block_matmul_tile.hip), whose 32-bit offsets
+// inside a tile of 256 rows limit k.
+constexpr uint32_t kTileMaxK = 1u << 23;
+hipError_t launch_matmul_tile(const MatmulArgs &args, int out_dtype, bool reduce,
+                              hipStream_t stream);
 
 }  // namespace ar

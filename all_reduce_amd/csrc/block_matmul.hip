@@ -16,54 +16,9 @@
 // (output columns) 4 (l / 16) .. + 3.
 #include "block_device.hpp"
 #include "block_internal.hpp"
+#include "block_matmul.hpp"
 
 namespace ar {
-
-typedef int i32x8 __attribute__((ext_vector_type(8)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-
-// Bytes 8 s .. 8 s + 7 of a lane's block as bfloat16, exactly.
-__device__ inline bf16x8 widen_eight(i32x8 x, int s)
-{
-    bf16x8 r;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const bf16x2 v = i % 2 == 0
-                             ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[2 * s + i / 2], 1.0f, false)
-                             : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[2 * s + i / 2], 1.0f, true);
-        r[2 * i] = v[0];
-        r[2 * i + 1] = v[1];
-    }
-    return r;
-}
-
-// The sums of one block of 128 products, 16 x 16 of them.
-//
-// The 8-bit instruction adds products in groups of eight (8 consecutive k);
-// inside a group each product is cut, toward zero, at 2^-13 of the largest
-// one's leading bit, and the groups' sums are added in binary32.  Measured on
-// MI355X: normal inputs come out 1.4e-5 off in the 2-norm (a binary32 sum is
-// 1e-7 off).  That is far below an output's rounding to 16 bits (2^-9 and
-// 2^-12), so 16-bit outputs take it; a binary32 output (EXACT) would show it,
-// so there the values are widened to bfloat16, which holds them exactly, and
-// multiplied at that type's rate, a third of the 8-bit one (1320 against 4460
-// TFLOP/s of instructions alone), to binary32 sums 1e-8 off.
-template <bool EXACT>
-__device__ inline f32x4 block_sums(i32x8 a, i32x8 b)
-{
-    f32x4 c = {0, 0, 0, 0};
-    if constexpr (EXACT) {
-#pragma unroll
-        for (int s = 0; s < 4; ++s)
-            c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen_eight(a, s), widen_eight(b, s), c, 0, 0,
-                                                        0);
-        return c;
-    } else {
-        // formats 0 and 0: e4m3 for both operands; no hardware scales
-        return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, 0, 0, 0);
-    }
-}
 
 // The lane's 32 bytes of one block of one row (`row_at`: the row's start plus
 // the lane's 16 g; `left`: bytes of the row from there on; rows end on a
@@ -194,6 +149,8 @@ hipError_t enqueue(const MatmulArgs &args, bool reduce, hipStream_t stream)
 template <typename T>
 hipError_t pick(const MatmulArgs &args, bool reduce, hipStream_t stream)
 {
+    if (args.rows > 128 && args.k <= kTileMaxK)
+        return launch_matmul_tile(args, T::kId, reduce, stream);
     return args.rows <= 16 ? enqueue<T, 1>(args, reduce, stream)
                            : enqueue<T, 4>(args, reduce, stream);
 }

@@ -1,0 +1,283 @@
+// block_matmul_tile.hip -- the block-scaled 8-bit product for many rows.
+//
+// A workgroup of eight waves computes 256 rows x 256 output columns; a step
+// is one block of 128 of k (of all ranks' k, one rank after the other, in the
+// form that sums over the ranks).  A step's 64 KiB of inputs go from global
+// memory straight to LDS (no registers in between), two steps' worth in
+// turn, so that one is loaded while the other is multiplied.  A wave computes
+// 64 rows x 128 columns in 32x32 tiles: the columns of a wave lie in one
+// weight scale block, so a step's scale is one number a lane and row tile,
+// applied with a fused multiply-add to the running sums.
+//
+// LDS rows are the 128 bytes of a step, in eight pieces of 16; piece c of row
+// r is kept at place c ^ (r / 2 % 8).  Two rows cover all banks once, so 16
+// rows of one piece, read together, lie in 16 different places (with r % 8,
+// rows 8 apart met: half of the LDS cycles were conflicts).  A direct load
+// writes its lanes' pieces one after the other, so the exchange is made in
+// the lanes' global addresses.
+#include "block_device.hpp"
+#include "block_internal.hpp"
+#include "block_matmul.hpp"
+
+namespace ar {
+
+constexpr uint32_t kTile = 256;                 // rows, and columns, of a workgroup
+constexpr uint32_t kStepBytes = kTile * 128u;   // of one operand
+
+// 16 bytes a lane from base + off to LDS at `to` + 16 * lane (`base` and `to`
+// are the same in every lane).  The compiler does not see the load: whoever
+// reads the bytes waits for vmcnt(0) first.
+__device__ inline void to_lds(const char *base, uint32_t off, uint32_t to)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                 :
+                 : "s"(to), "v"(off), "s"(base)
+                 : "memory");
+}
+
+// The same from an address of the lane's own.
+__device__ inline void to_lds_any(const char *at, uint32_t to)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+                 :
+                 : "s"(to), "v"(at)
+                 : "memory");
+}
+
+// What a lane's pieces past the end of a row are loaded from.
+__device__ uint32_t kZeros[4];
+
+template <typename T, bool REDUCE>
+__global__ __launch_bounds__(512, 2) void matmul_tile(MatmulArgs p)
+{
+    constexpr bool kExact = T::kBytes == 4;
+    __shared__ __align__(128) char lds[4 * kStepBytes];  // rows, rows, columns, columns
+    const uint32_t lane = threadIdx.x & 63u;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+
+    // Workgroup w runs on XCD w % 8: each XCD takes consecutive tiles, and 32
+    // consecutive tiles are 8 x 4, which its second-level cache serves with 12
+    // tiles' inputs instead of 64.
+    const uint32_t mt = (p.rows + kTile - 1) / kTile, nt = (p.n + kTile - 1) / kTile;
+    const uint32_t tiles = mt * nt * (REDUCE ? 1u : p.nranks);
+    uint32_t t = (blockIdx.x & 7u) * ((tiles + 7u) / 8u) + blockIdx.x / 8u;
+    if (blockIdx.x / 8u >= (tiles + 7u) / 8u || t >= tiles)
+        return;
+    const uint32_t rank0 = REDUCE ? 0u : t / (mt * nt);
+    t -= rank0 * mt * nt;
+    const uint32_t band = t / (mt * 4u);                      // four columns of tiles
+    const uint32_t wide = nt - band * 4u < 4u ? nt - band * 4u : 4u;
+    t -= band * mt * 4u;
+    const uint32_t m0 = t / wide * kTile, n0 = (band * 4u + t % wide) * kTile;
+
+    // This wave loads 32 rows and 32 columns, eight at a time; rows past the
+    // end repeat the last one, and what comes of them is not stored.
+    uint32_t offm[4], offn[4];
+    const uint32_t piece = (lane & 7u) ^ (lane >> 4);  // of even groups of eight; odd ones ^ 4
+#pragma unroll
+    for (uint32_t i = 0; i < 4; ++i) {
+        const uint32_t r = wave * 32u + i * 8u + (lane >> 3);
+        offm[i] = (r < p.rows - m0 ? r : p.rows - m0 - 1u) * p.k + (piece ^ (i & 1u) * 4u) * 16u;
+        offn[i] = (r < p.n - n0 ? r : p.n - n0 - 1u) * p.k + (piece ^ (i & 1u) * 4u) * 16u;
+    }
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)lds;
+    const uint32_t to = __builtin_amdgcn_readfirstlane(lds0) + wave * 4096u;
+
+    // This wave multiplies rows wm .. wm + 63 and columns wn .. wn + 127.
+    const uint32_t wm = (wave & 3u) * 64u, wn = (wave >> 2) * 128u;
+    const uint32_t l32 = lane & 31u, half = lane >> 5;
+    const uint32_t place = l32 * 128u + ((half * 2u) ^ (l32 >> 1 & 7u)) * 16u;
+    uint32_t m[2];
+#pragma unroll
+    for (uint32_t j = 0; j < 2; ++j) {
+        const uint32_t row = m0 + wm + j * 32u + l32;
+        m[j] = row < p.rows ? row : p.rows - 1u;
+    }
+    const uint32_t nblock = (n0 + wn) / 128u;  // past the end only where nothing is stored
+    const bool live = n0 + wn < p.n;
+
+    const uint32_t nranks = REDUCE ? p.nranks : 1u;
+    const uint32_t steps = p.kblocks * nranks;
+
+    // What the next load reads: a rank's operands and scales, from block kb on.
+    // The weight scale is loaded like the others, by a vector instruction: a
+    // scalar one shares its wait counter with LDS reads, which would then wait
+    // for it in every step.
+    const char *a = nullptr, *b = nullptr;
+    const float *sa = nullptr, *sb = nullptr;
+    uint32_t sb_off = (live ? nblock : 0u) * p.kblocks;
+    asm volatile("" : "+v"(sb_off));
+    auto at_rank = [&](uint32_t r) {
+        a = p.a[rank0 + r] + (uint64_t)m0 * p.k;
+        b = p.b[rank0 + r] + (uint64_t)n0 * p.k;
+        sa = p.sa[rank0 + r];
+        sb = p.sb[rank0 + r];
+    };
+    // Loads of one step into half `stage` of LDS, and its scales (multiplied
+    // later: here that would wait for all of these loads).
+    auto load = [&](uint32_t kb, uint32_t stage, float (&s)[3]) {
+        const uint32_t at = to + stage * kStepBytes;
+        if (kb * 128u + 128u <= p.k) {
+#pragma unroll
+            for (uint32_t i = 0; i < 4; ++i) {
+                to_lds(a, offm[i], at + i * 1024u);
+                to_lds(b, offn[i], at + 2 * kStepBytes + i * 1024u);
+            }
+        } else {
+#pragma unroll
+            for (uint32_t i = 0; i < 4; ++i) {
+                const bool in = kb * 128u + (piece ^ (i & 1u) * 4u) * 16u < p.k;
+                to_lds_any(in ? a + offm[i] : (const char *)kZeros, at + i * 1024u);
+                to_lds_any(in ? b + offn[i] : (const char *)kZeros,
+                           at + 2 * kStepBytes + i * 1024u);
+            }
+        }
+#pragma unroll
+        for (uint32_t j = 0; j < 2; ++j)
+            s[j] = sa[m[j]];
+        s[2] = sb[sb_off];
+        a += 128;
+        b += 128;
+        sa += p.rows;
+        sb += 1;
+    };
+
+    f32x16 acc[4][2] = {};
+    uint32_t r = 0, kb = 0;
+    float s[2], s_next[3];
+    at_rank(0);
+    load(0, 0, s_next);
+    for (uint32_t step = 0; step < steps; ++step) {
+        const uint32_t stage = step & 1u;
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        // After this every wave's loads of this step are in LDS, and no wave
+        // reads the other half any more.
+        __syncthreads();
+        s[0] = s_next[0] * s_next[2];
+        s[1] = s_next[1] * s_next[2];
+        // (here, where they are at hand: a wait for them further down would
+        // also wait for the next step's loads)
+        asm volatile("" : "+v"(s[0]), "+v"(s[1]));
+        const char *pm = lds + stage * kStepBytes + wm * 128u;
+        const char *pn = lds + (2u + stage) * kStepBytes + wn * 128u;
+        i32x8 x[2][2], w[2];
+#pragma unroll
+        for (uint32_t h = 0; h < 2; ++h) {
+            x[0][h] = pieces(pm, place ^ (h * 64u));
+            w[h] = pieces(pn, place ^ (h * 64u));
+        }
+#pragma unroll
+        for (uint32_t h = 0; h < 2; ++h)
+            x[1][h] = pieces(pm + 4096u, place ^ (h * 64u));
+        __builtin_amdgcn_sched_barrier(0);
+        if (step + 1u < steps) {
+            if (++kb == p.kblocks) {
+                kb = 0;
+                at_rank(++r);
+            }
+            load(kb, stage ^ 1u, s_next);
+        }
+        // A tile's products are under way while the one before it is scaled.
+        f32x16 c[2];
+#pragma unroll
+        for (uint32_t i = 0; i < 4; ++i) {
+            if (i > 0) {
+#pragma unroll
+                for (uint32_t h = 0; h < 2; ++h)
+                    w[h] = pieces(pn + i * 4096u, place ^ (h * 64u));
+            }
+#pragma unroll
+            for (uint32_t j = 0; j < 2; ++j) {
+                c[j] = block_sums32<kExact>(w, x[j]);
+                __builtin_amdgcn_sched_barrier(0);
+                if (i + j > 0) {
+                    const uint32_t pi = j == 0 ? i - 1u : i, pj = j ^ 1u;
+#pragma unroll
+                    for (uint32_t e = 0; e < 16; ++e)
+                        acc[pi][pj][e] = __builtin_fmaf(c[pj][e], s[pj], acc[pi][pj][e]);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+#pragma unroll
+        for (uint32_t e = 0; e < 16; ++e)
+            acc[3][1][e] = __builtin_fmaf(c[1][e], s[1], acc[3][1][e]);
+    }
+
+    // The sums go through LDS, 32 rows x 128 columns of a wave at a time, so
+    // that a store covers whole lines: 16-byte pieces, piece c of row r at
+    // place c ^ (r % 16) (of 16 pieces for 16-bit outputs, 32 for binary32).
+    __syncthreads();
+    constexpr uint32_t kRow = 128u * T::kBytes;
+    char *mine = lds + wave * (32u * kRow);
+#pragma unroll
+    for (uint32_t j = 0; j < 2; ++j) {
+#pragma unroll
+        for (uint32_t i = 0; i < 4; ++i) {
+#pragma unroll
+            for (uint32_t q = 0; q < 4; ++q) {
+                const uint32_t col = i * 32u + q * 8u + half * 4u;
+                float f[4];
+#pragma unroll
+                for (uint32_t e = 0; e < 4; ++e)
+                    f[e] = acc[i][j][q * 4u + e];
+                uint32_t v[T::kBytes];
+#pragma unroll
+                for (uint32_t e = 0; e < 4 / T::kPerWord; ++e)
+                    v[e] = T::narrow(f + e * T::kPerWord);
+                const uint32_t at = col * T::kBytes;
+                char *to16 = mine + l32 * kRow + (((at >> 4) ^ (l32 & 15u)) << 4) + (at & 15u);
+                __builtin_memcpy(__builtin_assume_aligned(to16, 2 * T::kBytes * 2), v, 4 * T::kBytes);
+            }
+        }
+        // (a wave's own LDS accesses are in order, and no other wave's are here)
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        constexpr uint32_t kPieces = kRow / 16u, kEach = 16u / T::kBytes;
+#pragma unroll
+        for (uint32_t u = 0; u < 32u * kPieces / 64u; ++u) {
+            const uint32_t row = u * (64u / kPieces) + lane / kPieces;
+            const uint32_t c = lane % kPieces;
+            const u32x4 v = *(const u32x4 *)(mine + row * kRow + ((c ^ (row & 15u)) << 4));
+            const uint32_t gm = m0 + wm + j * 32u + row, gn = n0 + wn + c * kEach;
+            if (gm < p.rows && gn < p.n) {
+                const uint64_t at = ((uint64_t)gm * p.n + gn) * T::kBytes;
+                if constexpr (REDUCE) {
+                    for (uint32_t o = 0; o < p.nranks; ++o)
+                        store_piece<T>(p.out[o] + at, v, p.n - gn);
+                } else {
+                    store_piece<T>(p.out[rank0] + at, v, p.n - gn);
+                }
+            }
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    }
+}
+
+namespace {
+
+template <typename T>
+hipError_t enqueue(const MatmulArgs &args, bool reduce, hipStream_t stream)
+{
+    const uint32_t tiles = (args.rows + kTile - 1) / kTile * ((args.n + kTile - 1) / kTile) *
+                           (reduce ? 1u : args.nranks);
+    const dim3 grid((tiles + 7u) / 8u * 8u);
+    if (reduce)
+        hipLaunchKernelGGL((matmul_tile<T, true>), grid, dim3(512), 0, stream, args);
+    else
+        hipLaunchKernelGGL((matmul_tile<T, false>), grid, dim3(512), 0, stream, args);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_matmul_tile(const MatmulArgs &args, int out_dtype, bool reduce,
+                              hipStream_t stream)
+{
+    switch (out_dtype) {
+    case kBf16: return enqueue<Bf16>(args, reduce, stream);
+    case kFp16: return enqueue<Fp16>(args, reduce, stream);
+    default: return enqueue<Fp32>(args, reduce, stream);
+    }
+}
+
+}  // namespace ar

@@ -129,8 +129,9 @@ arResult_t arGateQuant(const void *const *inbufs, void *const *outbufs, float *c
  *  k               a multiple of 16, at least 16 (else arUnsupported).
  *  outDtype        arBfloat16, arFloat16 or arFloat32 (else arUnsupported).
  * Rules (arInvalidArgument when broken): no NULL pointer; every pointer
- * 16-byte aligned; rows, n and k at most 2^30; no written range overlaps another
- * written or read one (inputs may be shared between ranks). */
+ * 16-byte aligned; rows, n and k at most 2^30 and rows * n at most 2^40; no
+ * written range overlaps another written or read one (inputs may be shared
+ * between ranks). */
 arResult_t arMatmulScaled(const void *const *abufs, const float *const *ascales,
                           const void *const *bbufs, const float *const *bscales,
                           void *const *outbufs, size_t rows, size_t n, size_t k,
