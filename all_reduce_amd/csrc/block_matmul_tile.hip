@@ -15,6 +15,8 @@
 // rows 8 apart met: half of the LDS cycles were conflicts).  A direct load
 // writes its lanes' pieces one after the other, so the exchange is made in
 // the lanes' global addresses.
+#include <type_traits>
+
 #include "block_device.hpp"
 #include "block_internal.hpp"
 #include "block_matmul.hpp"
@@ -34,18 +36,6 @@ __device__ inline void to_lds(const char *base, uint32_t off, uint32_t to)
                  : "s"(to), "v"(off), "s"(base)
                  : "memory");
 }
-
-// The same from an address of the lane's own.
-__device__ inline void to_lds_any(const char *at, uint32_t to)
-{
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
-                 :
-                 : "s"(to), "v"(at)
-                 : "memory");
-}
-
-// What a lane's pieces past the end of a row are loaded from.
-__device__ uint32_t kZeros[4];
 
 template <typename T, bool REDUCE>
 __global__ __launch_bounds__(512, 2) void matmul_tile(MatmulArgs p)
@@ -73,12 +63,12 @@ __global__ __launch_bounds__(512, 2) void matmul_tile(MatmulArgs p)
     // This wave loads 32 rows and 32 columns, eight at a time; rows past the
     // end repeat the last one, and what comes of them is not stored.
     uint32_t offm[4], offn[4];
-    const uint32_t piece = (lane & 7u) ^ (lane >> 4);  // of even groups of eight; odd ones ^ 4
+    const uint32_t piece16 = ((lane & 7u) ^ (lane >> 4)) * 16u;  // even groups of eight; odd ^ 64
 #pragma unroll
     for (uint32_t i = 0; i < 4; ++i) {
         const uint32_t r = wave * 32u + i * 8u + (lane >> 3);
-        offm[i] = (r < p.rows - m0 ? r : p.rows - m0 - 1u) * p.k + (piece ^ (i & 1u) * 4u) * 16u;
-        offn[i] = (r < p.n - n0 ? r : p.n - n0 - 1u) * p.k + (piece ^ (i & 1u) * 4u) * 16u;
+        offm[i] = (r < p.rows - m0 ? r : p.rows - m0 - 1u) * p.k + (piece16 ^ (i & 1u) * 64u);
+        offn[i] = (r < p.n - n0 ? r : p.n - n0 - 1u) * p.k + (piece16 ^ (i & 1u) * 64u);
     }
     const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)lds;
     const uint32_t to = __builtin_amdgcn_readfirstlane(lds0) + wave * 4096u;
@@ -93,98 +83,104 @@ __global__ __launch_bounds__(512, 2) void matmul_tile(MatmulArgs p)
         const uint32_t row = m0 + wm + j * 32u + l32;
         m[j] = row < p.rows ? row : p.rows - 1u;
     }
-    const uint32_t nblock = (n0 + wn) / 128u;  // past the end only where nothing is stored
-    const bool live = n0 + wn < p.n;
 
+    // What the next load reads: block kb of rank r, from these on.  The weight
+    // scale is loaded like the others, by a vector instruction: a scalar one
+    // shares its wait counter with LDS reads, which would then wait for it in
+    // every step.
     const uint32_t nranks = REDUCE ? p.nranks : 1u;
-    const uint32_t steps = p.kblocks * nranks;
-
-    // What the next load reads: a rank's operands and scales, from block kb on.
-    // The weight scale is loaded like the others, by a vector instruction: a
-    // scalar one shares its wait counter with LDS reads, which would then wait
-    // for it in every step.
-    const char *a = nullptr, *b = nullptr;
-    const float *sa = nullptr, *sb = nullptr;
-    uint32_t sb_off = (live ? nblock : 0u) * p.kblocks;
+    uint32_t r = 0, kb = 0;
+    const char *a, *b;
+    const float *sa, *sb;
+    uint32_t sb_off = n0 + wn < p.n ? (n0 + wn) / 128u * p.kblocks : 0u;
     asm volatile("" : "+v"(sb_off));
-    auto at_rank = [&](uint32_t r) {
+    auto at_rank = [&] {
         a = p.a[rank0 + r] + (uint64_t)m0 * p.k;
         b = p.b[rank0 + r] + (uint64_t)n0 * p.k;
         sa = p.sa[rank0 + r];
         sb = p.sb[rank0 + r];
     };
-    // Loads of one step into half `stage` of LDS, and its scales (multiplied
-    // later: here that would wait for all of these loads).
-    auto load = [&](uint32_t kb, uint32_t stage, float (&s)[3]) {
-        const uint32_t at = to + stage * kStepBytes;
-        if (kb * 128u + 128u <= p.k) {
-#pragma unroll
-            for (uint32_t i = 0; i < 4; ++i) {
-                to_lds(a, offm[i], at + i * 1024u);
-                to_lds(b, offn[i], at + 2 * kStepBytes + i * 1024u);
-            }
-        } else {
-#pragma unroll
-            for (uint32_t i = 0; i < 4; ++i) {
-                const bool in = kb * 128u + (piece ^ (i & 1u) * 4u) * 16u < p.k;
-                to_lds_any(in ? a + offm[i] : (const char *)kZeros, at + i * 1024u);
-                to_lds_any(in ? b + offn[i] : (const char *)kZeros,
-                           at + 2 * kStepBytes + i * 1024u);
-            }
-        }
+    // Eight rows and eight columns of them into half `stage` of LDS.  A piece
+    // past the end of its row repeats the row's last one.
+    auto load = [&](uint32_t stage, uint32_t i) {
+        const int32_t over = (int32_t)(piece16 ^ (i & 1u) * 64u) - (int32_t)(p.k - 16u - kb * 128u);
+        const uint32_t back = over > 0 ? (uint32_t)over : 0u;
+        const uint32_t at = to + stage * kStepBytes + i * 1024u;
+        to_lds(a, offm[i] - back, at);
+        to_lds(b, offn[i] - back, at + 2 * kStepBytes);
+    };
+    // Their scales (multiplied later: here that would wait for the loads
+    // before), then on to the next block; after the last one the loads repeat.
+    auto load_scales = [&](float (&s)[3]) {
 #pragma unroll
         for (uint32_t j = 0; j < 2; ++j)
             s[j] = sa[m[j]];
         s[2] = sb[sb_off];
-        a += 128;
-        b += 128;
-        sa += p.rows;
-        sb += 1;
+        if (kb + 1u < p.kblocks) {
+            ++kb;
+            a += 128;
+            b += 128;
+            sa += p.rows;
+            sb += 1;
+        } else if (r + 1u < nranks) {
+            kb = 0;
+            ++r;
+            at_rank();
+        }
     };
 
     f32x16 acc[4][2] = {};
-    uint32_t r = 0, kb = 0;
-    float s[2], s_next[3];
-    at_rank(0);
-    load(0, 0, s_next);
-    for (uint32_t step = 0; step < steps; ++step) {
-        const uint32_t stage = step & 1u;
+    float s_next[3];
+    at_rank();
+#pragma unroll
+    for (uint32_t i = 0; i < 4; ++i)
+        load(0, i);
+    load_scales(s_next);
+
+    // One step: multiplies half `stage`, loads the other one.  `left`: bytes of
+    // the block that are in the row; those past it (TAIL) are zero in the
+    // weights, and in the activations a repeat of the row's own, so that a NaN
+    // there is one that the row has anyway.
+    auto step = [&](uint32_t stage, auto tail, uint32_t left) {
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         // After this every wave's loads of this step are in LDS, and no wave
         // reads the other half any more.
         __syncthreads();
-        s[0] = s_next[0] * s_next[2];
-        s[1] = s_next[1] * s_next[2];
+        float s[2] = {s_next[0] * s_next[2], s_next[1] * s_next[2]};
         // (here, where they are at hand: a wait for them further down would
         // also wait for the next step's loads)
         asm volatile("" : "+v"(s[0]), "+v"(s[1]));
         const char *pm = lds + stage * kStepBytes + wm * 128u;
         const char *pn = lds + (2u + stage) * kStepBytes + wn * 128u;
+        auto weights = [&](uint32_t i, uint32_t h) {
+            i32x8 w = pieces(pn + i * 4096u, place ^ (h * 64u));
+            if constexpr (decltype(tail)::value) {
+#pragma unroll
+                for (uint32_t e = 0; e < 8; ++e)
+                    w[e] = (h * 4u + half * 2u + e / 4u) * 16u < left ? w[e] : 0;
+            }
+            return w;
+        };
         i32x8 x[2][2], w[2];
 #pragma unroll
         for (uint32_t h = 0; h < 2; ++h) {
             x[0][h] = pieces(pm, place ^ (h * 64u));
-            w[h] = pieces(pn, place ^ (h * 64u));
+            w[h] = weights(0, h);
         }
 #pragma unroll
         for (uint32_t h = 0; h < 2; ++h)
             x[1][h] = pieces(pm + 4096u, place ^ (h * 64u));
         __builtin_amdgcn_sched_barrier(0);
-        if (step + 1u < steps) {
-            if (++kb == p.kblocks) {
-                kb = 0;
-                at_rank(++r);
-            }
-            load(kb, stage ^ 1u, s_next);
-        }
         // A tile's products are under way while the one before it is scaled.
+        // The next step's loads go out between the products: all of them at
+        // once would hold the first product back.
         f32x16 c[2];
 #pragma unroll
         for (uint32_t i = 0; i < 4; ++i) {
             if (i > 0) {
 #pragma unroll
                 for (uint32_t h = 0; h < 2; ++h)
-                    w[h] = pieces(pn + i * 4096u, place ^ (h * 64u));
+                    w[h] = weights(i, h);
             }
 #pragma unroll
             for (uint32_t j = 0; j < 2; ++j) {
@@ -195,14 +191,31 @@ __global__ __launch_bounds__(512, 2) void matmul_tile(MatmulArgs p)
 #pragma unroll
                     for (uint32_t e = 0; e < 16; ++e)
                         acc[pi][pj][e] = __builtin_fmaf(c[pj][e], s[pj], acc[pi][pj][e]);
+                    // (done here: put off, it keeps every tile's registers)
+                    asm volatile("" : "+v"(acc[pi][pj]));
                 }
+                if (i < 2)
+                    load(stage ^ 1u, i * 2u + j);
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
+        load_scales(s_next);
 #pragma unroll
         for (uint32_t e = 0; e < 16; ++e)
             acc[3][1][e] = __builtin_fmaf(c[1][e], s[1], acc[3][1][e]);
+        asm volatile("" : "+v"(acc[3][1]));
+    };
+    uint32_t stage = 0;
+    const uint32_t full = p.k / 128u;
+    for (uint32_t q = 0; q < nranks; ++q) {
+        for (uint32_t i = 0; i < full; ++i, stage ^= 1u)
+            step(stage, std::false_type{}, 128u);
+        if (full != p.kblocks) {
+            step(stage, std::true_type{}, p.k % 128u);
+            stage ^= 1u;
+        }
     }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 
     // The sums go through LDS, 32 rows x 128 columns of a wave at a time, so
     // that a store covers whole lines: 16-byte pieces, piece c of row r at
