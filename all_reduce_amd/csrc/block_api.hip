@@ -250,13 +250,15 @@ arResult_t arMatmulScaled(const void *const *abufs, const float *const *ascales,
         return reject(arUnsupported, "nranks must be in 1..32");
     if (k < 16 || k % 16 != 0)
         return reject(arUnsupported, "k must be a positive multiple of 16");
+    if (k > ar::kMatmulMaxK)
+        return reject(arUnsupported, "k must be at most 2^23");
     if (reduce != 0 && reduce != 1)
         return reject(arInvalidArgument, "reduce must be 0 or 1");
     if (rows == 0 || n == 0)
         return arSuccess;
     const size_t most = (size_t)1 << 30;
-    if (rows > most || n > most || k > most)
-        return reject(arInvalidArgument, "rows, n and k must be at most 2^30");
+    if (rows > most || n > most)
+        return reject(arInvalidArgument, "rows and n must be at most 2^30");
     if (rows * n > ((size_t)1 << 40))
         return reject(arInvalidArgument, "rows * n must be at most 2^40");
     Ranges mem;

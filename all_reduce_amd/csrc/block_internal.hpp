@@ -54,10 +54,14 @@ hipError_t launch_gate(const GateArgs &args, int dtype, int act, int nranks, int
                        hipStream_t stream);
 hipError_t launch_matmul(const MatmulArgs &args, int out_dtype, bool reduce, int cu_count,
                          hipStream_t stream);
-// Its kernel for many rows (block_matmul_tile.hip), whose 32-bit offsets
-// inside a tile of 256 rows limit k.
-constexpr uint32_t kTileMaxK = 1u << 23;
-hipError_t launch_matmul_tile(const MatmulArgs &args, int out_dtype, bool reduce,
+// Its kernels for a batch of rows (block_matmul_mid.hip; mt, nt: tiles of 32
+// rows and columns, 1 and 1, 2 and 1 or 2 and 2) and for many
+// (block_matmul_tile.hip; tiles of 256 x 256 or 128 x 128).  Their 32-bit
+// offsets inside a tile limit k.
+constexpr uint32_t kMatmulMaxK = 1u << 23;
+hipError_t launch_matmul_mid(const MatmulArgs &args, int out_dtype, bool reduce, int mt, int nt,
+                             uint32_t waves, hipStream_t stream);
+hipError_t launch_matmul_tile(const MatmulArgs &args, int out_dtype, bool reduce, bool large,
                               hipStream_t stream);
 
 }  // namespace ar

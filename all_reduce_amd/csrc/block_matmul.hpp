@@ -87,6 +87,46 @@ __device__ inline i32x8 pieces(const char *base, uint32_t at)
     return r;
 }
 
+// 16 bytes a lane from base + off to LDS at `to` + 16 * lane (`base` and `to`
+// are the same in every lane).  The compiler does not see the load: whoever
+// reads the bytes waits for vmcnt(0) first.
+__device__ inline void to_lds(const char *base, uint32_t off, uint32_t to)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                 :
+                 : "s"(to), "v"(off), "s"(base)
+                 : "memory");
+}
+
+// Four bytes a lane from an address of its own to LDS at `to` + 4 * lane.
+__device__ inline void to_lds4(const char *at, uint32_t to)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off"
+                 :
+                 : "s"(to), "v"(at)
+                 : "memory");
+}
+
+// Four consecutive columns of a row, those below `n`.
+template <typename T>
+__device__ inline void store4(char *out, uint64_t row, uint32_t n, uint32_t col, f32x4 c)
+{
+    const uint64_t at = row * n + col;
+    float f[4] = {c[0], c[1], c[2], c[3]};
+    uint32_t w[2 * T::kBytes / 2];
+#pragma unroll
+    for (int i = 0; i < 4 / T::kPerWord; ++i)
+        w[i] = T::narrow(f + i * T::kPerWord);
+    if (col + 4u <= n) {
+        __builtin_memcpy(out + at * T::kBytes, w, 4 * T::kBytes);
+    } else {
+#pragma unroll
+        for (uint32_t i = 0; i < 4; ++i)
+            if (col + i < n)
+                __builtin_memcpy(out + (at + i) * T::kBytes, (const char *)w + i * T::kBytes, T::kBytes);
+    }
+}
+
 // 16 bytes of an output row with `left` elements to its end.
 template <typename T>
 __device__ inline void store_piece(char *p, u32x4 v, uint32_t left)

@@ -1,13 +1,14 @@
 // block_matmul_tile.hip -- the block-scaled 8-bit product for many rows.
 //
-// A workgroup of eight waves computes 256 rows x 256 output columns; a step
-// is one block of 128 of k (of all ranks' k, one rank after the other, in the
-// form that sums over the ranks).  A step's 64 KiB of inputs go from global
-// memory straight to LDS (no registers in between), two steps' worth in
-// turn, so that one is loaded while the other is multiplied.  A wave computes
-// 64 rows x 128 columns in 32x32 tiles: the columns of a wave lie in one
-// weight scale block, so a step's scale is one number a lane and row tile,
-// applied with a fused multiply-add to the running sums.
+// A workgroup computes a tile of 256 rows x 256 output columns with eight
+// waves, or 128 x 128 with four where there would be too few of the larger
+// ones; a step is one block of 128 of k (of all ranks' k, one rank after the
+// other, in the form that sums over the ranks).  A step's inputs go from
+// global memory straight to LDS (no registers in between), two steps' worth
+// in turn, so that one is loaded while the other is multiplied.  A wave
+// computes 64 rows x 128 (64) columns in 32x32 tiles: the columns of a wave
+// lie in one weight scale block, so a step's scale is one number a lane and
+// row tile, applied with a fused multiply-add to the running sums.
 //
 // LDS rows are the 128 bytes of a step, in eight pieces of 16; piece c of row
 // r is kept at place c ^ (r / 2 % 8).  Two rows cover all banks once, so 16
@@ -23,32 +24,29 @@
 
 namespace ar {
 
-constexpr uint32_t kTile = 256;                 // rows, and columns, of a workgroup
-constexpr uint32_t kStepBytes = kTile * 128u;   // of one operand
+// NT: 32-column tiles of a wave (it has two 32-row ones).  WM, WN: waves along
+// rows and columns.
+template <int NT, int WM, int WN>
+struct TileShape {
+    static constexpr uint32_t kRows = WM * 64u, kCols = WN * NT * 32u, kWaves = WM * WN;
+    static constexpr uint32_t kRowBytes = kRows * 128u, kColBytes = kCols * 128u;  // of a step
+    static constexpr uint32_t kLoadsM = kRows / 8u / kWaves, kLoadsN = kCols / 8u / kWaves;
+};
 
-// 16 bytes a lane from base + off to LDS at `to` + 16 * lane (`base` and `to`
-// are the same in every lane).  The compiler does not see the load: whoever
-// reads the bytes waits for vmcnt(0) first.
-__device__ inline void to_lds(const char *base, uint32_t off, uint32_t to)
-{
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
-                 :
-                 : "s"(to), "v"(off), "s"(base)
-                 : "memory");
-}
-
-template <typename T, bool REDUCE>
-__global__ __launch_bounds__(512, 2) void matmul_tile(MatmulArgs p)
+template <typename T, int NT, int WM, int WN, bool REDUCE>
+__global__ __launch_bounds__(WM * WN * 64, 2) void matmul_tile(MatmulArgs p)
 {
     constexpr bool kExact = T::kBytes == 4;
-    __shared__ __align__(128) char lds[4 * kStepBytes];  // rows, rows, columns, columns
+    typedef TileShape<NT, WM, WN> S;
+    // rows of both steps, then columns of both
+    __shared__ __align__(128) char lds[2 * (S::kRowBytes + S::kColBytes)];
     const uint32_t lane = threadIdx.x & 63u;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 
     // Workgroup w runs on XCD w % 8: each XCD takes consecutive tiles, and 32
     // consecutive tiles are 8 x 4, which its second-level cache serves with 12
     // tiles' inputs instead of 64.
-    const uint32_t mt = (p.rows + kTile - 1) / kTile, nt = (p.n + kTile - 1) / kTile;
+    const uint32_t mt = (p.rows + S::kRows - 1) / S::kRows, nt = (p.n + S::kCols - 1) / S::kCols;
     const uint32_t tiles = mt * nt * (REDUCE ? 1u : p.nranks);
     uint32_t t = (blockIdx.x & 7u) * ((tiles + 7u) / 8u) + blockIdx.x / 8u;
     if (blockIdx.x / 8u >= (tiles + 7u) / 8u || t >= tiles)
@@ -58,23 +56,30 @@ __global__ __launch_bounds__(512, 2) void matmul_tile(MatmulArgs p)
     const uint32_t band = t / (mt * 4u);                      // four columns of tiles
     const uint32_t wide = nt - band * 4u < 4u ? nt - band * 4u : 4u;
     t -= band * mt * 4u;
-    const uint32_t m0 = t / wide * kTile, n0 = (band * 4u + t % wide) * kTile;
+    const uint32_t m0 = t / wide * S::kRows, n0 = (band * 4u + t % wide) * S::kCols;
 
-    // This wave loads 32 rows and 32 columns, eight at a time; rows past the
-    // end repeat the last one, and what comes of them is not stored.
-    uint32_t offm[4], offn[4];
+    // This wave loads rows and columns eight at a time; rows past the end
+    // repeat the last one, and what comes of them is not stored.
+    uint32_t offm[S::kLoadsM], offn[S::kLoadsN];
     const uint32_t piece16 = ((lane & 7u) ^ (lane >> 4)) * 16u;  // even groups of eight; odd ^ 64
 #pragma unroll
-    for (uint32_t i = 0; i < 4; ++i) {
-        const uint32_t r = wave * 32u + i * 8u + (lane >> 3);
+    for (uint32_t i = 0; i < S::kLoadsM; ++i) {
+        const uint32_t r = (wave * S::kLoadsM + i) * 8u + (lane >> 3);
         offm[i] = (r < p.rows - m0 ? r : p.rows - m0 - 1u) * p.k + (piece16 ^ (i & 1u) * 64u);
+    }
+#pragma unroll
+    for (uint32_t i = 0; i < S::kLoadsN; ++i) {
+        const uint32_t r = (wave * S::kLoadsN + i) * 8u + (lane >> 3);
         offn[i] = (r < p.n - n0 ? r : p.n - n0 - 1u) * p.k + (piece16 ^ (i & 1u) * 64u);
     }
-    const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)lds;
-    const uint32_t to = __builtin_amdgcn_readfirstlane(lds0) + wave * 4096u;
+    static_assert(S::kLoadsM % 2 == 0 && S::kLoadsN % 2 == 0, "odd groups start on odd i");
+    const uint32_t lds0 =
+        __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)lds);
+    const uint32_t tom = lds0 + wave * S::kLoadsM * 1024u;
+    const uint32_t ton = lds0 + 2u * S::kRowBytes + wave * S::kLoadsN * 1024u;
 
-    // This wave multiplies rows wm .. wm + 63 and columns wn .. wn + 127.
-    const uint32_t wm = (wave & 3u) * 64u, wn = (wave >> 2) * 128u;
+    // This wave multiplies rows wm .. wm + 63 and columns wn .. wn + 32 NT - 1.
+    const uint32_t wm = wave % WM * 64u, wn = wave / WM * (NT * 32u);
     const uint32_t l32 = lane & 31u, half = lane >> 5;
     const uint32_t place = l32 * 128u + ((half * 2u) ^ (l32 >> 1 & 7u)) * 16u;
     uint32_t m[2];
@@ -100,15 +105,17 @@ __global__ __launch_bounds__(512, 2) void matmul_tile(MatmulArgs p)
         sa = p.sa[rank0 + r];
         sb = p.sb[rank0 + r];
     };
-    // Eight rows and eight columns of them into half `stage` of LDS.  A piece
-    // past the end of its row repeats the row's last one.
+    // Part `i` of its loads into half `stage` of LDS: eight rows and eight
+    // columns.  A piece past the end of its row repeats the row's last one.
     auto load = [&](uint32_t stage, uint32_t i) {
         const int32_t over = (int32_t)(piece16 ^ (i & 1u) * 64u) - (int32_t)(p.k - 16u - kb * 128u);
         const uint32_t back = over > 0 ? (uint32_t)over : 0u;
-        const uint32_t at = to + stage * kStepBytes + i * 1024u;
-        to_lds(a, offm[i] - back, at);
-        to_lds(b, offn[i] - back, at + 2 * kStepBytes);
+        if (i < S::kLoadsM)
+            to_lds(a, offm[i] - back, tom + stage * S::kRowBytes + i * 1024u);
+        if (i < S::kLoadsN)
+            to_lds(b, offn[i] - back, ton + stage * S::kColBytes + i * 1024u);
     };
+    constexpr uint32_t kParts = S::kLoadsM > S::kLoadsN ? S::kLoadsM : S::kLoadsN;
     // Their scales (multiplied later: here that would wait for the loads
     // before), then on to the next block; after the last one the loads repeat.
     auto load_scales = [&](float (&s)[3]) {
@@ -129,11 +136,11 @@ __global__ __launch_bounds__(512, 2) void matmul_tile(MatmulArgs p)
         }
     };
 
-    f32x16 acc[4][2] = {};
+    f32x16 acc[NT][2] = {};
     float s_next[3];
     at_rank();
 #pragma unroll
-    for (uint32_t i = 0; i < 4; ++i)
+    for (uint32_t i = 0; i < kParts; ++i)
         load(0, i);
     load_scales(s_next);
 
@@ -150,8 +157,8 @@ __global__ __launch_bounds__(512, 2) void matmul_tile(MatmulArgs p)
         // (here, where they are at hand: a wait for them further down would
         // also wait for the next step's loads)
         asm volatile("" : "+v"(s[0]), "+v"(s[1]));
-        const char *pm = lds + stage * kStepBytes + wm * 128u;
-        const char *pn = lds + (2u + stage) * kStepBytes + wn * 128u;
+        const char *pm = lds + stage * S::kRowBytes + wm * 128u;
+        const char *pn = lds + 2u * S::kRowBytes + stage * S::kColBytes + wn * 128u;
         auto weights = [&](uint32_t i, uint32_t h) {
             i32x8 w = pieces(pn + i * 4096u, place ^ (h * 64u));
             if constexpr (decltype(tail)::value) {
@@ -176,7 +183,7 @@ __global__ __launch_bounds__(512, 2) void matmul_tile(MatmulArgs p)
         // once would hold the first product back.
         f32x16 c[2];
 #pragma unroll
-        for (uint32_t i = 0; i < 4; ++i) {
+        for (uint32_t i = 0; i < NT; ++i) {
             if (i > 0) {
 #pragma unroll
                 for (uint32_t h = 0; h < 2; ++h)
@@ -194,7 +201,7 @@ __global__ __launch_bounds__(512, 2) void matmul_tile(MatmulArgs p)
                     // (done here: put off, it keeps every tile's registers)
                     asm volatile("" : "+v"(acc[pi][pj]));
                 }
-                if (i < 2)
+                if (i * 2u + j < kParts)
                     load(stage ^ 1u, i * 2u + j);
                 __builtin_amdgcn_sched_barrier(0);
             }
@@ -202,8 +209,8 @@ __global__ __launch_bounds__(512, 2) void matmul_tile(MatmulArgs p)
         load_scales(s_next);
 #pragma unroll
         for (uint32_t e = 0; e < 16; ++e)
-            acc[3][1][e] = __builtin_fmaf(c[1][e], s[1], acc[3][1][e]);
-        asm volatile("" : "+v"(acc[3][1]));
+            acc[NT - 1][1][e] = __builtin_fmaf(c[1][e], s[1], acc[NT - 1][1][e]);
+        asm volatile("" : "+v"(acc[NT - 1][1]));
     };
     uint32_t stage = 0;
     const uint32_t full = p.k / 128u;
@@ -217,16 +224,17 @@ __global__ __launch_bounds__(512, 2) void matmul_tile(MatmulArgs p)
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 
-    // The sums go through LDS, 32 rows x 128 columns of a wave at a time, so
+    // The sums go through LDS, 32 rows x 32 NT columns of a wave at a time, so
     // that a store covers whole lines: 16-byte pieces, piece c of row r at
-    // place c ^ (r % 16) (of 16 pieces for 16-bit outputs, 32 for binary32).
+    // place c ^ (r % 8).
     __syncthreads();
-    constexpr uint32_t kRow = 128u * T::kBytes;
+    constexpr uint32_t kRow = NT * 32u * T::kBytes;
+    static_assert(S::kWaves * 32u * kRow <= sizeof(lds), "the waves' parts fit");
     char *mine = lds + wave * (32u * kRow);
 #pragma unroll
     for (uint32_t j = 0; j < 2; ++j) {
 #pragma unroll
-        for (uint32_t i = 0; i < 4; ++i) {
+        for (uint32_t i = 0; i < NT; ++i) {
 #pragma unroll
             for (uint32_t q = 0; q < 4; ++q) {
                 const uint32_t col = i * 32u + q * 8u + half * 4u;
@@ -239,8 +247,8 @@ __global__ __launch_bounds__(512, 2) void matmul_tile(MatmulArgs p)
                 for (uint32_t e = 0; e < 4 / T::kPerWord; ++e)
                     v[e] = T::narrow(f + e * T::kPerWord);
                 const uint32_t at = col * T::kBytes;
-                char *to16 = mine + l32 * kRow + (((at >> 4) ^ (l32 & 15u)) << 4) + (at & 15u);
-                __builtin_memcpy(__builtin_assume_aligned(to16, 2 * T::kBytes * 2), v, 4 * T::kBytes);
+                char *to = mine + l32 * kRow + (((at >> 4) ^ (l32 & 7u)) << 4) + (at & 15u);
+                __builtin_memcpy(__builtin_assume_aligned(to, 4 * T::kBytes), v, 4 * T::kBytes);
             }
         }
         // (a wave's own LDS accesses are in order, and no other wave's are here)
@@ -250,7 +258,7 @@ __global__ __launch_bounds__(512, 2) void matmul_tile(MatmulArgs p)
         for (uint32_t u = 0; u < 32u * kPieces / 64u; ++u) {
             const uint32_t row = u * (64u / kPieces) + lane / kPieces;
             const uint32_t c = lane % kPieces;
-            const u32x4 v = *(const u32x4 *)(mine + row * kRow + ((c ^ (row & 15u)) << 4));
+            const u32x4 v = *(const u32x4 *)(mine + row * kRow + ((c ^ (row & 7u)) << 4));
             const uint32_t gm = m0 + wm + j * 32u + row, gn = n0 + wn + c * kEach;
             if (gm < p.rows && gn < p.n) {
                 const uint64_t at = ((uint64_t)gm * p.n + gn) * T::kBytes;
@@ -268,28 +276,40 @@ __global__ __launch_bounds__(512, 2) void matmul_tile(MatmulArgs p)
 
 namespace {
 
-template <typename T>
-hipError_t enqueue(const MatmulArgs &args, bool reduce, hipStream_t stream)
+template <typename T, int NT, int WM, int WN>
+hipError_t enqueue_tile(const MatmulArgs &args, bool reduce, hipStream_t stream)
 {
-    const uint32_t tiles = (args.rows + kTile - 1) / kTile * ((args.n + kTile - 1) / kTile) *
-                           (reduce ? 1u : args.nranks);
+    typedef TileShape<NT, WM, WN> S;
+    const uint32_t tiles = (args.rows + S::kRows - 1) / S::kRows *
+                           ((args.n + S::kCols - 1) / S::kCols) * (reduce ? 1u : args.nranks);
     const dim3 grid((tiles + 7u) / 8u * 8u);
     if (reduce)
-        hipLaunchKernelGGL((matmul_tile<T, true>), grid, dim3(512), 0, stream, args);
+        hipLaunchKernelGGL((matmul_tile<T, NT, WM, WN, true>), grid, dim3(S::kWaves * 64), 0, stream,
+                           args);
     else
-        hipLaunchKernelGGL((matmul_tile<T, false>), grid, dim3(512), 0, stream, args);
+        hipLaunchKernelGGL((matmul_tile<T, NT, WM, WN, false>), grid, dim3(S::kWaves * 64), 0, stream,
+                           args);
     return hipGetLastError();
+}
+
+template <typename T>
+hipError_t pick_tile(const MatmulArgs &args, bool reduce, bool large, hipStream_t stream)
+{
+    if constexpr (T::kBytes == 2)
+        if (large)
+            return enqueue_tile<T, 4, 4, 2>(args, reduce, stream);
+    return enqueue_tile<T, 2, 2, 2>(args, reduce, stream);
 }
 
 }  // namespace
 
-hipError_t launch_matmul_tile(const MatmulArgs &args, int out_dtype, bool reduce,
+hipError_t launch_matmul_tile(const MatmulArgs &args, int out_dtype, bool reduce, bool large,
                               hipStream_t stream)
 {
     switch (out_dtype) {
-    case kBf16: return enqueue<Bf16>(args, reduce, stream);
-    case kFp16: return enqueue<Fp16>(args, reduce, stream);
-    default: return enqueue<Fp32>(args, reduce, stream);
+    case kBf16: return pick_tile<Bf16>(args, reduce, large, stream);
+    case kFp16: return pick_tile<Fp16>(args, reduce, large, stream);
+    default: return pick_tile<Fp32>(args, reduce, large, stream);
     }
 }
 

@@ -126,10 +126,10 @@ arResult_t arGateQuant(const void *const *inbufs, void *const *outbufs, float *c
  *  bbufs, bscales  host arrays of nranks device pointers: weights [n, k] of
  *                  8-bit values, dense, and [ceil(n / 128)][ceil(k / 128)].
  *  outbufs         host array of nranks device pointers, [rows, n] of outDtype.
- *  k               a multiple of 16, at least 16 (else arUnsupported).
+ *  k               a multiple of 16 in 16 .. 2^23 (else arUnsupported).
  *  outDtype        arBfloat16, arFloat16 or arFloat32 (else arUnsupported).
  * Rules (arInvalidArgument when broken): no NULL pointer; every pointer
- * 16-byte aligned; rows, n and k at most 2^30 and rows * n at most 2^40; no
+ * 16-byte aligned; rows and n at most 2^30 and rows * n at most 2^40; no
  * written range overlaps another written or read one (inputs may be shared
  * between ranks). */
 arResult_t arMatmulScaled(const void *const *abufs, const float *const *ascales,
