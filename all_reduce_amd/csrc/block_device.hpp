@@ -1,112 +1,104 @@
 // block_device.hpp -- device-side building blocks of the operators of
-// ar_block.h: groups of eight elements, sums and maxima across lanes, 8-bit
+// ar_block.h: 16-byte pieces of a row, sums and maxima across lanes, 8-bit
 // values.
 //
-// A lane works on groups of eight consecutive columns: one 16-byte access for
-// the 16-bit types, two for binary32, 8 bytes of 8-bit values; the 128
-// columns that share a scale are the groups of 16 neighbouring lanes (one row
-// of the lane network).  A row may start at any element, so the vector types
-// carry the element's alignment; gfx950 serves such accesses with the same
-// instructions as aligned ones.
+// A lane works on pieces of 16 bytes: eight consecutive columns of a 16-bit
+// type, four of binary32, so that neighbouring lanes always cover whole lines
+// (two pieces a lane for binary32 leave gaps: 16 ranks of 1024 x 7168 took
+// 311 us that way and take 211 us this way).  The 128 columns that share a
+// scale are the pieces of 16 or 32 neighbouring lanes.  A row may start at
+// any element, so the vector types carry the element's alignment; gfx950
+// serves such accesses with the same instructions as aligned ones.
 #pragma once
 
+#include "ar_allreduce.h"
 #include "ar_device.hpp"
 
 namespace ar {
 
 typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(1)));
+typedef uint32_t u32_any __attribute__((aligned(1)));
 
 constexpr float kEightMax = 448.0f;        // largest e4m3 value
 constexpr float kScaleMin = 0x1p-126f;     // smallest scale: its reciprocal is finite
 
-// Eight elements as they lie in memory.
-template <typename T>
-struct Raw8 {
-    static constexpr int kVecs = T::kBytes / 2;  // 16-byte vectors
-    u32x4 v[kVecs];
-};
-
-template <typename T, bool NT>
-__device__ inline Raw8<T> load8(const char *p)
+// Brings a rank table's first eight entries into the scalar cache.
+template <typename P>
+__device__ inline void touch(P *const (&table)[AR_MAX_RANKS])
 {
-    Raw8<T> r;
-#pragma unroll
-    for (int i = 0; i < Raw8<T>::kVecs; ++i) {
-        const u32x4_any *q = (const u32x4_any *)p + i;
-        if constexpr (NT)
-            r.v[i] = __builtin_nontemporal_load(q);
-        else
-            r.v[i] = *q;
-    }
-    return r;
+    asm volatile("" : : "s"(table[0]));
 }
 
-template <typename T, bool NT>
-__device__ inline void store8(char *p, const Raw8<T> &r)
+// Elements of a 16-byte piece.
+template <typename T>
+constexpr int kPiece = 16 / T::kBytes;
+
+template <bool NT>
+__device__ inline u32x4 load_piece(const char *p)
 {
-#pragma unroll
-    for (int i = 0; i < Raw8<T>::kVecs; ++i) {
-        u32x4_any *q = (u32x4_any *)p + i;
-        if constexpr (NT)
-            __builtin_nontemporal_store((u32x4_any)r.v[i], q);
-        else
-            *q = r.v[i];
-    }
+    if constexpr (NT)
+        return __builtin_nontemporal_load((const u32x4_any *)p);
+    else
+        return *(const u32x4_any *)p;
 }
 
-// The first `n` (1..7) of eight elements; the others read as zero.
-template <typename T>
-__device__ inline Raw8<T> load_some(const char *p, uint32_t n)
+template <bool NT>
+__device__ inline void store_piece(char *p, u32x4 v)
 {
-    uint32_t w[T::kBytes * 2] = {};
+    if constexpr (NT)
+        __builtin_nontemporal_store((u32x4_any)v, (u32x4_any *)p);
+    else
+        *(u32x4_any *)p = v;
+}
+
+// The first `n` (less than a piece's) elements; the others read as zero.
+template <typename T>
+__device__ inline u32x4 load_some(const char *p, uint32_t n)
+{
+    u32x4 r = {0, 0, 0, 0};
 #pragma unroll
-    for (uint32_t i = 0; i < 8; ++i) {
+    for (uint32_t i = 0; i < (uint32_t)kPiece<T>; ++i) {
         if (i < n) {
             if constexpr (T::kBytes == 2)
-                w[i / 2] |= (uint32_t)((const uint16_t *)p)[i] << (16 * (i % 2));
+                r[i / 2] |= (uint32_t)((const uint16_t *)p)[i] << (16 * (i % 2));
             else
-                w[i] = ((const uint32_t *)p)[i];
+                r[i] = ((const uint32_t *)p)[i];
         }
     }
-    Raw8<T> r;
-#pragma unroll
-    for (int i = 0; i < Raw8<T>::kVecs; ++i)
-        r.v[i] = u32x4{w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]};
     return r;
 }
 
 template <typename T>
-__device__ inline void store_some(char *p, const Raw8<T> &r, uint32_t n)
+__device__ inline void store_some(char *p, u32x4 v, uint32_t n)
 {
 #pragma unroll
-    for (uint32_t i = 0; i < 8; ++i) {
+    for (uint32_t i = 0; i < (uint32_t)kPiece<T>; ++i) {
         if (i < n) {
             if constexpr (T::kBytes == 2)
-                ((uint16_t *)p)[i] = (uint16_t)(r.v[0][i / 2] >> (16 * (i % 2)));
+                ((uint16_t *)p)[i] = (uint16_t)(v[i / 2] >> (16 * (i % 2)));
             else
-                ((uint32_t *)p)[i] = r.v[i / 4][i % 4];
+                ((uint32_t *)p)[i] = v[i];
         }
     }
 }
 
 template <typename T>
-__device__ inline void widen8(const Raw8<T> &r, float (&f)[8])
+__device__ inline void widen_piece(u32x4 v, float (&f)[kPiece<T>])
 {
 #pragma unroll
-    for (int i = 0; i < 8 / T::kPerWord; ++i)
-        T::widen(r.v[i / 4][i % 4], f + i * T::kPerWord);
+    for (int i = 0; i < 4; ++i)
+        T::widen(v[i], f + i * T::kPerWord);
 }
 
 template <typename T>
-__device__ inline Raw8<T> narrow8(const float (&f)[8])
+__device__ inline u32x4 narrow_piece(const float (&f)[kPiece<T>])
 {
-    Raw8<T> r;
+    u32x4 v;
 #pragma unroll
-    for (int i = 0; i < 8 / T::kPerWord; ++i)
-        r.v[i / 4][i % 4] = T::narrow(f + i * T::kPerWord);
-    return r;
+    for (int i = 0; i < 4; ++i)
+        v[i] = T::narrow(f + i * T::kPerWord);
+    return v;
 }
 
 template <int CTRL>
@@ -129,6 +121,19 @@ __device__ inline uint32_t max16(uint32_t x)
     return x > y ? x : y;
 }
 
+// The largest of the lanes that hold the 128 columns of a scale, in each of
+// them: 16 lanes, or 32 where a piece has four columns.
+template <typename T>
+__device__ inline uint32_t max_block(uint32_t x)
+{
+    x = max16(x);
+    if constexpr (kPiece<T> == 4) {
+        const uint32_t y = (uint32_t)__shfl_xor((int)x, 16);
+        x = x > y ? x : y;
+    }
+    return x;
+}
+
 // The sum over a wave, in every lane, in a fixed order.
 __device__ inline float sum64(float x)
 {
@@ -143,11 +148,12 @@ __device__ inline float sum64(float x)
 
 // Magnitude bits order like the magnitudes, with infinity above every finite
 // value and NaN above infinity, so a maximum over them keeps a NaN.
-__device__ inline uint32_t max_bits8(const float (&y)[8])
+template <int N>
+__device__ inline uint32_t max_bits(const float (&y)[N])
 {
     uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < N; ++i) {
         const uint32_t b = __builtin_bit_cast(uint32_t, y[i]) & 0x7fffffffu;
         m = m > b ? m : b;
     }
@@ -161,38 +167,54 @@ __device__ inline float scale_of(uint32_t m)
     return s < kScaleMin ? kScaleMin : s;  // keeps NaN
 }
 
-// Eight e4m3 values of y * inv, rounded to nearest even.  |y| * inv is at most
-// 448 but for a few units in the last place, which round back to 448, so the
-// conversion's overflow is never reached.  The reciprocal in place of a
-// division moves a value by 2^-23 of itself before a rounding of 2^-4.
-__device__ inline u32x2 eight_of(const float (&y)[8], float inv)
+// The e4m3 values of y * inv, rounded to nearest even, four to a word.
+// |y| * inv is at most 448 but for a few units in the last place, which round
+// back to 448, so the conversion's overflow is never reached.  The reciprocal
+// in place of a division moves a value by 2^-23 of itself before a rounding
+// of 2^-4.
+template <int N>
+struct Eights {
+    uint32_t w[N / 4];
+};
+
+template <int N>
+__device__ inline Eights<N> to_eights(const float (&y)[N], float inv)
 {
-    u32x2 q;
+    Eights<N> q;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < N / 4; ++i) {
         int w = 0;
         w = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * i] * inv, y[4 * i + 1] * inv, w, false);
         w = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * i + 2] * inv, y[4 * i + 3] * inv, w, true);
-        q[i] = (uint32_t)w;
+        q.w[i] = (uint32_t)w;
     }
     return q;
 }
 
-template <bool NT>
-__device__ inline void store_eight(char *p, u32x2 q)
+template <bool NT, int N>
+__device__ inline void store_eights(char *p, const Eights<N> &q)
 {
-    if constexpr (NT)
-        __builtin_nontemporal_store((u32x2_any)q, (u32x2_any *)p);
-    else
-        *(u32x2_any *)p = q;
+    if constexpr (N == 8) {
+        const u32x2_any v = {q.w[0], q.w[1]};
+        if constexpr (NT)
+            __builtin_nontemporal_store(v, (u32x2_any *)p);
+        else
+            *(u32x2_any *)p = v;
+    } else {
+        if constexpr (NT)
+            __builtin_nontemporal_store(q.w[0], (u32_any *)p);
+        else
+            *(u32_any *)p = q.w[0];
+    }
 }
 
-__device__ inline void store_eight_some(char *p, u32x2 q, uint32_t n)
+template <int N>
+__device__ inline void store_eights_some(char *p, const Eights<N> &q, uint32_t n)
 {
 #pragma unroll
-    for (uint32_t i = 0; i < 8; ++i)
+    for (uint32_t i = 0; i < (uint32_t)N; ++i)
         if (i < n)
-            p[i] = (char)(q[i / 4] >> (8 * (i % 4)));
+            p[i] = (char)(q.w[i / 4] >> (8 * (i % 4)));
 }
 
 }  // namespace ar

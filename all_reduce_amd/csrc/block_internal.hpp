@@ -31,6 +31,7 @@ struct GateArgs {
     float *scales[AR_MAX_RANKS];
     uint64_t rows;
     uint64_t cols;
+    uint32_t tall;  // rows a workgroup takes at once (the launcher sets it)
 };
 
 struct MatmulArgs {

@@ -129,22 +129,12 @@ __device__ inline void store4(char *out, uint64_t row, uint32_t n, uint32_t col,
 
 // 16 bytes of an output row with `left` elements to its end.
 template <typename T>
-__device__ inline void store_piece(char *p, u32x4 v, uint32_t left)
+__device__ inline void store_row_piece(char *p, u32x4 v, uint32_t left)
 {
-    constexpr uint32_t kEach = 16u / T::kBytes;
-    if (left >= kEach) {
-        *(u32x4_any *)p = v;
-    } else {
-#pragma unroll
-        for (uint32_t i = 0; i < kEach; ++i) {
-            if (i < left) {
-                if constexpr (T::kBytes == 2)
-                    ((uint16_t *)p)[i] = (uint16_t)(v[i / 2] >> (16 * (i % 2)));
-                else
-                    ((uint32_t *)p)[i] = v[i];
-            }
-        }
-    }
+    if (left >= (uint32_t)kPiece<T>)
+        store_piece<false>(p, v);
+    else
+        store_some<T>(p, v, left);
 }
 
 }  // namespace ar

@@ -264,9 +264,9 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void matmul_tile(MatmulArgs p)
                 const uint64_t at = ((uint64_t)gm * p.n + gn) * T::kBytes;
                 if constexpr (REDUCE) {
                     for (uint32_t o = 0; o < p.nranks; ++o)
-                        store_piece<T>(p.out[o] + at, v, p.n - gn);
+                        store_row_piece<T>(p.out[o] + at, v, p.n - gn);
                 } else {
-                    store_piece<T>(p.out[rank0] + at, v, p.n - gn);
+                    store_row_piece<T>(p.out[rank0] + at, v, p.n - gn);
                 }
             }
         }

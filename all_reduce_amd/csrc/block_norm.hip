@@ -10,90 +10,139 @@
 // (which is what makes the exact in-place forms safe).
 //
 // It is bound by memory: R + 1 reads and 2 R writes a column at two or three
-// operations each.
+// operations each.  On MI355X 8 x 8192 x 8192 bfloat16 with residual takes
+// 650 us (5.2 TB/s; a large copy runs at 5.1), 16 x 1024 x 7168 float32 with
+// an 8-bit output 211 us (5.1 TB/s); one row of 8 x 8192, on one compute unit,
+// 6.0 us and 64 rows 8.4, bound by a row's chain of loads, sum and stores.
 #include "block_device.hpp"
 #include "block_internal.hpp"
 
 namespace ar {
 
-// acc += the values of `COUNT` ranks from rank `r0` on, every load issued
-// before the first addition.
-template <typename T, int COUNT, bool NT>
-__device__ inline void add_ranks(const NormArgs &p, uint32_t r0, uint64_t at, float (&acc)[8])
+// h += the values of `COUNT` ranks from rank `r0` on, in rank order.  Every
+// load is issued before the first addition.
+template <typename T, int V, int COUNT, bool NT>
+__device__ inline void add_ranks(const NormArgs &p, uint32_t r0, uint64_t row_at,
+                                 const uint32_t (&col)[V], float (&h)[V][kPiece<T>])
 {
-    Raw8<T> x[COUNT];
+    u32x4 x[V][COUNT];
 #pragma unroll
-    for (int j = 0; j < COUNT; ++j)
-        x[j] = load8<T, NT>(p.send[r0 + j] + at);
+    for (int v = 0; v < V; ++v)
+        if (col[v] + kPiece<T> <= p.cols)
 #pragma unroll
-    for (int j = 0; j < COUNT; ++j) {
-        float f[8];
-        widen8<T>(x[j], f);
+            for (int j = 0; j < COUNT; ++j)
+                x[v][j] = load_piece<NT>(p.send[r0 + j] + (row_at + col[v]) * T::kBytes);
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            acc[e] = acc[e] + f[e];
-    }
+    for (int v = 0; v < V; ++v)
+        if (col[v] + kPiece<T> <= p.cols)
+#pragma unroll
+            for (int j = 0; j < COUNT; ++j) {
+                float f[kPiece<T>];
+                widen_piece<T>(x[v][j], f);
+#pragma unroll
+                for (int e = 0; e < kPiece<T>; ++e)
+                    h[v][e] = h[v][e] + f[e];
+            }
 }
 
-// V: groups of eight columns a lane holds (lane i holds groups i, i + threads,
-// ..).  EIGHT: 8-bit output with scales.  NT: non-temporal accesses.
+// V: pieces a lane holds (lane i holds pieces i, i + threads, ..).  EIGHT:
+// 8-bit output with scales.  NT: non-temporal accesses.
 template <typename T, int V, bool EIGHT, bool NT>
 __global__ __launch_bounds__(1024) void norm_rows(NormArgs p)
 {
+    constexpr uint32_t E = kPiece<T>;
+    constexpr uint32_t kBatch = 8 / V;  // ranks whose loads are under way at once: 8 pieces a lane
     __shared__ float part[2][16];
     const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
     const uint32_t waves = blockDim.x >> 6;
+    // The tables of where to store are touched here: their first use costs a
+    // trip to memory, one after the other where they are used.
+    touch(p.res_out);
+    touch(p.out);
+    touch(p.scales);
+    uint32_t col[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+        col[v] = (v * blockDim.x + threadIdx.x) * E;
+    auto load_weight = [&](int v) {
+        const char *at = p.weight + (uint64_t)col[v] * T::kBytes;
+        if (col[v] + E <= p.cols)
+            return load_piece<false>(at);
+        return col[v] < p.cols ? load_some<T>(at, p.cols - col[v]) : u32x4{0, 0, 0, 0};
+    };
+    // The weights are loaded here, and a row's residual before its sum, so that
+    // a single row does not wait for them one after the other; a lane with
+    // many pieces has no registers for it.
+    constexpr bool kEarly = V <= 2;
+    u32x4 weight[V];
+    if constexpr (kEarly) {
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            weight[v] = load_weight(v);
+    }
     uint32_t turn = 0;
     for (uint64_t row = blockIdx.x; row < p.rows; row += gridDim.x, turn ^= 1u) {
         const uint64_t row_at = row * p.cols;
-        float h[V][8];
+        float h[V][E];
+        u32x4 res[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            // -0 + x is x for every x: the sum starts from rank 0's value
+#pragma unroll
+            for (uint32_t e = 0; e < E; ++e)
+                h[v][e] = -0.0f;
+            if (kEarly && p.residual != nullptr && col[v] + E <= p.cols)
+                res[v] = load_piece<NT>(p.residual + (row_at + col[v]) * T::kBytes);
+        }
+        uint32_t r = 0;
+        for (; r + kBatch <= p.nranks; r += kBatch)
+            add_ranks<T, V, kBatch, NT>(p, r, row_at, col, h);
+        if constexpr (kBatch > 4) {
+            if (p.nranks & 4u) {
+                add_ranks<T, V, 4, NT>(p, r, row_at, col, h);
+                r += 4u;
+            }
+        }
+        if constexpr (kBatch > 2) {
+            if (p.nranks & 2u) {
+                add_ranks<T, V, 2, NT>(p, r, row_at, col, h);
+                r += 2u;
+            }
+        }
+        if constexpr (kBatch > 1) {
+            if (p.nranks & 1u)
+                add_ranks<T, V, 1, NT>(p, r, row_at, col, h);
+        }
         float sq = 0.0f;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const uint32_t col = (v * blockDim.x + threadIdx.x) * 8u;
-            // -0 + x is x for every x: the sum starts from rank 0's value
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                h[v][e] = -0.0f;
-            if (col + 8u <= p.cols) {
-                const uint64_t at = (row_at + col) * T::kBytes;
-                uint32_t r = 0;
-                for (; r + 8u <= p.nranks; r += 8u)
-                    add_ranks<T, 8, NT>(p, r, at, h[v]);
-                if (p.nranks & 4u) {
-                    add_ranks<T, 4, NT>(p, r, at, h[v]);
-                    r += 4u;
-                }
-                if (p.nranks & 2u) {
-                    add_ranks<T, 2, NT>(p, r, at, h[v]);
-                    r += 2u;
-                }
-                if (p.nranks & 1u)
-                    add_ranks<T, 1, NT>(p, r, at, h[v]);
+            if (col[v] + E <= p.cols) {
                 if (p.residual != nullptr) {
-                    float f[8];
-                    widen8<T>(load8<T, NT>(p.residual + at), f);
+                    float f[E];
+                    if constexpr (!kEarly)
+                        res[v] = load_piece<NT>(p.residual + (row_at + col[v]) * T::kBytes);
+                    widen_piece<T>(res[v], f);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
+                    for (uint32_t e = 0; e < E; ++e)
                         h[v][e] = h[v][e] + f[e];
                 }
-            } else if (col < p.cols) {
-                const uint64_t at = (row_at + col) * T::kBytes;
-                const uint32_t n = p.cols - col;
-                for (uint32_t r = 0; r <= p.nranks; ++r) {
-                    const char *from = r < p.nranks ? p.send[r] : p.residual;
+            } else if (col[v] < p.cols) {
+                // the row's last columns, fewer than a piece
+                for (uint32_t q = 0; q <= p.nranks; ++q) {
+                    const char *from = q < p.nranks ? p.send[q] : p.residual;
                     if (from == nullptr)
                         break;
-                    float f[8];
-                    widen8<T>(load_some<T>(from + at, n), f);
+                    float f[E];
+                    widen_piece<T>(load_some<T>(from + (row_at + col[v]) * T::kBytes, p.cols - col[v]),
+                                   f);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
+                    for (uint32_t e = 0; e < E; ++e)
                         h[v][e] = h[v][e] + f[e];
                 }
             }
             // (columns past the row hold -0 or 0 and add nothing)
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
+            for (uint32_t e = 0; e < E; ++e)
                 sq = __builtin_fmaf(h[v][e], h[v][e], sq);
         }
         sq = sum64(sq);
@@ -108,48 +157,45 @@ __global__ __launch_bounds__(1024) void norm_rows(NormArgs p)
         const float inv = 1.0f / __builtin_sqrtf(total / (float)p.cols + p.eps);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const uint32_t col = (v * blockDim.x + threadIdx.x) * 8u;
-            const bool full = col + 8u <= p.cols;
-            const uint32_t n = col < p.cols ? p.cols - col : 0u;
-            const uint64_t at = row_at + col;
+            const bool full = col[v] + E <= p.cols;
+            const uint32_t n = col[v] < p.cols ? p.cols - col[v] : 0u;
+            const uint64_t at = row_at + col[v];
             if (p.has_res_out != 0 && n != 0) {
-                const Raw8<T> x = narrow8<T>(h[v]);
+                const u32x4 x = narrow_piece<T>(h[v]);
                 for (uint32_t r = 0; r < p.nranks; ++r) {
                     if (full)
-                        store8<T, NT>(p.res_out[r] + at * T::kBytes, x);
+                        store_piece<NT>(p.res_out[r] + at * T::kBytes, x);
                     else
                         store_some<T>(p.res_out[r] + at * T::kBytes, x, n);
                 }
             }
-            float y[8] = {};
-            if (n != 0) {
-                const char *w = p.weight + (uint64_t)col * T::kBytes;
-                float f[8];
-                widen8<T>(full ? load8<T, false>(w) : load_some<T>(w, n), f);
+            float y[E], f[E];
+            if constexpr (!kEarly)
+                weight[v] = load_weight(v);
+            widen_piece<T>(weight[v], f);
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    y[e] = full || (uint32_t)e < n ? h[v][e] * inv * f[e] : 0.0f;
-            }
+            for (uint32_t e = 0; e < E; ++e)
+                y[e] = full || e < n ? h[v][e] * inv * f[e] : 0.0f;
             if constexpr (EIGHT) {
-                // all lanes of a scale's 16 take part; those past the row hold 0
-                const float s = scale_of(max16(max_bits8(y)));
-                const u32x2 q = eight_of(y, 1.0f / s);
+                // all lanes of a scale take part; those past the row hold 0
+                const float s = scale_of(max_block<T>(max_bits(y)));
+                const Eights<E> q = to_eights(y, 1.0f / s);
                 if (n != 0) {
-                    const uint64_t sat = (uint64_t)(col / AR_SCALE_BLOCK) * p.rows + row;
+                    const uint64_t sat = (uint64_t)(col[v] / AR_SCALE_BLOCK) * p.rows + row;
                     for (uint32_t r = 0; r < p.nranks; ++r) {
                         if (full)
-                            store_eight<NT>(p.out[r] + at, q);
+                            store_eights<NT>(p.out[r] + at, q);
                         else
-                            store_eight_some(p.out[r] + at, q, n);
-                        if ((lane & 15u) == 0)
+                            store_eights_some(p.out[r] + at, q, n);
+                        if (col[v] % AR_SCALE_BLOCK == 0)
                             p.scales[r][sat] = s;
                     }
                 }
             } else if (n != 0) {
-                const Raw8<T> x = narrow8<T>(y);
+                const u32x4 x = narrow_piece<T>(y);
                 for (uint32_t r = 0; r < p.nranks; ++r) {
                     if (full)
-                        store8<T, NT>(p.out[r] + at * T::kBytes, x);
+                        store_piece<NT>(p.out[r] + at * T::kBytes, x);
                     else
                         store_some<T>(p.out[r] + at * T::kBytes, x, n);
                 }
@@ -171,20 +217,36 @@ hipError_t enqueue(const NormArgs &args, uint32_t threads, bool nt, hipStream_t 
     return hipGetLastError();
 }
 
+// As many lanes a row as it has pieces where rows are few (the pieces' loads
+// are then all under way at once: one row of 8 ranks x 8192 takes 6.0 us with
+// 1024 lanes and 8.0 with 512); two pieces a lane where there are rows for
+// every compute unit (the smaller workgroups overlap one row's stores with
+// another's loads: 1 x 8192 x 8192 takes 96 against 111 us, 8 x 512 x 8192
+// 32.6 against 33.9, 8 x 8192 x 8192 638 against 645).
+// Non-temporal accesses from 64 MiB moved (8 x 512 x 8192: 33 against 43 us;
+// 8 x 4096 x 512, 88 MB: 19.7 against 19.9; below that the two are equal, and
+// what reads the results next finds them in the last-level cache).
 template <typename T, bool EIGHT>
-hipError_t pick(const NormArgs &args, hipStream_t stream)
+hipError_t pick(const NormArgs &args, int cu_count, hipStream_t stream)
 {
-    const uint32_t groups = (args.cols + 7u) / 8u;
-    uint32_t threads = (groups + 63u) / 64u * 64u;
-    if (threads > 1024u)
-        threads = 1024u;
-    const uint32_t v = (groups + threads - 1u) / threads;
-    const bool nt = args.rows * args.cols * T::kBytes * args.nranks > ((uint64_t)128 << 20);
-    if (v <= 1)
-        return enqueue<T, 1, EIGHT>(args, threads, nt, stream);
-    if (v <= 2)
-        return enqueue<T, 2, EIGHT>(args, threads, nt, stream);
-    return enqueue<T, 4, EIGHT>(args, threads, nt, stream);
+    const uint32_t pieces = (args.cols + kPiece<T> - 1u) / kPiece<T>;
+    const bool many = args.rows >= 2u * (uint64_t)cu_count;
+    uint32_t v = many && pieces >= 128u ? 2u : 1u;
+    while (v * 1024u < pieces)
+        v *= 2u;
+    const uint32_t threads = (pieces + 64u * v - 1u) / (64u * v) * 64u;
+    const uint64_t moved = args.rows * args.cols * args.nranks *
+                           (T::kBytes * (args.has_res_out != 0 ? 2u : 1u) + (EIGHT ? 1u : T::kBytes));
+    const bool nt = moved >= (uint64_t)64 << 20;
+    switch (v) {
+    case 1: return enqueue<T, 1, EIGHT>(args, threads, nt, stream);
+    case 2: return enqueue<T, 2, EIGHT>(args, threads, nt, stream);
+    case 4: return enqueue<T, 4, EIGHT>(args, threads, nt, stream);
+    }
+    // (a 16-bit row of 32768 columns has four pieces a lane)
+    if constexpr (kPiece<T> == 4)
+        return enqueue<T, 8, EIGHT>(args, threads, nt, stream);
+    return hipErrorInvalidValue;
 }
 
 }  // namespace
@@ -192,11 +254,10 @@ hipError_t pick(const NormArgs &args, hipStream_t stream)
 hipError_t launch_norm(const NormArgs &args, int dtype, bool eight, int cu_count,
                        hipStream_t stream)
 {
-    (void)cu_count;
     switch (dtype) {
-    case kBf16: return eight ? pick<Bf16, true>(args, stream) : pick<Bf16, false>(args, stream);
-    case kFp16: return eight ? pick<Fp16, true>(args, stream) : pick<Fp16, false>(args, stream);
-    default: return eight ? pick<Fp32, true>(args, stream) : pick<Fp32, false>(args, stream);
+    case kBf16: return eight ? pick<Bf16, true>(args, cu_count, stream) : pick<Bf16, false>(args, cu_count, stream);
+    case kFp16: return eight ? pick<Fp16, true>(args, cu_count, stream) : pick<Fp16, false>(args, cu_count, stream);
+    default: return eight ? pick<Fp32, true>(args, cu_count, stream) : pick<Fp32, false>(args, cu_count, stream);
     }
 }
 
