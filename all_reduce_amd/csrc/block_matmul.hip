@@ -15,6 +15,8 @@
 // loaded alike, so the instruction's own order of k inside the 128 does not
 // matter.  Result: lane l holds column (activation row) l % 16 and rows
 // (output columns) 4 (l / 16) .. + 3.
+#include <math.h>
+
 #include "block_device.hpp"
 #include "block_internal.hpp"
 #include "block_matmul.hpp"
@@ -162,12 +164,22 @@ uint64_t ceil_div(uint64_t a, uint64_t b) { return (a + b - 1) / b; }
 
 }  // namespace
 
-// The kernel that is expected to be fastest.  Each one's time is rounds of
-// workgroups over the chip times blocks of k (a wave's share of them in the
-// decode-batch kernel) times what one block takes, and not less than the
-// weights take from memory; the constants were measured on MI355X over 1 to
-// 2048 rows, 512 to 8192 columns, k 1024 and 8192, 1 and 8 ranks, each rank's
-// own product and the sum.  Some of what they tell apart (us, bfloat16 out):
+// The kernels for three rows and more: tiles of rows x columns whose `waves`
+// share k, `resident` workgroups to a compute unit, and the time they take (us)
+//
+//     base + each * Q + MB written / 3
+//          + max(alone * ceil(Q / resident) * S, full * W * S, MB read / rate)
+//
+// for Q = ceil(W) workgroups a compute unit (W of them on average) of S steps
+// (blocks of k to a wave): a step takes `alone` where nothing else is on the
+// compute unit and `full` a workgroup where it is filled; the rate is 5 MB/us,
+// less where inputs that no cache keeps (from 64 MB) have to come through a
+// part of the compute units (64 x 8192 x 8 x 3584 summed: 58 us with one
+// workgroup a compute unit, 77 with one on every second).  The numbers were
+// fitted to 700 measured shapes on MI355X (3 to 8192 rows, 64 to 8192 columns,
+// k 128 to 8192, 1 to 8 ranks, each rank's product and the sum; 10 to 17 % off
+// in the mean): the kernel chosen by them takes 1.02 times the fastest one's
+// time in the mean.  What they tell apart, for example (us, bfloat16 out):
 //
 //                                    64x32   64x64   128x128  256x256
 //     1 rank,    64 x 8192 x 8192     14      17       52       85
@@ -177,6 +189,25 @@ uint64_t ceil_div(uint64_t a, uint64_t b) { return (a + b - 1) / b; }
 //     8 ranks,  100 x 8192 x 8192             157      108      125
 //     8 ranks,  256 x 8192 x 8192             273      191      155
 //     8 ranks, 1024 x 8192 x 8192            1023      632      448
+struct Choice {
+    uint32_t rows, cols, waves, resident;
+    float base, alone, full, each;
+};
+
+constexpr int kChoices = 9;
+constexpr Choice kChoice16[kChoices] = {
+    {32, 32, 8, 1, 2.29f, 0.67f, 1.13f, 0.86f}, {32, 32, 4, 2, 3.47f, 0.39f, 0.57f, 0.0f},
+    {32, 32, 2, 4, 3.35f, 0.37f, 0.30f, 0.0f},  {64, 32, 4, 1, 2.47f, 0.56f, 0.93f, 1.32f},
+    {64, 32, 2, 3, 3.75f, 0.50f, 0.51f, 0.0f},  {64, 64, 4, 1, 2.54f, 0.84f, 1.22f, 2.07f},
+    {64, 64, 2, 2, 4.29f, 0.70f, 0.68f, 0.63f}, {128, 128, 1, 2, 3.27f, 0.73f, 0.64f, 0.0f},
+    {256, 256, 1, 1, 4.80f, 1.38f, 1.38f, 0.0f}};
+// With exact products; 256 x 256 tiles have no registers left for those.
+constexpr Choice kChoice32[kChoices - 1] = {
+    {32, 32, 8, 1, 2.37f, 0.81f, 1.19f, 1.11f}, {32, 32, 4, 2, 3.23f, 0.52f, 0.56f, 0.34f},
+    {32, 32, 2, 4, 3.41f, 0.52f, 0.33f, 0.04f}, {64, 32, 4, 1, 2.19f, 0.74f, 0.98f, 1.76f},
+    {64, 32, 2, 3, 3.90f, 0.67f, 0.60f, 0.12f}, {64, 64, 4, 1, 2.17f, 1.19f, 1.37f, 2.69f},
+    {64, 64, 2, 2, 4.22f, 1.07f, 0.81f, 1.03f}, {128, 128, 1, 2, 3.74f, 1.11f, 0.67f, 0.0f}};
+
 hipError_t launch_matmul(const MatmulArgs &args, int out_dtype, bool reduce, int cu_count,
                          hipStream_t stream)
 {
@@ -187,38 +218,30 @@ hipError_t launch_matmul(const MatmulArgs &args, int out_dtype, bool reduce, int
         default: return enqueue_rows<Fp32>(args, reduce, stream);
         }
     }
-    const uint64_t cus = (uint64_t)cu_count;
-    const uint64_t steps = (uint64_t)args.kblocks * (reduce ? args.nranks : 1u);
-    auto tiles = [&](uint32_t m, uint32_t n) {
-        return ceil_div(args.rows, m) * ceil_div(args.n, n) * (reduce ? 1u : args.nranks);
-    };
-    if (args.rows <= 32) {
-        // 32 x 32 tiles; eight waves where one workgroup a compute unit is all
-        // there is, else more workgroups of fewer waves
-        const uint32_t waves = tiles(32, 32) <= cus ? 8 : steps < 32 ? 2 : 4;
-        return launch_matmul_mid(args, out_dtype, reduce, 1, 1, waves, stream);
-    }
-    const double memory = (double)args.n * args.k * args.nranks / 5.2e6;
-    auto at_least = [&](double us) { return us > memory ? us : memory; };
-    // a binary32 output's products are exact, and take three times as long
     const bool exact = out_dtype == kFp32;
-    const uint64_t t21 = tiles(64, 32), t22 = tiles(64, 64), t1 = tiles(128, 128), t2 = tiles(256, 256);
-    const double share = (double)ceil_div(steps, 4);
-    const double us21 = 2.5 + at_least((double)ceil_div(t21, cus) * share * 0.70);
-    const double us22 = 2.5 + at_least((double)ceil_div(t22, cus) * share * 0.95);
-    const double us1 = 3.0 + at_least((t1 <= cus ? 0.80 : 1.20 * (double)ceil_div(t1, 2 * cus)) *
-                                      (double)steps * (exact ? 1.5 : 1.0));
-    // (256 x 256 tiles have no registers left for the exact products)
-    const double us2 = exact ? us1 + 1.0
-                             : 3.0 + at_least((double)ceil_div(t2, cus) * (double)steps *
-                                              (t2 <= cus ? 1.33 : 1.65));
-    if (us2 < us1 && us2 < us22 && us2 < us21)
-        return launch_matmul_tile(args, out_dtype, reduce, true, stream);
-    if (us1 < us22 && us1 < us21)
-        return launch_matmul_tile(args, out_dtype, reduce, false, stream);
-    if (us21 < us22)
-        return launch_matmul_mid(args, out_dtype, reduce, 2, 1, t21 > cus && steps < 32 ? 2 : 4, stream);
-    return launch_matmul_mid(args, out_dtype, reduce, 2, 2, t22 > cus && steps < 32 ? 2 : 4, stream);
+    const Choice *choices = exact ? kChoice32 : kChoice16;
+    const Choice *best = nullptr;
+    double best_us = 0.0;
+    const double ranks = args.nranks, steps = (double)args.kblocks * (reduce ? ranks : 1.0);
+    const double read = ((double)args.rows + args.n) * args.k * ranks * 1e-6;
+    for (int i = 0; i < (exact ? kChoices - 1 : kChoices); ++i) {
+        const Choice &c = choices[i];
+        const double w = (double)(ceil_div(args.rows, c.rows) * ceil_div(args.n, c.cols)) *
+                         (reduce ? 1.0 : ranks) / cu_count;
+        const double q = ceil(w), s = ceil(steps / c.waves);
+        const double rate = read > 64.0 ? 5.0 * fmin(1.0, 1.3 * w) : 5.0;
+        // (what is written is the same for all)
+        const double us = c.base + c.each * q +
+                          fmax(fmax(c.alone * ceil(q / c.resident) * s, c.full * w * s), read / rate);
+        if (best == nullptr || us < best_us) {
+            best = &c;
+            best_us = us;
+        }
+    }
+    if (best->rows >= 128u)
+        return launch_matmul_tile(args, out_dtype, reduce, best->rows == 256u, stream);
+    return launch_matmul_mid(args, out_dtype, reduce, (int)best->rows / 32, (int)best->cols / 32,
+                             best->waves, stream);
 }
 
 }  // namespace ar
