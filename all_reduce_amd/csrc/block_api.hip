@@ -154,7 +154,7 @@ arResult_t arAllReduceNorm(const void *const *sendbufs, const void *residual, co
     const size_t bytes = rows * cols * elem_bytes(dtype);
     const bool eight = scalebufs != nullptr;
     Ranges mem;
-    bool residual_written = false, ok = true;
+    bool residual_written = false, in_place = false, ok = true;
     for (int r = 0; r < nranks && ok; ++r) {
         // A written buffer that is exactly this rank's send buffer, or the
         // residual, stands for both: a row is read before it is written.
@@ -172,6 +172,7 @@ arResult_t arAllReduceNorm(const void *const *sendbufs, const void *residual, co
         if (eight)
             ok = ok && mem.add(scalebufs[r], scale_blocks(cols) * rows * sizeof(float), true);
         ok = ok && (send_written || mem.add(sendbufs[r], bytes, false));
+        in_place |= send_written;
     }
     if (residual != nullptr && !residual_written)
         ok = ok && mem.add(residual, bytes, false);
@@ -195,6 +196,7 @@ arResult_t arAllReduceNorm(const void *const *sendbufs, const void *residual, co
     args.cols = (uint32_t)cols;
     args.nranks = (uint32_t)nranks;
     args.has_res_out = residualOut != nullptr;
+    args.in_place = in_place || (residual != nullptr && residual_written);
     args.eps = eps;
     return launched(ar::launch_norm(args, dtype, eight, comm->cu_count, (hipStream_t)stream));
 }

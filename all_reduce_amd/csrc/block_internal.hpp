@@ -22,6 +22,8 @@ struct NormArgs {
     uint32_t cols;
     uint32_t nranks;
     uint32_t has_res_out;
+    uint32_t in_place;  // a written buffer is also a read one
+    uint32_t split;     // workgroups a row (the launcher sets it)
     float eps;
 };
 

@@ -7,13 +7,17 @@
 // squares crosses the workgroup through LDS; then every lane scales its own
 // columns and stores them to all ranks.  So each input is read once and each
 // output written once, and a row's reads are complete before its first write
-// (which is what makes the exact in-place forms safe).
+// (which is what makes the exact in-place forms safe).  Where there are fewer
+// rows than compute units, several workgroups take a row, each sums all of it
+// and each stores to its share of the ranks: a row's stores are more bytes
+// than its reads and take longer than reading it again from the cache.
 //
 // It is bound by memory: R + 1 reads and 2 R writes a column at two or three
 // operations each.  On MI355X 8 x 8192 x 8192 bfloat16 with residual takes
 // 650 us (5.2 TB/s; a large copy runs at 5.1), 16 x 1024 x 7168 float32 with
-// an 8-bit output 211 us (5.1 TB/s); one row of 8 x 8192, on one compute unit,
-// 6.0 us and 64 rows 8.4, bound by a row's chain of loads, sum and stores.
+// an 8-bit output 211 us (5.1 TB/s).  One row of 8 x 8192 takes 5.2 us (6.0
+// with one workgroup) and 64 rows 7.4 (8.4), bound by a row's chain of loads,
+// sum and stores.
 #include "block_device.hpp"
 #include "block_internal.hpp"
 
@@ -80,8 +84,13 @@ __global__ __launch_bounds__(1024) void norm_rows(NormArgs p)
         for (int v = 0; v < V; ++v)
             weight[v] = load_weight(v);
     }
+    // The p.split workgroups of a row each sum all of it, and each stores to
+    // every split-th rank.  Rows go round the eight XCDs (workgroup w runs on
+    // XCD w % 8) and a row's workgroups share one, and its cache.
+    const uint32_t share = blockIdx.x / 8u % p.split;
     uint32_t turn = 0;
-    for (uint64_t row = blockIdx.x; row < p.rows; row += gridDim.x, turn ^= 1u) {
+    for (uint64_t row = blockIdx.x / (8u * p.split) * 8u + blockIdx.x % 8u; row < p.rows;
+         row += gridDim.x / p.split, turn ^= 1u) {
         const uint64_t row_at = row * p.cols;
         float h[V][E];
         u32x4 res[V];
@@ -162,7 +171,7 @@ __global__ __launch_bounds__(1024) void norm_rows(NormArgs p)
             const uint64_t at = row_at + col[v];
             if (p.has_res_out != 0 && n != 0) {
                 const u32x4 x = narrow_piece<T>(h[v]);
-                for (uint32_t r = 0; r < p.nranks; ++r) {
+                for (uint32_t r = share; r < p.nranks; r += p.split) {
                     if (full)
                         store_piece<NT>(p.res_out[r] + at * T::kBytes, x);
                     else
@@ -182,7 +191,7 @@ __global__ __launch_bounds__(1024) void norm_rows(NormArgs p)
                 const Eights<E> q = to_eights(y, 1.0f / s);
                 if (n != 0) {
                     const uint64_t sat = (uint64_t)(col[v] / AR_SCALE_BLOCK) * p.rows + row;
-                    for (uint32_t r = 0; r < p.nranks; ++r) {
+                    for (uint32_t r = share; r < p.nranks; r += p.split) {
                         if (full)
                             store_eights<NT>(p.out[r] + at, q);
                         else
@@ -193,7 +202,7 @@ __global__ __launch_bounds__(1024) void norm_rows(NormArgs p)
                 }
             } else if (n != 0) {
                 const u32x4 x = narrow_piece<T>(y);
-                for (uint32_t r = 0; r < p.nranks; ++r) {
+                for (uint32_t r = share; r < p.nranks; r += p.split) {
                     if (full)
                         store_piece<NT>(p.out[r] + at * T::kBytes, x);
                     else
@@ -209,7 +218,8 @@ namespace {
 template <typename T, int V, bool EIGHT>
 hipError_t enqueue(const NormArgs &args, uint32_t threads, bool nt, hipStream_t stream)
 {
-    const uint32_t grid = args.rows < (1u << 20) ? (uint32_t)args.rows : (1u << 20);
+    const uint64_t rows = args.rows < (1u << 20) ? args.rows : (1u << 20);
+    const uint32_t grid = (uint32_t)((rows + 7u) / 8u * 8u * args.split);
     if (nt)
         hipLaunchKernelGGL((norm_rows<T, V, EIGHT, true>), dim3(grid), dim3(threads), 0, stream, args);
     else
@@ -227,7 +237,7 @@ hipError_t enqueue(const NormArgs &args, uint32_t threads, bool nt, hipStream_t 
 // 8 x 4096 x 512, 88 MB: 19.7 against 19.9; below that the two are equal, and
 // what reads the results next finds them in the last-level cache).
 template <typename T, bool EIGHT>
-hipError_t pick(const NormArgs &args, int cu_count, hipStream_t stream)
+hipError_t pick(NormArgs args, int cu_count, hipStream_t stream)
 {
     const uint32_t pieces = (args.cols + kPiece<T> - 1u) / kPiece<T>;
     const bool many = args.rows >= 2u * (uint64_t)cu_count;
@@ -238,6 +248,11 @@ hipError_t pick(const NormArgs &args, int cu_count, hipStream_t stream)
     const uint64_t moved = args.rows * args.cols * args.nranks *
                            (T::kBytes * (args.has_res_out != 0 ? 2u : 1u) + (EIGHT ? 1u : T::kBytes));
     const bool nt = moved >= (uint64_t)64 << 20;
+    // Fewer rows than compute units: a row's stores are shared out by rank.
+    // (In place that would write what another workgroup has yet to read.)
+    uint64_t split = args.in_place != 0 ? 1u : (uint64_t)cu_count / args.rows;
+    split = split < args.nranks ? split : args.nranks;
+    args.split = split < 1u ? 1u : (uint32_t)split;
     switch (v) {
     case 1: return enqueue<T, 1, EIGHT>(args, threads, nt, stream);
     case 2: return enqueue<T, 2, EIGHT>(args, threads, nt, stream);
