@@ -107,6 +107,14 @@ __device__ inline void to_lds4(const char *at, uint32_t to)
                  : "memory");
 }
 
+// Waits until at most N of the wave's loads are under way.
+template <int N>
+__device__ inline void wait_loads()
+{
+    static_assert(N < 64, "the counter has six bits");
+    asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory");
+}
+
 // Four consecutive columns of a row, those below `n`.
 template <typename T>
 __device__ inline void store4(char *out, uint64_t row, uint32_t n, uint32_t col, f32x4 c)

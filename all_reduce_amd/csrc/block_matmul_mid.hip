@@ -29,14 +29,6 @@ struct MidPlace {
     static constexpr int kLoads = (MT + NT) * 4 + MT / 2 + 1;
 };
 
-// Waits until at most N of the wave's loads are under way.
-template <int N>
-__device__ inline void wait_loads()
-{
-    static_assert(N < 64, "the counter has six bits");
-    asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory");
-}
-
 template <typename T, int MT, int NT, int D, bool REDUCE>
 __global__ __launch_bounds__(512) void matmul_mid(MatmulArgs p)
 {

@@ -8,7 +8,15 @@
 // in turn, so that one is loaded while the other is multiplied.  A wave
 // computes 64 rows x 128 (64) columns in 32x32 tiles: the columns of a wave
 // lie in one weight scale block, so a step's scale is one number a lane and
-// row tile, applied with a fused multiply-add to the running sums.
+// row tile, applied with a fused multiply-add to the running sums.  (Four
+// 16x16x128 instructions in place of two 32x32x64 ones: 2 % slower.)
+//
+// On MI355X 8 x (4096 x 7168 x 8192) takes 1740 to 1780 us on random values,
+// 2.16 to 2.21 PFLOP/s, and 1416 us, 2.72 PFLOP/s, on constant ones: the
+// card's power sets the clock (1.5 to 1.8 against 2.3 GHz).  Of copies on
+// random values, one without the scaling took 12 % less, one without the LDS
+// reads 8 %, one without the loads 12 %.  The instructions alone reach 4.1
+// PFLOP/s with the scaling on constant values, 3.25 on random ones.
 //
 // LDS rows are the 128 bytes of a step, in eight pieces of 16; piece c of row
 // r is kept at place c ^ (r / 2 % 8).  Two rows cover all banks once, so 16
@@ -16,8 +24,6 @@
 // rows 8 apart met: half of the LDS cycles were conflicts).  A direct load
 // writes its lanes' pieces one after the other, so the exchange is made in
 // the lanes' global addresses.
-#include <type_traits>
-
 #include "block_device.hpp"
 #include "block_internal.hpp"
 #include "block_matmul.hpp"
@@ -31,6 +37,14 @@ struct TileShape {
     static constexpr uint32_t kRows = WM * 64u, kCols = WN * NT * 32u, kWaves = WM * WN;
     static constexpr uint32_t kRowBytes = kRows * 128u, kColBytes = kCols * 128u;  // of a step
     static constexpr uint32_t kLoadsM = kRows / 8u / kWaves, kLoadsN = kCols / 8u / kWaves;
+    // LDS: rows of both steps, columns of both, scales of both (a float a row,
+    // then 64 times the same for each 128 columns), a place that nothing reads
+    static constexpr uint32_t kScaleWaves = kRows / 64u + kCols / 128u;
+    static constexpr uint32_t kScaleBytes = kScaleWaves * 256u;
+    static constexpr uint32_t kScalesAt = 2u * (kRowBytes + kColBytes);
+    static constexpr uint32_t kUnusedAt = kScalesAt + 2u * kScaleBytes;
+    static constexpr uint32_t kBytes = kUnusedAt + (kWaves - kScaleWaves) * 256u;
+    static_assert(kScaleWaves < kWaves, "a wave is left to bring lines");
 };
 
 template <typename T, int NT, int WM, int WN, bool REDUCE>
@@ -38,8 +52,7 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void matmul_tile(MatmulArgs p)
 {
     constexpr bool kExact = T::kBytes == 4;
     typedef TileShape<NT, WM, WN> S;
-    // rows of both steps, then columns of both
-    __shared__ __align__(128) char lds[2 * (S::kRowBytes + S::kColBytes)];
+    __shared__ __align__(128) char lds[S::kBytes];
     const uint32_t lane = threadIdx.x & 63u;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 
@@ -82,23 +95,11 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void matmul_tile(MatmulArgs p)
     const uint32_t wm = wave % WM * 64u, wn = wave / WM * (NT * 32u);
     const uint32_t l32 = lane & 31u, half = lane >> 5;
     const uint32_t place = l32 * 128u + ((half * 2u) ^ (l32 >> 1 & 7u)) * 16u;
-    uint32_t m[2];
-#pragma unroll
-    for (uint32_t j = 0; j < 2; ++j) {
-        const uint32_t row = m0 + wm + j * 32u + l32;
-        m[j] = row < p.rows ? row : p.rows - 1u;
-    }
-
-    // What the next load reads: block kb of rank r, from these on.  The weight
-    // scale is loaded like the others, by a vector instruction: a scalar one
-    // shares its wait counter with LDS reads, which would then wait for it in
-    // every step.
+    // What the next load reads: block kb of rank r, from these on.
     const uint32_t nranks = REDUCE ? p.nranks : 1u;
     uint32_t r = 0, kb = 0;
     const char *a, *b;
     const float *sa, *sb;
-    uint32_t sb_off = n0 + wn < p.n ? (n0 + wn) / 128u * p.kblocks : 0u;
-    asm volatile("" : "+v"(sb_off));
     auto at_rank = [&] {
         a = p.a[rank0 + r] + (uint64_t)m0 * p.k;
         b = p.b[rank0 + r] + (uint64_t)n0 * p.k;
@@ -116,13 +117,42 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void matmul_tile(MatmulArgs p)
             to_lds(b, offn[i] - back, ton + stage * S::kColBytes + i * 1024u);
     };
     constexpr uint32_t kParts = S::kLoadsM > S::kLoadsN ? S::kLoadsM : S::kLoadsN;
-    // Their scales (multiplied later: here that would wait for the loads
-    // before), then on to the next block; after the last one the loads repeat.
-    auto load_scales = [&](float (&s)[3]) {
-#pragma unroll
-        for (uint32_t j = 0; j < 2; ++j)
-            s[j] = sa[m[j]];
-        s[2] = sb[sb_off];
+    // One more load a wave, then on to the next block (after the last one the
+    // loads repeat).  The first waves load the scales, 64 rows' or a block of
+    // columns' each (nothing in the loop goes through registers that the
+    // compiler would wait for).  The other waves bring lines of the block
+    // after the next into the second-level cache, so that the direct loads,
+    // which are waited for within a step, do not wait for memory: a quarter of
+    // the rows' and an eighth of the columns', the rest being the same tiles'
+    // to the sides and above, which run at the same time.  (On constant values,
+    // where power is no limit, 8 x 4096 x 7168 x 8192 takes 1416 against
+    // 1571 us; on random ones the two are within 2 %.)
+    const uint32_t helper = wave - S::kScaleWaves;  // (used where wave >= kScaleWaves)
+    uint32_t off1;
+    if (wave < S::kRows / 64u) {
+        const uint32_t row = wave * 64u + lane;
+        off1 = (m0 + row < p.rows ? m0 + row : p.rows - 1u) * 4u;
+    } else if (wave < S::kScaleWaves) {
+        const uint32_t col = n0 + (wave - S::kRows / 64u) * 128u;
+        off1 = (col < p.n ? col / 128u : 0u) * p.kblocks * 4u;
+    } else {
+        const uint32_t i = helper * 64u + lane;
+        uint32_t row = t / wide % 8u * (S::kCols / 8u) + (i - S::kRows / 4u) % (S::kCols / 8u), end = p.n - n0;
+        if (i < S::kRows / 4u) {
+            row = t % wide * (S::kRows / 4u) + i;
+            end = p.rows - m0;
+        }
+        off1 = (row < end ? row : end - 1u) * p.k;
+    }
+    auto finish = [&](uint32_t stage) {
+        const uint32_t to = lds0 + S::kScalesAt + stage * S::kScaleBytes + wave * 256u;
+        const uint32_t far = kb + 2u < p.kblocks ? 256u : 0u;
+        if (wave < S::kRows / 64u)
+            to_lds4((const char *)sa + off1, to);
+        else if (wave < S::kScaleWaves)
+            to_lds4((const char *)sb + off1, to);
+        else
+            to_lds4((helper * 64u + lane < S::kRows / 4u ? a : b) + far + off1, lds0 + S::kUnusedAt + helper * 256u);
         if (kb + 1u < p.kblocks) {
             ++kb;
             a += 128;
@@ -136,92 +166,117 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void matmul_tile(MatmulArgs p)
         }
     };
 
+    // The steps run into one another: the wave waits for the others (all have
+    // read this step's LDS, all have the next step's loads in it) before its
+    // last two tiles, whose operands are in registers, so that their products
+    // cover the wait and the next step's first reads.  A tile's products are
+    // under way while the one before it is scaled, across steps too.  The
+    // loads of the step after next go out between the products of the two
+    // tiles before and after a step's end: all at once they would hold the
+    // products back.
     f32x16 acc[NT][2] = {};
-    float s_next[3];
-    at_rank();
-#pragma unroll
-    for (uint32_t i = 0; i < kParts; ++i)
-        load(0, i);
-    load_scales(s_next);
-
-    // One step: multiplies half `stage`, loads the other one.  `left`: bytes of
-    // the block that are in the row; those past it (TAIL) are zero in the
-    // weights, and in the activations a repeat of the row's own, so that a NaN
-    // there is one that the row has anyway.
-    auto step = [&](uint32_t stage, auto tail, uint32_t left) {
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        // After this every wave's loads of this step are in LDS, and no wave
-        // reads the other half any more.
-        __syncthreads();
-        float s[2] = {s_next[0] * s_next[2], s_next[1] * s_next[2]};
-        // (here, where they are at hand: a wait for them further down would
-        // also wait for the next step's loads)
-        asm volatile("" : "+v"(s[0]), "+v"(s[1]));
-        const char *pm = lds + stage * S::kRowBytes + wm * 128u;
-        const char *pn = lds + 2u * S::kRowBytes + stage * S::kColBytes + wn * 128u;
-        auto weights = [&](uint32_t i, uint32_t h) {
-            i32x8 w = pieces(pn + i * 4096u, place ^ (h * 64u));
-            if constexpr (decltype(tail)::value) {
-#pragma unroll
-                for (uint32_t e = 0; e < 8; ++e)
-                    w[e] = (h * 4u + half * 2u + e / 4u) * 16u < left ? w[e] : 0;
-            }
-            return w;
-        };
-        i32x8 x[2][2], w[2];
-#pragma unroll
-        for (uint32_t h = 0; h < 2; ++h) {
-            x[0][h] = pieces(pm, place ^ (h * 64u));
-            w[h] = weights(0, h);
-        }
+    f32x16 c[2] = {};
+    i32x8 x[2][2], w[2];
+    float s[2], s_last = 0.0f;
+    auto rows = [&](uint32_t stage, uint32_t j) {
+        const char *pm = lds + stage * S::kRowBytes + wm * 128u + j * 4096u;
 #pragma unroll
         for (uint32_t h = 0; h < 2; ++h)
-            x[1][h] = pieces(pm + 4096u, place ^ (h * 64u));
-        __builtin_amdgcn_sched_barrier(0);
-        // A tile's products are under way while the one before it is scaled.
-        // The next step's loads go out between the products: all of them at
-        // once would hold the first product back.
-        f32x16 c[2];
+            x[j][h] = pieces(pm, place ^ (h * 64u));
+    };
+    auto columns = [&](uint32_t stage, uint32_t i) {
+        const char *pn = lds + 2u * S::kRowBytes + stage * S::kColBytes + wn * 128u + i * 4096u;
+#pragma unroll
+        for (uint32_t h = 0; h < 2; ++h)
+            w[h] = pieces(pn, place ^ (h * 64u));
+    };
+    auto arrived = [&](uint32_t stage) {
+        if (wave < S::kScaleWaves)
+            wait_loads<0>();
+        else
+            wait_loads<1>();
+        __syncthreads();
+        const float *scales = (const float *)(lds + S::kScalesAt + stage * S::kScaleBytes);
+        const float sw = scales[S::kRows + wn / 128u * 64u + lane];
+#pragma unroll
+        for (uint32_t j = 0; j < 2; ++j)
+            s[j] = scales[wm + j * 32u + l32] * sw;
+    };
+
+    // One step: half `stage`.  `left`: bytes of the block that are in the row;
+    // those past it are zero in the weights, and in the activations a repeat
+    // of the row's own, so that a NaN there is one that the row has anyway.
+    auto step = [&](uint32_t stage, uint32_t left) {
+        float s_this[2] = {s[0], s[1]};
 #pragma unroll
         for (uint32_t i = 0; i < NT; ++i) {
-            if (i > 0) {
+            if (left < 128u) {
 #pragma unroll
                 for (uint32_t h = 0; h < 2; ++h)
-                    w[h] = weights(i, h);
+#pragma unroll
+                    for (uint32_t e = 0; e < 8; ++e)
+                        w[h][e] = (h * 4u + half * 2u + e / 4u) * 16u < left ? w[h][e] : 0;
+            }
+            if (i == NT - 1u) {
+                __builtin_amdgcn_sched_barrier(0);
+                arrived(stage ^ 1u);
             }
 #pragma unroll
             for (uint32_t j = 0; j < 2; ++j) {
                 c[j] = block_sums32<kExact>(w, x[j]);
                 __builtin_amdgcn_sched_barrier(0);
-                if (i + j > 0) {
-                    const uint32_t pi = j == 0 ? i - 1u : i, pj = j ^ 1u;
+                if (i == NT - 1u)
+                    rows(stage ^ 1u, j);
+                if (j == 1)
+                    columns(i == NT - 1u ? stage ^ 1u : stage, i == NT - 1u ? 0u : i + 1u);
+                __builtin_amdgcn_sched_barrier(0);
+                const uint32_t pi = j == 1 ? i : i == 0 ? NT - 1u : i - 1u, pj = j ^ 1u;
+                const float ps = i + j == 0 ? s_last : s_this[pj];
 #pragma unroll
-                    for (uint32_t e = 0; e < 16; ++e)
-                        acc[pi][pj][e] = __builtin_fmaf(c[pj][e], s[pj], acc[pi][pj][e]);
-                    // (done here: put off, it keeps every tile's registers)
-                    asm volatile("" : "+v"(acc[pi][pj]));
+                for (uint32_t e = 0; e < 16; ++e)
+                    acc[pi][pj][e] = __builtin_fmaf(c[pj][e], ps, acc[pi][pj][e]);
+                // (done here: put off, it keeps every tile's registers)
+                asm volatile("" : "+v"(acc[pi][pj]));
+                if (i == 0) {
+#pragma unroll
+                    for (uint32_t q = kParts / 2u + j * (kParts / 4u);
+                         q < kParts / 2u + (j + 1u) * (kParts / 4u); ++q)
+                        load(stage ^ 1u, q);
+                    if (j == 1)
+                        finish(stage ^ 1u);
                 }
-                if (i * 2u + j < kParts)
-                    load(stage ^ 1u, i * 2u + j);
+                if (i == NT - 1u) {
+#pragma unroll
+                    for (uint32_t q = j * (kParts / 4u); q < (j + 1u) * (kParts / 4u); ++q)
+                        load(stage, q);
+                }
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
-        load_scales(s_next);
-#pragma unroll
-        for (uint32_t e = 0; e < 16; ++e)
-            acc[NT - 1][1][e] = __builtin_fmaf(c[1][e], s[1], acc[NT - 1][1][e]);
-        asm volatile("" : "+v"(acc[NT - 1][1]));
+        s_last = s_this[1];
     };
-    uint32_t stage = 0;
-    const uint32_t full = p.k / 128u;
-    for (uint32_t q = 0; q < nranks; ++q) {
-        for (uint32_t i = 0; i < full; ++i, stage ^= 1u)
-            step(stage, std::false_type{}, 128u);
-        if (full != p.kblocks) {
-            step(stage, std::true_type{}, p.k % 128u);
-            stage ^= 1u;
-        }
+    static_assert(kParts % 4 == 0, "the loads go out in four parts");
+
+    at_rank();
+#pragma unroll
+    for (uint32_t q = 0; q < kParts; ++q)
+        load(0, q);
+    finish(0);
+    arrived(0);
+    rows(0, 0);
+    columns(0, 0);
+    rows(0, 1);
+#pragma unroll
+    for (uint32_t q = 0; q < kParts / 2u; ++q)
+        load(1, q);
+    uint32_t left = p.k;
+    for (uint32_t n = 0; n < p.kblocks * nranks; ++n) {
+        step(n & 1u, left);
+        left = left > 128u ? left - 128u : p.k;
     }
+#pragma unroll
+    for (uint32_t e = 0; e < 16; ++e)
+        acc[NT - 1][1][e] = __builtin_fmaf(c[1][e], s_last, acc[NT - 1][1][e]);
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 
     // The sums go through LDS, 32 rows x 32 NT columns of a wave at a time, so
@@ -229,7 +284,7 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void matmul_tile(MatmulArgs p)
     // place c ^ (r % 8).
     __syncthreads();
     constexpr uint32_t kRow = NT * 32u * T::kBytes;
-    static_assert(S::kWaves * 32u * kRow <= sizeof(lds), "the waves' parts fit");
+    static_assert(S::kWaves * 32u * kRow <= S::kScalesAt, "the waves' parts fit");
     char *mine = lds + wave * (32u * kRow);
 #pragma unroll
     for (uint32_t j = 0; j < 2; ++j) {
