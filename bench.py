@@ -60,9 +60,12 @@ share of the 8 TB/s HBM peak, HBM GB/s from the committed rocprofv3 counter
 summaries where one covers the kernel, the oracle's time at 1 and at all
 host threads and its own GB/s, parity.
 
-``--only {sweep, prefill, copy, c5, c5b, hier, ll_variants, ceilings}`` runs
-one part alone (for profiler passes; c5b is the fp32 R = 16 / 32 workload at
-112 MiB per rank, hier the same in the two-level order, fused and staged).
+``--only {sweep, prefill, copy, c5, c5b, hier, ll_variants, ceilings, layer}``
+runs one part alone (for profiler passes; c5b is the fp32 R = 16 / 32 workload
+at 112 MiB per rank, hier the same in the two-level order, fused and staged;
+layer the MLP half of a tensor-parallel layer, 8 ranks of hidden 8192 and a
+28672-wide MLP in 8-bit values, at 1 and 64 tokens: µs of each operator and of
+the pass, graph-replayed).
 """
 from __future__ import annotations
 
@@ -94,7 +97,7 @@ def parse():
     ap.add_argument("--steps", type=int, default=10)
     ap.add_argument("--warmup", type=int, default=2)
     ap.add_argument("--only", choices=["all", "sweep", "prefill", "copy", "c5", "c5b", "hier",
-                                       "ll_variants", "ceilings"],
+                                       "ll_variants", "ceilings", "layer"],
                     default="all", help="run one part (for profiler passes and ablations)")
     ap.add_argument("--configs", action="store_true",
                     help="also measure every named workload and print the full table")
@@ -559,6 +562,10 @@ def main():
         for key in [k for k in rows[0] if k.endswith("_us")]:
             result[f"ll_variants_mean_{key}"] = round(statistics.mean(r[key] for r in rows), 3)
 
+    # ---- the operators around the all-reduce, as a layer runs them ------------
+    if args.only == "layer":
+        result["layer"] = [run_layer(B, tokens) for tokens in (1, 64)]
+
     # ---- every named workload as one table ----------------------------------
     if args.configs and args.only == "all":
         result["configs"] = run_configs(B, inputs, sweep_rows, result)
@@ -764,6 +771,68 @@ def run_c5(B, inputs, fp16=True):
                 f"({100 * g / HBM_PEAK_GBPS:.1f}% of 8 TB/s), parity {par}, exact {ex}")
         del x, sv, rv, exact
     return rows
+
+
+def run_layer(B, tokens):
+    """The MLP half of a tensor-parallel layer over 8 ranks: all-reduce of the
+    attention's partial sums with residual and norm into 8 bits, up product,
+    SiLU gate into 8 bits, down product, all-reduce with residual and norm; and
+    the down product with its all-reduce in one kernel.  Synthetic 8-bit
+    weights; the last output is checked to be finite and alike on every rank."""
+    torch, ar = B.torch, B.ar
+    ranks, hidden, inner = 8, 8192, 28672 // 8
+    e4m3, bf16 = torch.float8_e4m3fn, torch.bfloat16
+    gen = torch.Generator("cuda").manual_seed(tokens)
+
+    def bufs(rows, cols, dtype):
+        return list(torch.empty((ranks, rows, cols), dtype=dtype, device=B.dev).unbind(0))
+
+    def weights(n, k):
+        w, s = bufs(n, k, e4m3), bufs(ar.scale_blocks(n), ar.scale_blocks(k), torch.float32)
+        for t, u in zip(w, s):
+            t.copy_(torch.randn((n, k), generator=gen, device=B.dev).mul_(110).clamp_(-448, 448))
+            u.fill_(1 / (110 * k ** 0.5))
+        return w, s
+
+    x, h, h2, y = (bufs(tokens, hidden, bf16) for _ in range(4))
+    for t in x:
+        t.normal_(generator=gen)
+    res = torch.randn((tokens, hidden), generator=gen, device=B.dev).to(bf16)
+    norm = torch.ones(hidden, dtype=bf16, device=B.dev)
+    q, qs = bufs(tokens, hidden, e4m3), bufs(ar.scale_blocks(hidden), tokens, torch.float32)
+    up, part = bufs(tokens, 2 * inner, bf16), bufs(tokens, hidden, bf16)
+    g, gs = bufs(tokens, inner, e4m3), bufs(ar.scale_blocks(inner), tokens, torch.float32)
+    w1, s1 = weights(2 * inner, hidden)
+    w2, s2 = weights(hidden, inner)
+    c = B.comm
+    # (streams are taken where a call is made: graph capture has its own)
+    calls = {
+        "all-reduce + norm, 8-bit": lambda: c.all_reduce_norm(x, norm, 1e-5, res, h, q, qs),
+        "up product": lambda: c.matmul_scaled(q, qs, w1, s1, up),
+        "gate, 8-bit": lambda: c.gate_quant(up, g, gs),
+        "down product": lambda: c.matmul_scaled(g, gs, w2, s2, part),
+        "all-reduce + norm": lambda: c.all_reduce_norm(part, norm, 1e-5, h[0], h2, y),
+    }
+
+    def layer():
+        for call in calls.values():
+            call()
+
+    def us(call):
+        return round(statistics.median(B.graph_passes(None, None, 0, None, passes=MEDIAN_PASSES,
+                                                      call=call)), 2)
+
+    layer()
+    row = {"ranks": ranks, "tokens": tokens, "hidden": hidden, "mlp": 28672,
+           "us": {name: us(call) for name, call in calls.items()}, "layer_us": us(layer)}
+    row["us"]["down product + all-reduce"] = us(
+        lambda: c.matmul_scaled(g, gs, w2, s2, part, reduce=True))
+    layer()
+    torch.cuda.synchronize()
+    row["finite_and_alike"] = bool(y[0].isfinite().all()) and all(torch.equal(t, y[0]) for t in y)
+    log(f"layer, {tokens} tokens: {row['layer_us']} us; " +
+        "  ".join(f"{k} {v}" for k, v in row["us"].items()))
+    return row
 
 
 def run_hier(B, inputs, cases):
