@@ -261,8 +261,8 @@ arResult_t arMatmulScaled(const void *const *abufs, const float *const *ascales,
     const size_t most = (size_t)1 << 30;
     if (rows > most || n > most)
         return reject(arInvalidArgument, "rows and n must be at most 2^30");
-    if (rows * n > ((size_t)1 << 40))
-        return reject(arInvalidArgument, "rows * n must be at most 2^40");
+    if (rows * n > ((size_t)1 << 38))
+        return reject(arInvalidArgument, "rows * n must be at most 2^38");
     Ranges mem;
     if (!mem.add_ranks(abufs, nranks, rows * k, false) ||
         !mem.add_ranks((const void *const *)ascales, nranks,

@@ -211,7 +211,9 @@ constexpr Choice kChoice32[kChoices - 1] = {
 hipError_t launch_matmul(const MatmulArgs &args, int out_dtype, bool reduce, int cu_count,
                          hipStream_t stream)
 {
-    if (args.rows <= 2) {
+    // (a launch has fewer than 2^32 threads)
+    const double most = 4.0e9;
+    if (args.rows <= 2 && 32.0 * args.n * args.nranks < most) {
         switch (out_dtype) {
         case kBf16: return enqueue_rows<Bf16>(args, reduce, stream);
         case kFp16: return enqueue_rows<Fp16>(args, reduce, stream);
@@ -229,6 +231,8 @@ hipError_t launch_matmul(const MatmulArgs &args, int out_dtype, bool reduce, int
         const double w = (double)(ceil_div(args.rows, c.rows) * ceil_div(args.n, c.cols)) *
                          (reduce ? 1.0 : ranks) / cu_count;
         const double q = ceil(w), s = ceil(steps / c.waves);
+        if (ceil(w) * cu_count * 64.0 * (c.rows == 256u ? 8.0 : c.rows == 128u ? 4.0 : c.waves) > most)
+            continue;
         const double rate = read > 64.0 ? 5.0 * fmin(1.0, 1.3 * w) : 5.0;
         // (what is written is the same for all)
         const double us = c.base + c.each * q +
@@ -238,6 +242,8 @@ hipError_t launch_matmul(const MatmulArgs &args, int out_dtype, bool reduce, int
             best_us = us;
         }
     }
+    if (best == nullptr)
+        return hipErrorInvalidConfiguration;
     if (best->rows >= 128u)
         return launch_matmul_tile(args, out_dtype, reduce, best->rows == 256u, stream);
     return launch_matmul_mid(args, out_dtype, reduce, (int)best->rows / 32, (int)best->cols / 32,

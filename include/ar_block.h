@@ -65,7 +65,10 @@ extern "C" {
  *     y = h / sqrt(mean_i(h^2) + eps) * weight[i]
  *     out_r[t][i] = y, or 8-bit values and scales of y
  *
- * The norm is taken of h before its rounding to the element type.
+ * The norm is taken of h before its rounding to the element type.  The sum of
+ * squares is binary32: a row whose squares overflow it gives zeros, and one
+ * that holds an infinity zeros but NaN at the infinity; a row with a NaN is
+ * NaN, and so is a row of zeros with eps 0.
  *
  *  sendbufs     host array of nranks device pointers, each [rows, cols] dense.
  *  residual     device pointer, [rows, cols] dense: the residual stream, which
@@ -96,7 +99,8 @@ typedef enum { arActNone = 0, arActSiLU = 1 } arActivation_t;
 /* Activation and quantisation, for every rank r:
  *
  *     arActSiLU:  y = g / (1 + exp(-g)) * u, in binary32, with an input row
- *                 holding g in its first `cols` columns and u in the next;
+ *                 holding g in its first `cols` columns and u in the next
+ *                 (0 for g below -87.3);
  *     arActNone:  y = x, an input row holds `cols` columns;
  *     out_r, scales_r = 8-bit values and scales of y.
  *
@@ -119,7 +123,11 @@ arResult_t arGateQuant(const void *const *inbufs, void *const *outbufs, float *c
  *     reduce 1:  out_r = c_0 + .. + c_{R-1}, the same for every rank r
  *
  * with binary32 sums (over k in an order that depends on the shape alone) and
- * one rounding to outDtype.
+ * one rounding to outDtype.  Where outDtype is arFloat32 every product is
+ * exact; for the 16-bit types the matrix instruction adds eight products at a
+ * time after cutting each, toward zero, at 2^-13 of the leading bit of the
+ * largest of them, which on normally distributed values leaves the sums
+ * 1.4e-5 off (the rounding to bfloat16 or float16 leaves 1.7e-3 or 2.1e-4).
  *
  *  abufs, ascales  host arrays of nranks device pointers: activations
  *                  [rows, k] of 8-bit values, dense, and [ceil(k / 128)][rows].
@@ -129,7 +137,7 @@ arResult_t arGateQuant(const void *const *inbufs, void *const *outbufs, float *c
  *  k               a multiple of 16 in 16 .. 2^23 (else arUnsupported).
  *  outDtype        arBfloat16, arFloat16 or arFloat32 (else arUnsupported).
  * Rules (arInvalidArgument when broken): no NULL pointer; every pointer
- * 16-byte aligned; rows and n at most 2^30 and rows * n at most 2^40; no
+ * 16-byte aligned; rows and n at most 2^30 and rows * n at most 2^38; no
  * written range overlaps another written or read one (inputs may be shared
  * between ranks). */
 arResult_t arMatmulScaled(const void *const *abufs, const float *const *ascales,

@@ -22,10 +22,14 @@ def blocks(cols):
 
 
 def assert_within(got, want, tol, what):
-    """Finite values within `tol` of `want`; NaN and infinities in the same places."""
+    """Finite values within `tol` of `want`; NaN and infinities in the same
+    places, and infinities where the value is past the type's largest (half a
+    step above it rounds to infinity)."""
+    largest = torch.finfo(got.dtype).max
     got, want = got.double().cpu(), want.double()
     assert got.shape == want.shape, (what, got.shape, want.shape)
     same = (got == want) | (got.isnan() & want.isnan())
+    same |= got.isinf() & (got.sign() == want.sign()) & (want.abs() + tol > largest)
     bad = ~same & ~((got - want).abs() <= tol)
     if bad.any():
         i = tuple(x[0].item() for x in bad.nonzero(as_tuple=True))
@@ -90,9 +94,10 @@ def gate(x, act):
     return y, y.abs() * (2 * g.abs() + 10) * U
 
 
-def matmul(a, sa, b, sb, dtype):
-    """One rank's product in 64 bits, and its tolerance before the rounding to
-    dtype.
+def matmul(a, sa, b, sb, dtype, columns=None):
+    """One rank's product in 64 bits, its tolerance before the rounding to dtype
+    and what one more addition may lose.  ``columns``: b holds these output
+    columns alone, and sb the row of scales of each.
 
     A float32 output: sums of 128 products and of the blocks in binary32, in
     some order and at worst cut instead of rounded (2 U a step of the sum of
@@ -104,7 +109,8 @@ def matmul(a, sa, b, sb, dtype):
     k, n = a.shape[1], b.shape[0]
     at = torch.arange(k) // 128
     a = a.double() * sa.double()[at].t()
-    b = b.double() * sb.double()[torch.arange(n) // 128][:, at]
+    rows = torch.arange(n) // 128 if columns is None else torch.arange(n)
+    b = b.double() * sb.double()[rows][:, at]
     size = a.abs() @ b.abs().t().contiguous()
     tol = (128 + blocks(k) + 24) * 2 * U * size
     if dtype != torch.float32:

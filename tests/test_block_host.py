@@ -127,6 +127,9 @@ CASES = [
     ("matmul bad reduce", "arMatmulScaled", dict(MM, reduce=2), "arInvalidArgument", "reduce"),
     ("matmul 0 ranks", "arMatmulScaled", dict(MM, nranks=0), "arUnsupported", "nranks"),
     ("matmul rows huge", "arMatmulScaled", dict(MM, rows=(1 << 30) + 1), "arInvalidArgument", "2^30"),
+    ("matmul k huge", "arMatmulScaled", dict(MM, k=(1 << 23) + 16), "arUnsupported", "2^23"),
+    ("matmul output huge", "arMatmulScaled", dict(MM, rows=1 << 20, n=1 << 19), "arInvalidArgument",
+     "2^38"),
     ("matmul NULL a", "arMatmulScaled", dict(MM, abufs=None), "arInvalidArgument", "NULL"),
     ("matmul NULL scale", "arMatmulScaled", dict(MM, bscales=[0, at(7)]), "arInvalidArgument", "NULL"),
     ("matmul misaligned", "arMatmulScaled", dict(MM, outbufs=[at(8) + 4, at(9)]), "arInvalidArgument",

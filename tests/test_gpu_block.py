@@ -308,6 +308,76 @@ def test_matmul_is_repeatable(comm):
             assert torch.equal(one, run_matmul(comm, *args, torch.float32, True)[1].cpu())
 
 
+def test_matmul_subnormal_values(comm):
+    """The smallest 8-bit values, subnormal ones among them, keep their products:
+    small whole multiples of 2^-18, exact in every type that can hold them."""
+    g = torch.Generator("cpu").manual_seed(3)
+    for rows, n, k in ((2, 40, 144), (40, 70, 272), (700, 900, 128)):
+        a = torch.randint(-15, 16, (1, rows, k), generator=g).float() * 2.0 ** -9
+        b = torch.randint(-15, 16, (1, n, k), generator=g).float() * 2.0 ** -9
+        one = [torch.ones((1, ref.blocks(k), rows)), torch.ones((1, ref.blocks(n), ref.blocks(k)))]
+        got = run_matmul(comm, a.to(E4M3), one[0], b.to(E4M3), one[1], torch.float32, False)[0].cpu()
+        assert torch.equal(got.double(), a[0].double() @ b[0].double().t().contiguous())
+
+
+# ---- past 32 bits ------------------------------------------------------------
+def test_norm_past_32_bits(comm):
+    """A message of 2.2e9 elements: rows at both ends and around 2^31 and 2^32
+    bytes."""
+    rows, cols = 135_000, 16_384
+    note(f"norm {rows}x{cols} bf16")
+    x = torch.empty((rows, cols), dtype=torch.bfloat16, device="cuda:0").uniform_(-1, 1)
+    w = torch.ones(cols, dtype=torch.bfloat16, device="cuda:0")
+    q = torch.empty((rows, cols), dtype=E4M3, device="cuda:0")
+    s = torch.empty((ref.blocks(cols), rows), device="cuda:0")
+    h = torch.empty_like(x)
+    comm.all_reduce_norm([x], w, 1e-5, residual_out=[h], out=[q], scales=[s])
+    torch.cuda.synchronize()
+    for row in (0, 65_535, 65_536, 131_071, 131_072, rows - 1):
+        xr = x[row:row + 1].cpu()
+        check_norm(xr[None], None, w.cpu(), 1e-5, [h[row:row + 1]], [q[row:row + 1]],
+                   [s[:, row:row + 1]], f"row {row}")
+
+
+def test_gate_past_32_bits(comm):
+    rows, cols = 140_000, 8192
+    note(f"gate {rows}x{cols} bf16")
+    x = torch.empty((rows, 2 * cols), dtype=torch.bfloat16, device="cuda:0").uniform_(-4, 4)
+    q = torch.empty((rows, cols), dtype=E4M3, device="cuda:0")
+    s = torch.empty((ref.blocks(cols), rows), device="cuda:0")
+    comm.gate_quant([x], [q], [s])
+    torch.cuda.synchronize()
+    for row in (0, 65_536, 131_072, rows - 1):
+        y, tol = ref.gate(x[row:row + 1].cpu(), "silu")
+        check_eight(q[row:row + 1], s[:, row:row + 1], y, tol, f"row {row}")
+
+
+@pytest.mark.parametrize("rows,n,k,dtype", [(140_000, 16_400, 16, "bf16"), (300_000, 64, 8192, "fp16"),
+                                            (300_000, 64, 8192, "bf16"), (40, 300_000, 8192, "bf16"), (1, 300_000, 8192, "fp32")])
+def test_matmul_past_32_bits(comm, rows, n, k, dtype):
+    """Outputs, activations and weights of more than 2^31 bytes."""
+    note(f"matmul {rows}x{n}x{k} {dtype}")
+    g = torch.Generator("cuda").manual_seed(5)
+
+    def values(r):
+        t = torch.empty((r, k), dtype=E4M3, device="cuda:0")
+        for part in t.split(1 << 15):
+            part.copy_(torch.randn(part.shape, generator=g, device="cuda:0").mul_(110).clamp_(-448, 448))
+        return t
+
+    a, b = values(rows), values(n)
+    sa = torch.rand((ref.blocks(k), rows), generator=g, device="cuda:0").add_(0.5)
+    sb = torch.rand((ref.blocks(n), ref.blocks(k)), generator=g, device="cuda:0").add_(0.5)
+    out = torch.empty((rows, n), dtype=DT[dtype], device="cuda:0")
+    comm.matmul_scaled([a], [sa], [b], [sb], [out])
+    torch.cuda.synchronize()
+    ri = torch.tensor(sorted({0, rows // 2, rows - 1}))
+    ni = torch.tensor(sorted({0, n // 2, n - 1}))
+    c, tol, _ = ref.matmul(a[ri.cuda()].cpu(), sa[:, ri.cuda()].cpu(), b[ni.cuda()].cpu(),
+                           sb[(ni // 128).cuda()].cpu(), DT[dtype], columns=ni)
+    ref.assert_within(out[ri.cuda()][:, ni.cuda()], c, ref.rounded(c, tol, DT[dtype]), "corners")
+
+
 # ---- together -------------------------------------------------------------------
 class Layer:
     """The MLP half of a layer over `ranks` ranks: norm, up product, gate, down
