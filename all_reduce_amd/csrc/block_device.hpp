@@ -69,6 +69,22 @@ __device__ inline u32x4 load_some(const char *p, uint32_t n)
     return r;
 }
 
+// A piece without its first `n` elements, zeros behind the others.
+template <typename T>
+__device__ inline u32x4 drop(u32x4 v, uint32_t n)
+{
+    const uint32_t bits = n * 8u * T::kBytes;  // 16 .. 112
+    uint64_t lo = (uint64_t)v[1] << 32 | v[0], hi = (uint64_t)v[3] << 32 | v[2];
+    if (bits >= 64u) {
+        lo = hi >> (bits - 64u);
+        hi = 0;
+    } else {
+        lo = lo >> bits | hi << (64u - bits);
+        hi >>= bits;
+    }
+    return u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
+}
+
 template <typename T>
 __device__ inline void store_some(char *p, u32x4 v, uint32_t n)
 {

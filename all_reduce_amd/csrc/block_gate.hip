@@ -3,18 +3,16 @@
 //
 // Sixteen (binary32: 32) neighbouring lanes hold the 128 columns of a scale,
 // a piece each: the block's largest magnitude is a few lane rotations away,
-// and each value is read once and written once.  A workgroup takes four
-// blocks of 16 rows, so that their scales, next to each other in memory, are
-// written together; all loads are issued before the first is used.  Bound by
-// memory: 4 bytes read and 1 written a value for 16-bit gated inputs.  On
+// and each value is read once and written once.  A workgroup takes 16 rows of
+// one block, or of four, so that their scales, next to each other in memory,
+// are written together; all loads are issued before the first is used.  Bound
+// by memory: 4 bytes read and 1 written a value for 16-bit gated inputs.  On
 // MI355X 8 x 8192 x 3584 bfloat16 takes 195 us (6.0 TB/s; block by block along
 // a row, one load in flight and an IEEE division a value, it took 251).
 #include "block_device.hpp"
 #include "block_internal.hpp"
 
 namespace ar {
-
-constexpr uint32_t kTurns = 4;  // blocks of a group of lanes
 
 // g / (1 + exp(-g)), by exp(-|g|): nothing overflows.  (An exponential below
 // 2^-126 counts as 0: g below -87.3 gives 0.)
@@ -24,9 +22,10 @@ __device__ inline float silu(float g)
     return g * ((g < 0.0f ? e : 1.0f) * __builtin_amdgcn_rcpf(1.0f + e));
 }
 
-// One rank per grid row (blockIdx.y).  A workgroup has 256 / kLanes groups of
-// lanes: `tall` consecutive rows of them side by side in columns.
-template <typename T, bool GATED, bool NT>
+// kTurns: blocks of a group of lanes.  One rank per grid row (blockIdx.y).  A
+// workgroup has 256 / kLanes groups of lanes: `tall` consecutive rows of them
+// side by side in columns.
+template <typename T, bool GATED, bool NT, uint32_t kTurns>
 __global__ __launch_bounds__(256) void gate_quant(GateArgs p)
 {
     constexpr uint32_t E = kPiece<T>, kLanes = AR_SCALE_BLOCK / E, kGroups = 256 / kLanes;
@@ -92,31 +91,38 @@ __global__ __launch_bounds__(256) void gate_quant(GateArgs p)
 
 namespace {
 
-// Non-temporal accesses from 64 MiB moved, as in block_norm.hip.
-template <typename T, bool GATED>
-hipError_t enqueue(GateArgs args, int nranks, int cu_count, hipStream_t stream)
+template <typename T, bool GATED, bool NT, uint32_t TURNS>
+hipError_t enqueue(const GateArgs &args, int nranks, int cu_count, hipStream_t stream)
 {
     constexpr uint32_t kGroups = 256 / (AR_SCALE_BLOCK / kPiece<T>);
-    args.tall = args.rows >= kGroups ? kGroups : 1u;
     const uint64_t blocks = (args.cols + AR_SCALE_BLOCK - 1) / AR_SCALE_BLOCK;
-    const uint64_t each = kGroups / args.tall * kTurns;
+    const uint64_t each = kGroups / args.tall * TURNS;
     uint64_t grid = (args.rows + args.tall - 1) / args.tall * ((blocks + each - 1) / each);
     const uint64_t most = (uint64_t)cu_count * 256;
     grid = grid < most ? grid : most;
-    const uint64_t moved = args.rows * args.cols * nranks * (T::kBytes * (GATED ? 2u : 1u) + 1u);
-    const dim3 g((uint32_t)grid, (uint32_t)nranks);
-    if (moved >= (uint64_t)64 << 20)
-        hipLaunchKernelGGL((gate_quant<T, GATED, true>), g, dim3(256), 0, stream, args);
-    else
-        hipLaunchKernelGGL((gate_quant<T, GATED, false>), g, dim3(256), 0, stream, args);
+    hipLaunchKernelGGL((gate_quant<T, GATED, NT, TURNS>), dim3((uint32_t)grid, (uint32_t)nranks),
+                       dim3(256), 0, stream, args);
     return hipGetLastError();
+}
+
+// Non-temporal accesses from 64 MiB moved, as in block_norm.hip, and four
+// blocks a group of lanes from there on; below, one: the shorter chain counts
+// (8 x 64 x 3584: 4.0 against 4.4 us).
+template <typename T, bool GATED>
+hipError_t sized(GateArgs args, int nranks, int cu_count, hipStream_t stream)
+{
+    constexpr uint32_t kGroups = 256 / (AR_SCALE_BLOCK / kPiece<T>);
+    args.tall = args.rows >= kGroups ? kGroups : 1u;
+    const uint64_t moved = args.rows * args.cols * nranks * (T::kBytes * (GATED ? 2u : 1u) + 1u);
+    return moved >= (uint64_t)64 << 20 ? enqueue<T, GATED, true, 4>(args, nranks, cu_count, stream)
+                                       : enqueue<T, GATED, false, 1>(args, nranks, cu_count, stream);
 }
 
 template <typename T>
 hipError_t pick(const GateArgs &args, bool gated, int nranks, int cu_count, hipStream_t stream)
 {
-    return gated ? enqueue<T, true>(args, nranks, cu_count, stream)
-                 : enqueue<T, false>(args, nranks, cu_count, stream);
+    return gated ? sized<T, true>(args, nranks, cu_count, stream)
+                 : sized<T, false>(args, nranks, cu_count, stream);
 }
 
 }  // namespace

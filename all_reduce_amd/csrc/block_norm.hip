@@ -15,30 +15,39 @@
 // It is bound by memory: R + 1 reads and 2 R writes a column at two or three
 // operations each.  On MI355X 8 x 8192 x 8192 bfloat16 with residual takes
 // 650 us (5.2 TB/s; a large copy runs at 5.1), 16 x 1024 x 7168 float32 with
-// an 8-bit output 211 us (5.1 TB/s).  One row of 8 x 8192 takes 5.2 us (6.0
-// with one workgroup) and 64 rows 7.4 (8.4), bound by a row's chain of loads,
-// sum and stores.
+// an 8-bit output 211 us (5.1 TB/s).  In a graph one row of 8 x 8192 takes
+// 4.4 us (5.5 with one workgroup a row) and 64 rows 7.2, bound by a row's chain
+// of loads, sum and stores.
+#include <type_traits>
+
 #include "block_device.hpp"
 #include "block_internal.hpp"
 
 namespace ar {
 
 // h += the values of `COUNT` ranks from rank `r0` on, in rank order.  Every
-// load is issued before the first addition.
-template <typename T, int V, int COUNT, bool NT>
+// load is issued before the first addition.  `back`: columns that a lane's
+// piece starts early, to end with the row; they are dropped again.
+template <typename T, int V, int COUNT, bool NT, bool RAGGED>
 __device__ inline void add_ranks(const NormArgs &p, uint32_t r0, uint64_t row_at,
-                                 const uint32_t (&col)[V], float (&h)[V][kPiece<T>])
+                                 const uint32_t (&col)[V], const uint32_t (&back)[V],
+                                 float (&h)[V][kPiece<T>])
 {
     u32x4 x[V][COUNT];
 #pragma unroll
     for (int v = 0; v < V; ++v)
-        if (col[v] + kPiece<T> <= p.cols)
+        if (col[v] < p.cols)
 #pragma unroll
             for (int j = 0; j < COUNT; ++j)
-                x[v][j] = load_piece<NT>(p.send[r0 + j] + (row_at + col[v]) * T::kBytes);
+                x[v][j] = load_piece<NT>(p.send[r0 + j] +
+                                         (row_at + col[v] - (RAGGED ? back[v] : 0u)) * T::kBytes);
 #pragma unroll
     for (int v = 0; v < V; ++v)
-        if (col[v] + kPiece<T> <= p.cols)
+        if (col[v] < p.cols) {
+            if (RAGGED && back[v] != 0)
+#pragma unroll
+                for (int j = 0; j < COUNT; ++j)
+                    x[v][j] = drop<T>(x[v][j], back[v]);
 #pragma unroll
             for (int j = 0; j < COUNT; ++j) {
                 float f[kPiece<T>];
@@ -47,11 +56,13 @@ __device__ inline void add_ranks(const NormArgs &p, uint32_t r0, uint64_t row_at
                 for (int e = 0; e < kPiece<T>; ++e)
                     h[v][e] = h[v][e] + f[e];
             }
+        }
 }
 
 // V: pieces a lane holds (lane i holds pieces i, i + threads, ..).  EIGHT:
-// 8-bit output with scales.  NT: non-temporal accesses.
-template <typename T, int V, bool EIGHT, bool NT>
+// 8-bit output with scales.  NT: non-temporal accesses.  RAGGED: cols is not a
+// multiple of a piece's.
+template <typename T, int V, bool EIGHT, bool NT, bool RAGGED>
 __global__ __launch_bounds__(1024) void norm_rows(NormArgs p)
 {
     constexpr uint32_t E = kPiece<T>;
@@ -64,15 +75,28 @@ __global__ __launch_bounds__(1024) void norm_rows(NormArgs p)
     touch(p.res_out);
     touch(p.out);
     touch(p.scales);
-    uint32_t col[V];
+    // A row's last columns, fewer than a piece, are read with a piece that
+    // starts early (one load like the others'; element by element, rank after
+    // rank, 3 x 333 x 5001 took 7.5 us); a row that is shorter than a piece is
+    // read by elements.
+    const bool tiny = RAGGED && p.cols < E;
+    uint32_t col[V], back[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v)
+    for (int v = 0; v < V; ++v) {
         col[v] = (v * blockDim.x + threadIdx.x) * E;
-    auto load_weight = [&](int v) {
-        const char *at = p.weight + (uint64_t)col[v] * T::kBytes;
-        if (col[v] + E <= p.cols)
-            return load_piece<false>(at);
-        return col[v] < p.cols ? load_some<T>(at, p.cols - col[v]) : u32x4{0, 0, 0, 0};
+        back[v] = RAGGED && col[v] < p.cols && col[v] + E > p.cols && !tiny ? col[v] + E - p.cols : 0u;
+    }
+    auto load_at = [&](auto nt, const char *row, int v) {
+        if (tiny)
+            return col[v] < p.cols ? load_some<T>(row, p.cols) : u32x4{0, 0, 0, 0};
+        if (col[v] >= p.cols)
+            return u32x4{0, 0, 0, 0};
+        const u32x4 x = load_piece<decltype(nt)::value>(row + (uint64_t)(col[v] - back[v]) * T::kBytes);
+        return back[v] != 0 ? drop<T>(x, back[v]) : x;
+    };
+    auto load_weight = [&](int v) { return load_at(std::false_type{}, p.weight, v); };
+    auto load_residual = [&](uint64_t row_at, int v) {
+        return load_at(std::integral_constant<bool, NT>{}, p.residual + row_at * T::kBytes, v);
     };
     // The weights are loaded here, and a row's residual before its sum, so that
     // a single row does not wait for them one after the other; a lane with
@@ -100,54 +124,48 @@ __global__ __launch_bounds__(1024) void norm_rows(NormArgs p)
 #pragma unroll
             for (uint32_t e = 0; e < E; ++e)
                 h[v][e] = -0.0f;
-            if (kEarly && p.residual != nullptr && col[v] + E <= p.cols)
-                res[v] = load_piece<NT>(p.residual + (row_at + col[v]) * T::kBytes);
+            if (kEarly && p.residual != nullptr)
+                res[v] = load_residual(row_at, v);
         }
-        uint32_t r = 0;
+        uint32_t r = tiny ? p.nranks : 0u;
         for (; r + kBatch <= p.nranks; r += kBatch)
-            add_ranks<T, V, kBatch, NT>(p, r, row_at, col, h);
+            add_ranks<T, V, kBatch, NT, RAGGED>(p, r, row_at, col, back, h);
         if constexpr (kBatch > 4) {
-            if (p.nranks & 4u) {
-                add_ranks<T, V, 4, NT>(p, r, row_at, col, h);
+            if (p.nranks & 4u && !tiny) {
+                add_ranks<T, V, 4, NT, RAGGED>(p, r, row_at, col, back, h);
                 r += 4u;
             }
         }
         if constexpr (kBatch > 2) {
-            if (p.nranks & 2u) {
-                add_ranks<T, V, 2, NT>(p, r, row_at, col, h);
+            if (p.nranks & 2u && !tiny) {
+                add_ranks<T, V, 2, NT, RAGGED>(p, r, row_at, col, back, h);
                 r += 2u;
             }
         }
         if constexpr (kBatch > 1) {
-            if (p.nranks & 1u)
-                add_ranks<T, V, 1, NT>(p, r, row_at, col, h);
+            if (p.nranks & 1u && !tiny)
+                add_ranks<T, V, 1, NT, RAGGED>(p, r, row_at, col, back, h);
         }
         float sq = 0.0f;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            if (col[v] + E <= p.cols) {
-                if (p.residual != nullptr) {
+            if (tiny && col[v] < p.cols) {
+                for (uint32_t q = 0; q < p.nranks; ++q) {
                     float f[E];
-                    if constexpr (!kEarly)
-                        res[v] = load_piece<NT>(p.residual + (row_at + col[v]) * T::kBytes);
-                    widen_piece<T>(res[v], f);
+                    widen_piece<T>(load_some<T>(p.send[q] + row_at * T::kBytes, p.cols), f);
 #pragma unroll
                     for (uint32_t e = 0; e < E; ++e)
                         h[v][e] = h[v][e] + f[e];
                 }
-            } else if (col[v] < p.cols) {
-                // the row's last columns, fewer than a piece
-                for (uint32_t q = 0; q <= p.nranks; ++q) {
-                    const char *from = q < p.nranks ? p.send[q] : p.residual;
-                    if (from == nullptr)
-                        break;
-                    float f[E];
-                    widen_piece<T>(load_some<T>(from + (row_at + col[v]) * T::kBytes, p.cols - col[v]),
-                                   f);
+            }
+            if (p.residual != nullptr) {
+                float f[E];
+                if constexpr (!kEarly)
+                    res[v] = load_residual(row_at, v);
+                widen_piece<T>(res[v], f);
 #pragma unroll
-                    for (uint32_t e = 0; e < E; ++e)
-                        h[v][e] = h[v][e] + f[e];
-                }
+                for (uint32_t e = 0; e < E; ++e)
+                    h[v][e] = h[v][e] + f[e];
             }
             // (columns past the row hold -0 or 0 and add nothing)
 #pragma unroll
@@ -166,7 +184,7 @@ __global__ __launch_bounds__(1024) void norm_rows(NormArgs p)
         const float inv = 1.0f / __builtin_sqrtf(total / (float)p.cols + p.eps);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const bool full = col[v] + E <= p.cols;
+            const bool full = !RAGGED || col[v] + E <= p.cols;
             const uint32_t n = col[v] < p.cols ? p.cols - col[v] : 0u;
             const uint64_t at = row_at + col[v];
             if (p.has_res_out != 0 && n != 0) {
@@ -184,7 +202,7 @@ __global__ __launch_bounds__(1024) void norm_rows(NormArgs p)
             widen_piece<T>(weight[v], f);
 #pragma unroll
             for (uint32_t e = 0; e < E; ++e)
-                y[e] = full || e < n ? h[v][e] * inv * f[e] : 0.0f;
+                y[e] = (RAGGED ? e < n : n != 0) ? h[v][e] * inv * f[e] : 0.0f;
             if constexpr (EIGHT) {
                 // all lanes of a scale take part; those past the row hold 0
                 const float s = scale_of(max_block<T>(max_bits(y)));
@@ -215,16 +233,23 @@ __global__ __launch_bounds__(1024) void norm_rows(NormArgs p)
 
 namespace {
 
-template <typename T, int V, bool EIGHT>
-hipError_t enqueue(const NormArgs &args, uint32_t threads, bool nt, hipStream_t stream)
+template <typename T, int V, bool EIGHT, bool NT>
+hipError_t enqueue(const NormArgs &args, uint32_t threads, hipStream_t stream)
 {
     const uint64_t rows = args.rows < (1u << 20) ? args.rows : (1u << 20);
     const uint32_t grid = (uint32_t)((rows + 7u) / 8u * 8u * args.split);
-    if (nt)
-        hipLaunchKernelGGL((norm_rows<T, V, EIGHT, true>), dim3(grid), dim3(threads), 0, stream, args);
+    if (args.cols % kPiece<T> != 0)
+        hipLaunchKernelGGL((norm_rows<T, V, EIGHT, NT, true>), dim3(grid), dim3(threads), 0, stream, args);
     else
-        hipLaunchKernelGGL((norm_rows<T, V, EIGHT, false>), dim3(grid), dim3(threads), 0, stream, args);
+        hipLaunchKernelGGL((norm_rows<T, V, EIGHT, NT, false>), dim3(grid), dim3(threads), 0, stream, args);
     return hipGetLastError();
+}
+
+template <typename T, int V, bool EIGHT>
+hipError_t enqueue(const NormArgs &args, uint32_t threads, bool nt, hipStream_t stream)
+{
+    return nt ? enqueue<T, V, EIGHT, true>(args, threads, stream)
+              : enqueue<T, V, EIGHT, false>(args, threads, stream);
 }
 
 // As many lanes a row as it has pieces where rows are few (the pieces' loads
