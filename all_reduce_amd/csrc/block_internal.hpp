@@ -47,6 +47,7 @@ struct MatmulArgs {
     uint32_t k;
     uint32_t kblocks;  // ceil(k / 128)
     uint32_t nranks;
+    uint32_t split;    // workgroups that share a tile's k (the launcher sets it)
 };
 
 // Launchers: validate nothing (the entry points did), pick the kernel and
@@ -60,10 +61,15 @@ hipError_t launch_matmul(const MatmulArgs &args, int out_dtype, bool reduce, int
 // Its kernels for a batch of rows (block_matmul_mid.hip; mt, nt: tiles of 32
 // rows and columns, 1 and 1, 2 and 1 or 2 and 2) and for many
 // (block_matmul_tile.hip; tiles of 256 x 256 or 128 x 128).  Their 32-bit
-// offsets inside a tile limit k.
+// offsets inside a tile limit k.  `split` > 1: that many workgroups share the k
+// of a tile, in the summed form only, and at most matmul_most_split of them.
 constexpr uint32_t kMatmulMaxK = 1u << 23;
+inline uint32_t matmul_most_split(int out_dtype, uint32_t nranks)
+{
+    return out_dtype == kFp32 ? nranks : nranks / 2u > 0u ? nranks / 2u : 1u;
+}
 hipError_t launch_matmul_mid(const MatmulArgs &args, int out_dtype, bool reduce, int mt, int nt,
-                             uint32_t waves, hipStream_t stream);
+                             uint32_t waves, uint32_t split, hipStream_t stream);
 hipError_t launch_matmul_tile(const MatmulArgs &args, int out_dtype, bool reduce, bool large,
                               hipStream_t stream);
 

@@ -167,7 +167,7 @@ uint64_t ceil_div(uint64_t a, uint64_t b) { return (a + b - 1) / b; }
 // The kernels for three rows and more: tiles of rows x columns whose `waves`
 // share k, `resident` workgroups to a compute unit, and the time they take (us)
 //
-//     base + each * Q + MB written / 3
+//     base + each * Q + MB written / 4
 //          + max(alone * ceil(Q / resident) * S, full * W * S, MB read / rate)
 //
 // for Q = ceil(W) workgroups a compute unit (W of them on average) of S steps
@@ -175,11 +175,16 @@ uint64_t ceil_div(uint64_t a, uint64_t b) { return (a + b - 1) / b; }
 // compute unit and `full` a workgroup where it is filled; the rate is 5 MB/us,
 // less where inputs that no cache keeps (from 64 MB) have to come through a
 // part of the compute units (64 x 8192 x 8 x 3584 summed: 58 us with one
-// workgroup a compute unit, 77 with one on every second).  The numbers were
-// fitted to 700 measured shapes on MI355X (3 to 8192 rows, 64 to 8192 columns,
-// k 128 to 8192, 1 to 8 ranks, each rank's product and the sum; 10 to 17 % off
-// in the mean): the kernel chosen by them takes 1.02 times the fastest one's
-// time in the mean.  What they tell apart, for example (us, bfloat16 out):
+// workgroup a compute unit, 77 with one on every second) or where most of a
+// tile's rows are past the last one.  In a summed form workgroups may share a
+// tile's k too (block_matmul_mid.hip), at the price of a second kernel.
+//
+// The numbers were fitted to 900 measured shapes on MI355X (3 to 8192 rows, 64
+// to 8192 columns, k 128 to 8192, 1 to 8 ranks, each rank's product and the
+// sum; 8 to 19 % off in the mean): the kernel chosen by them takes 1.03 times
+// the fastest one's time in the mean, over 300 other shapes and with k shared
+// among workgroups 1.05 times.  What they tell apart, for example (us, bfloat16
+// out):
 //
 //                                    64x32   64x64   128x128  256x256
 //     1 rank,    64 x 8192 x 8192     14      17       52       85
@@ -196,50 +201,61 @@ struct Choice {
 
 constexpr int kChoices = 9;
 constexpr Choice kChoice16[kChoices] = {
-    {32, 32, 8, 1, 2.29f, 0.67f, 1.13f, 0.86f}, {32, 32, 4, 2, 3.47f, 0.39f, 0.57f, 0.0f},
-    {32, 32, 2, 4, 3.35f, 0.37f, 0.30f, 0.0f},  {64, 32, 4, 1, 2.47f, 0.56f, 0.93f, 1.32f},
-    {64, 32, 2, 3, 3.75f, 0.50f, 0.51f, 0.0f},  {64, 64, 4, 1, 2.54f, 0.84f, 1.22f, 2.07f},
-    {64, 64, 2, 2, 4.29f, 0.70f, 0.68f, 0.63f}, {128, 128, 1, 2, 3.27f, 0.73f, 0.64f, 0.0f},
-    {256, 256, 1, 1, 4.80f, 1.38f, 1.38f, 0.0f}};
+    {32, 32, 8, 1, 2.40f, 0.71f, 1.19f, 1.05f}, {32, 32, 4, 2, 3.15f, 0.43f, 0.54f, 0.27f},
+    {32, 32, 2, 4, 3.33f, 0.37f, 0.31f, 0.0f},  {64, 32, 4, 1, 2.53f, 0.60f, 0.98f, 1.33f},
+    {64, 32, 2, 3, 3.79f, 0.49f, 0.53f, 0.0f},  {64, 64, 4, 1, 2.95f, 0.84f, 1.30f, 1.83f},
+    {64, 64, 2, 2, 4.40f, 0.68f, 0.71f, 0.29f}, {128, 128, 1, 2, 3.92f, 0.81f, 0.70f, 0.0f},
+    {256, 256, 1, 1, 4.65f, 1.40f, 1.40f, 0.78f}};
 // With exact products; 256 x 256 tiles have no registers left for those.
 constexpr Choice kChoice32[kChoices - 1] = {
-    {32, 32, 8, 1, 2.37f, 0.81f, 1.19f, 1.11f}, {32, 32, 4, 2, 3.23f, 0.52f, 0.56f, 0.34f},
-    {32, 32, 2, 4, 3.41f, 0.52f, 0.33f, 0.04f}, {64, 32, 4, 1, 2.19f, 0.74f, 0.98f, 1.76f},
-    {64, 32, 2, 3, 3.90f, 0.67f, 0.60f, 0.12f}, {64, 64, 4, 1, 2.17f, 1.19f, 1.37f, 2.69f},
-    {64, 64, 2, 2, 4.22f, 1.07f, 0.81f, 1.03f}, {128, 128, 1, 2, 3.74f, 1.11f, 0.67f, 0.0f}};
+    {32, 32, 8, 1, 2.45f, 0.85f, 1.24f, 1.10f}, {32, 32, 4, 2, 3.29f, 0.52f, 0.57f, 0.23f},
+    {32, 32, 2, 4, 3.39f, 0.49f, 0.33f, 0.0f},  {64, 32, 4, 1, 2.61f, 0.72f, 1.03f, 1.37f},
+    {64, 32, 2, 3, 3.71f, 0.66f, 0.58f, 0.0f},  {64, 64, 4, 1, 2.35f, 1.20f, 1.37f, 2.31f},
+    {64, 64, 2, 2, 4.07f, 1.06f, 0.81f, 0.48f}, {128, 128, 1, 2, 4.22f, 1.21f, 0.81f, 0.0f}};
 
 hipError_t launch_matmul(const MatmulArgs &args, int out_dtype, bool reduce, int cu_count,
                          hipStream_t stream)
 {
     // (a launch has fewer than 2^32 threads)
     const double most = 4.0e9;
-    if (args.rows <= 2 && 32.0 * args.n * args.nranks < most) {
+    const bool exact = out_dtype == kFp32;
+    const Choice *choices = exact ? kChoice32 : kChoice16;
+    const Choice *best = nullptr;
+    uint32_t best_split = 1;
+    double best_us = 0.0;
+    const double ranks = args.nranks, steps = (double)args.kblocks * (reduce ? ranks : 1.0);
+    const double read = ((double)args.rows + args.n) * args.k * ranks * 1e-6;
+    // (what is written is the same for all, but that sums are read again)
+    const double join = 3.0 + (double)args.rows * args.n * ranks * (exact ? 4.0 : 2.0) * 0.1e-6;
+    const uint32_t splits = reduce ? matmul_most_split(out_dtype, args.nranks) : 1u;
+    for (int i = 0; i < (exact ? kChoices - 1 : kChoices); ++i) {
+        const Choice &c = choices[i];
+        const double tiles = (double)(ceil_div(args.rows, c.rows) * ceil_div(args.n, c.cols)) *
+                             (reduce ? 1.0 : ranks);
+        for (uint32_t split = 1; split <= (c.rows < 128u ? splits : 1u); split *= 2u) {
+            const double w = tiles * split / cu_count, q = ceil(w);
+            const double s = ceil(steps / (c.waves * split));
+            if (q * cu_count * 64.0 * (c.rows == 256u ? 8.0 : c.rows == 128u ? 4.0 : c.waves) > most)
+                continue;
+            const double rate = (read > 64.0 ? 5.0 * fmin(1.0, 1.3 * w) : 5.0) *
+                                fmin(1.0, 0.5 + (double)args.rows / c.rows);
+            const double us = c.base + c.each * q + (split > 1u ? join : 0.0) +
+                              fmax(fmax(c.alone * ceil(q / c.resident) * s, c.full * w * s), read / rate);
+            if (best == nullptr || us < best_us) {
+                best = &c;
+                best_split = split;
+                best_us = us;
+            }
+        }
+    }
+    // One or two rows take the kernel made for them, unless sharing k among
+    // workgroups wins (8 x (1 x 512 x 8192) summed, for example: 14 in place of
+    // 39 us).
+    if (args.rows <= 2 && best_split == 1u && 32.0 * args.n * args.nranks < most) {
         switch (out_dtype) {
         case kBf16: return enqueue_rows<Bf16>(args, reduce, stream);
         case kFp16: return enqueue_rows<Fp16>(args, reduce, stream);
         default: return enqueue_rows<Fp32>(args, reduce, stream);
-        }
-    }
-    const bool exact = out_dtype == kFp32;
-    const Choice *choices = exact ? kChoice32 : kChoice16;
-    const Choice *best = nullptr;
-    double best_us = 0.0;
-    const double ranks = args.nranks, steps = (double)args.kblocks * (reduce ? ranks : 1.0);
-    const double read = ((double)args.rows + args.n) * args.k * ranks * 1e-6;
-    for (int i = 0; i < (exact ? kChoices - 1 : kChoices); ++i) {
-        const Choice &c = choices[i];
-        const double w = (double)(ceil_div(args.rows, c.rows) * ceil_div(args.n, c.cols)) *
-                         (reduce ? 1.0 : ranks) / cu_count;
-        const double q = ceil(w), s = ceil(steps / c.waves);
-        if (ceil(w) * cu_count * 64.0 * (c.rows == 256u ? 8.0 : c.rows == 128u ? 4.0 : c.waves) > most)
-            continue;
-        const double rate = read > 64.0 ? 5.0 * fmin(1.0, 1.3 * w) : 5.0;
-        // (what is written is the same for all)
-        const double us = c.base + c.each * q +
-                          fmax(fmax(c.alone * ceil(q / c.resident) * s, c.full * w * s), read / rate);
-        if (best == nullptr || us < best_us) {
-            best = &c;
-            best_us = us;
         }
     }
     if (best == nullptr)
@@ -247,7 +263,7 @@ hipError_t launch_matmul(const MatmulArgs &args, int out_dtype, bool reduce, int
     if (best->rows >= 128u)
         return launch_matmul_tile(args, out_dtype, reduce, best->rows == 256u, stream);
     return launch_matmul_mid(args, out_dtype, reduce, (int)best->rows / 32, (int)best->cols / 32,
-                             best->waves, stream);
+                             best->waves, best_split, stream);
 }
 
 }  // namespace ar

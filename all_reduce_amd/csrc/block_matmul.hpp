@@ -89,7 +89,7 @@ __device__ inline i32x8 pieces(const char *base, uint32_t at)
 
 // 16 bytes a lane from base + off to LDS at `to` + 16 * lane (`base` and `to`
 // are the same in every lane).  The compiler does not see the load: whoever
-// reads the bytes waits for vmcnt(0) first.
+// reads the bytes waits for vmcnt first.  (It never keeps a value in m0.)
 __device__ inline void to_lds(const char *base, uint32_t off, uint32_t to)
 {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"

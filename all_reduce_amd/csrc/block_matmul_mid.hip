@@ -11,6 +11,15 @@
 // but their own loads until their sums are added, in wave order, at the end.
 //
 // Tiles are 32x32 (see block_matmul_tile.hip for the layout in LDS).
+//
+// Where a sum over the ranks has few tiles, p.split workgroups share a tile's
+// k as well, and a second kernel adds their binary32 sums in order.  These lie
+// in the output buffers until then, which are as many as there are ranks:
+// workgroup s's sum of an element is where the element goes in buffer s, or
+// for 16-bit outputs in two halves in buffers 2 s and 2 s + 1.  A lane of the
+// second kernel reads all sums of its elements before it writes any, and no
+// other lane touches them.  (8 x (91 x 66 x 6224), float32: 15 us in place of
+// 58.)
 #include <type_traits>
 
 #include "block_device.hpp"
@@ -29,6 +38,101 @@ struct MidPlace {
     static constexpr int kLoads = (MT + NT) * 4 + MT / 2 + 1;
 };
 
+// Eight consecutive columns of a row, `left` of them to its end.
+template <typename T>
+__device__ inline void store8(char *to, const float (&c)[8], uint32_t left)
+{
+    constexpr uint32_t E = kPiece<T>;
+#pragma unroll
+    for (uint32_t i = 0; i < 8u / E; ++i) {
+        float f[E];
+#pragma unroll
+        for (uint32_t e = 0; e < E; ++e)
+            f[e] = c[i * E + e];
+        if (left > i * E)
+            store_row_piece<T>(to + i * 16u, narrow_piece<T>(f), left - i * E);
+    }
+}
+
+// Workgroup `part`'s sums of them, to wait in the outputs.
+template <typename T>
+__device__ inline void store_part(const MatmulArgs &p, uint32_t part, uint64_t at, uint32_t left,
+                                  const float (&c)[8])
+{
+    if constexpr (T::kBytes == 4) {
+        store8<T>(p.out[part] + at * 4u, c, left);
+    } else {
+        u32x4 hi, lo;
+#pragma unroll
+        for (uint32_t i = 0; i < 4; ++i) {
+            const uint32_t x = __builtin_bit_cast(uint32_t, c[2 * i]);
+            const uint32_t y = __builtin_bit_cast(uint32_t, c[2 * i + 1]);
+            hi[i] = x >> 16 | (y & 0xffff0000u);
+            lo[i] = (x & 0xffffu) | y << 16;
+        }
+        store_row_piece<T>(p.out[2u * part] + at * 2u, hi, left);
+        store_row_piece<T>(p.out[2u * part + 1u] + at * 2u, lo, left);
+    }
+}
+
+// Adds the workgroups' sums of a piece of the outputs (ONE: of one element),
+// in order, and stores the result to all ranks.
+template <typename T, bool ONE>
+__device__ inline void join(const MatmulArgs &p, uint64_t at)
+{
+    constexpr uint32_t E = ONE ? 1 : kPiece<T>;
+    constexpr uint32_t kParts = T::kBytes == 4 ? 1 : 2;
+    auto load = [&](uint32_t o) {
+        const char *from = p.out[o] + at * T::kBytes;
+        return ONE ? load_some<T>(from, 1) : load_piece<false>(from);
+    };
+    float sum[kPiece<T>] = {};
+    // (splits are powers of two: four at a time, loaded before any is added)
+    for (uint32_t s = 0; s < p.split; s += 4u) {
+        u32x4 v[4][kParts];
+#pragma unroll
+        for (uint32_t u = 0; u < 4; ++u)
+            if (s + u < p.split)
+#pragma unroll
+                for (uint32_t h = 0; h < kParts; ++h)
+                    v[u][h] = load((s + u) * kParts + h);
+#pragma unroll
+        for (uint32_t u = 0; u < 4; ++u)
+            if (s + u < p.split)
+#pragma unroll
+                for (uint32_t e = 0; e < E; ++e) {
+                    uint32_t b;
+                    if constexpr (kParts == 1)
+                        b = v[u][0][e];
+                    else
+                        b = (v[u][0][e / 2u] >> 16u * (e % 2u)) << 16 |
+                            (v[u][kParts - 1][e / 2u] >> 16u * (e % 2u) & 0xffffu);
+                    sum[e] = sum[e] + __builtin_bit_cast(float, b);
+                }
+    }
+    const u32x4 y = narrow_piece<T>(sum);
+    for (uint32_t o = 0; o < p.nranks; ++o) {
+        char *to = p.out[o] + at * T::kBytes;
+        if constexpr (ONE)
+            store_some<T>(to, y, 1);
+        else
+            store_piece<false>(to, y);
+    }
+}
+
+// All pieces, and one by one the elements after the last whole one.
+template <typename T>
+__global__ __launch_bounds__(256) void matmul_join(MatmulArgs p)
+{
+    constexpr uint32_t E = kPiece<T>;
+    const uint64_t count = (uint64_t)p.rows * p.n, pieces = count / E;
+    for (uint64_t i = (uint64_t)blockIdx.x * 256u + threadIdx.x; i < pieces;
+         i += (uint64_t)gridDim.x * 256u)
+        join<T, false>(p, i * E);
+    if (blockIdx.x == gridDim.x - 1u && threadIdx.x < count % E)
+        join<T, true>(p, pieces * E + threadIdx.x);
+}
+
 template <typename T, int MT, int NT, int D, bool REDUCE>
 __global__ __launch_bounds__(512) void matmul_mid(MatmulArgs p)
 {
@@ -44,13 +148,15 @@ __global__ __launch_bounds__(512) void matmul_mid(MatmulArgs p)
     // Workgroup w runs on XCD w % 8: each XCD takes consecutive tiles, rows
     // first, so that the row tiles of the same weights meet in one cache.
     const uint32_t mtiles = (p.rows + kRows - 1) / kRows, ntiles = (p.n + kCols - 1) / kCols;
-    const uint32_t tiles = mtiles * ntiles * (REDUCE ? 1u : p.nranks);
+    const uint32_t tiles = mtiles * ntiles * (REDUCE ? p.split : p.nranks);
     const uint32_t each = (tiles + 7u) / 8u;
     const uint32_t tile = (blockIdx.x & 7u) * each + blockIdx.x / 8u;
     if (blockIdx.x / 8u >= each || tile >= tiles)
         return;
     const uint32_t m0 = tile % mtiles * kRows, n0 = tile / mtiles % ntiles * kCols;
     const uint32_t rank0 = REDUCE ? 0u : tile / (mtiles * ntiles);
+    const uint32_t part = REDUCE ? tile / (mtiles * ntiles) : 0u;
+    const uint32_t first = part * waves + wave, stride = REDUCE ? p.split * waves : waves;
     const uint32_t nranks = REDUCE ? p.nranks : 1u;
 
     // Rows and columns past the end repeat the last one, and what comes of
@@ -88,7 +194,7 @@ __global__ __launch_bounds__(512) void matmul_mid(MatmulArgs p)
             ++at.r;
         }
     };
-    At next = {0, wave};
+    At next = {0, first};
     normal(next);
     uint32_t known = ~0u;  // the rank that these belong to
     const char *a = nullptr, *b = nullptr;
@@ -122,18 +228,18 @@ __global__ __launch_bounds__(512) void matmul_mid(MatmulArgs p)
                 to_lds4(s + offs[i], to + Place::kScales + i * 256u);
             to_lds4((const char *)(sb + next.kb), to + Place::kScales + MT * 128u);
         }
-        next.kb += waves;
+        next.kb += stride;
         normal(next);
     };
 
     const uint32_t place = l32 * 128u + ((half * 2u) ^ (l32 >> 1 & 7u)) * 16u;
     f32x16 acc[NT][MT] = {};
     const uint32_t blocks = p.kblocks * nranks;
-    const uint32_t steps = wave < blocks ? (blocks - wave + waves - 1u) / waves : 0u;
+    const uint32_t steps = first < blocks ? (blocks - first + stride - 1u) / stride : 0u;
     uint32_t issued = 0, slot_in = 0, slot_out = 0;
     for (; issued < D - 1u && issued < steps; ++issued)
         load(slot_in++);
-    At now = {0, wave};
+    At now = {0, first};
     normal(now);
     for (uint32_t step = 0; step < steps; ++step) {
         if (issued < steps) {
@@ -147,7 +253,7 @@ __global__ __launch_bounds__(512) void matmul_mid(MatmulArgs p)
         const char *at = lds + ring + slot_out * Place::kBytes;
         slot_out = slot_out + 1u == D ? 0u : slot_out + 1u;
         const uint32_t left = p.k - now.kb * 128u;
-        now.kb += waves;
+        now.kb += stride;
         normal(now);
         i32x8 x[MT][2];
         float s[MT];
@@ -188,30 +294,35 @@ __global__ __launch_bounds__(512) void matmul_mid(MatmulArgs p)
 
     // The waves' sums: [wave][tile][16][64] floats in LDS, added in wave order.
     __syncthreads();
-    float *part = (float *)lds;
+    float *sums = (float *)lds;
 #pragma unroll
     for (uint32_t i = 0; i < NT; ++i)
 #pragma unroll
         for (uint32_t j = 0; j < MT; ++j)
 #pragma unroll
             for (uint32_t e = 0; e < 16; ++e)
-                part[(((wave * NT + i) * MT + j) * 16u + e) * 64u + lane] = acc[i][j][e];
+                sums[(((wave * NT + i) * MT + j) * 16u + e) * 64u + lane] = acc[i][j][e];
     __syncthreads();
-    // four consecutive columns of a row each (elements 4 q .. 4 q + 3 of a tile)
-    for (uint32_t it = wave; it < NT * MT * 4; it += waves) {
-        const uint32_t q = it & 3u, j = it / 4u % MT, i = it / 4u / MT;
-        f32x4 c = {};
+    // Eight consecutive columns of a row each: elements 4 q .. 4 q + 3 of a
+    // tile, of both halves of the wave.
+    for (uint32_t it = threadIdx.x; it < NT * MT * 128u; it += blockDim.x) {
+        const uint32_t t = it / 128u, r32 = it / 4u % 32u, q = it & 3u;
+        float c[8] = {};
         for (uint32_t w = 0; w < waves; ++w)
 #pragma unroll
-            for (uint32_t e = 0; e < 4; ++e)
-                c[e] += part[(((w * NT + i) * MT + j) * 16u + q * 4u + e) * 64u + lane];
-        const uint32_t row = m0 + j * 32u + l32, col = n0 + i * 32u + q * 8u + half * 4u;
+            for (uint32_t e = 0; e < 8; ++e)
+                c[e] += sums[((w * (NT * MT) + t) * 16u + q * 4u + e % 4u) * 64u + e / 4u * 32u + r32];
+        const uint32_t row = m0 + t % MT * 32u + r32, col = n0 + t / MT * 32u + q * 8u;
         if (row < p.rows && col < p.n) {
+            const uint64_t at = (uint64_t)row * p.n + col;
             if constexpr (REDUCE) {
-                for (uint32_t o = 0; o < p.nranks; ++o)
-                    store4<T>(p.out[o], row, p.n, col, c);
+                if (p.split > 1u)
+                    store_part<T>(p, part, at, p.n - col, c);
+                else
+                    for (uint32_t o = 0; o < p.nranks; ++o)
+                        store8<T>(p.out[o] + at * T::kBytes, c, p.n - col);
             } else {
-                store4<T>(p.out[rank0], row, p.n, col, c);
+                store8<T>(p.out[rank0] + at * T::kBytes, c, p.n - col);
             }
         }
     }
@@ -226,7 +337,8 @@ hipError_t enqueue_mid(const MatmulArgs &args, uint32_t waves, bool reduce, hipS
     const size_t part = (size_t)waves * NT * MT * 4096u;
     const size_t lds = ring > part ? ring : part;
     const uint32_t tiles = (args.rows + MT * 32u - 1) / (MT * 32u) *
-                           ((args.n + NT * 32u - 1) / (NT * 32u)) * (reduce ? 1u : args.nranks);
+                           ((args.n + NT * 32u - 1) / (NT * 32u)) *
+                           (reduce ? args.split : args.nranks);
     const dim3 grid((tiles + 7u) / 8u * 8u);
     if (reduce)
         hipLaunchKernelGGL((matmul_mid<T, MT, NT, D, true>), grid, dim3(waves * 64), lds, stream, args);
@@ -248,14 +360,27 @@ hipError_t pick_mid(const MatmulArgs &args, bool reduce, int mt, int nt, uint32_
 
 }  // namespace
 
-hipError_t launch_matmul_mid(const MatmulArgs &args, int out_dtype, bool reduce, int mt, int nt,
-                             uint32_t waves, hipStream_t stream)
+hipError_t launch_matmul_mid(const MatmulArgs &given, int out_dtype, bool reduce, int mt, int nt,
+                             uint32_t waves, uint32_t split, hipStream_t stream)
 {
+    MatmulArgs args = given;
+    args.split = split;
+    hipError_t e;
     switch (out_dtype) {
-    case kBf16: return pick_mid<Bf16>(args, reduce, mt, nt, waves, stream);
-    case kFp16: return pick_mid<Fp16>(args, reduce, mt, nt, waves, stream);
-    default: return pick_mid<Fp32>(args, reduce, mt, nt, waves, stream);
+    case kBf16: e = pick_mid<Bf16>(args, reduce, mt, nt, waves, stream); break;
+    case kFp16: e = pick_mid<Fp16>(args, reduce, mt, nt, waves, stream); break;
+    default: e = pick_mid<Fp32>(args, reduce, mt, nt, waves, stream); break;
     }
+    if (e != hipSuccess || split == 1u)
+        return e;
+    const uint64_t pieces = ((uint64_t)args.rows * args.n * (out_dtype == kFp32 ? 4u : 2u) + 15u) / 16u;
+    const dim3 grid((uint32_t)(pieces < ((uint64_t)1 << 28) ? (pieces + 255u) / 256u : 1u << 20));
+    switch (out_dtype) {
+    case kBf16: hipLaunchKernelGGL((matmul_join<Bf16>), grid, dim3(256), 0, stream, args); break;
+    case kFp16: hipLaunchKernelGGL((matmul_join<Fp16>), grid, dim3(256), 0, stream, args); break;
+    default: hipLaunchKernelGGL((matmul_join<Fp32>), grid, dim3(256), 0, stream, args); break;
+    }
+    return hipGetLastError();
 }
 
 }  // namespace ar

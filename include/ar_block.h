@@ -133,7 +133,9 @@ arResult_t arGateQuant(const void *const *inbufs, void *const *outbufs, float *c
  *                  [rows, k] of 8-bit values, dense, and [ceil(k / 128)][rows].
  *  bbufs, bscales  host arrays of nranks device pointers: weights [n, k] of
  *                  8-bit values, dense, and [ceil(n / 128)][ceil(k / 128)].
- *  outbufs         host array of nranks device pointers, [rows, n] of outDtype.
+ *  outbufs         host array of nranks device pointers, [rows, n] of outDtype
+ *                  (with reduce 1 they may hold partial sums while the call
+ *                  runs).
  *  k               a multiple of 16 in 16 .. 2^23 (else arUnsupported).
  *  outDtype        arBfloat16, arFloat16 or arFloat32 (else arUnsupported).
  * Rules (arInvalidArgument when broken): no NULL pointer; every pointer

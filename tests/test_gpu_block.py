@@ -238,6 +238,8 @@ MATMULS = [
     (8, 40, 136, 272), (32, 2, 48, 160), (1, 512, 768, 1024), (2, 1000, 264, 128),
     (1, 33, 8, 8192), (1, 5, 4100, 2064), (5, 128, 128, 128), (1, 8, 7, 96),
     (2, 2, 200, 1040), (3, 9, 1000, 640), (1, 30, 9000, 272), (8, 40, 2100, 400),
+    # few tiles and a long k: workgroups share a summed tile's k
+    (8, 91, 66, 6224), (6, 35, 130, 2064), (5, 1, 8, 4096), (32, 3, 100, 640),
     # enough tiles for 128 x 128 (each, sum) and 256 x 256 (each, sum)
     (8, 200, 2048, 1136), (2, 2100, 2000, 272), (8, 520, 2000, 1040), (2, 2100, 4000, 400),
 ]
