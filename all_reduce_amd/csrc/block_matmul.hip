@@ -61,9 +61,9 @@ __device__ inline i32x8 load_last(const char *at, int32_t left)
 // REDUCE), kAhead of them at a time, and their sums are added through LDS in
 // wave order.  Weights go straight from memory to the registers of the one
 // wave that multiplies them, each byte once: it is bound by that.  On MI355X
-// 8 x (1 x 7168 x 8192) takes 76 us, 6.2 TB/s (two blocks at a time 78 us,
-// one 83 us; 32 columns a workgroup 84 us; through LDS, as in
-// block_matmul_mid.hip, 87 us).
+// 8 x (1 x 7168 x 8192) takes 76 to 80 us, 5.9 to 6.2 TB/s (measured beside 76: two
+// blocks at a time 78 us, one 83 us; 32 columns a workgroup 84 us; through
+// LDS, as in block_matmul_mid.hip, 87 us).
 template <typename T, bool REDUCE>
 __global__ __launch_bounds__(kRowsWaves * 64) void matmul_rows(MatmulArgs p)
 {
@@ -250,7 +250,7 @@ hipError_t launch_matmul(const MatmulArgs &args, int out_dtype, bool reduce, int
     }
     // One or two rows take the kernel made for them, unless sharing k among
     // workgroups wins (8 x (1 x 512 x 8192) summed, for example: 14 in place of
-    // 39 us).
+    // 41 us).
     if (args.rows <= 2 && best_split == 1u && 32.0 * args.n * args.nranks < most) {
         switch (out_dtype) {
         case kBf16: return enqueue_rows<Bf16>(args, reduce, stream);
