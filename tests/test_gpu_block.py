@@ -139,6 +139,30 @@ def test_norm_in_place(comm, ranks, rows, cols, dtype, inplace):
     check_norm(x, res, w, 1e-6, *got, inplace)
 
 
+@pytest.mark.parametrize("ranks,rows,cols,dtype", [(8, 5, 8192, "bf16"), (2, 600, 1001, "fp16"),
+                                                   (3, 7, 30, "fp32")])
+def test_norm_in_place_combined(comm, ranks, rows, cols, dtype):
+    """Every exact overlap at once: the sums kept in the send buffers and an
+    output in the residual; the residual that is rank 0's send buffer, with the
+    sum kept there too.  Both against the same call with buffers of its own."""
+    x = draw((ranks, rows, cols), 71, DT[dtype])
+    w = draw((cols,), 72, DT[dtype]).cuda()
+    for shared, res in ((False, draw((rows, cols), 73, DT[dtype])), (True, x[0])):
+        note(f"norm in place, combined R={ranks} {rows}x{cols} {dtype}")
+        own = [Planes(ranks, rows, cols, DT[dtype]) for _ in range(3)]
+        own[0].fill(x)
+        comm.all_reduce_norm(own[0].ranks, w, 1e-5, residual=res.cuda(), residual_out=own[1].ranks,
+                             out=own[2].ranks)
+        send = Planes(ranks, rows, cols, DT[dtype]).fill(x)
+        out = Planes(ranks, rows, cols, DT[dtype])
+        r = send.ranks[0] if shared else out.ranks[1].copy_(res)
+        comm.all_reduce_norm(send.ranks, w, 1e-5, residual=r, residual_out=send.ranks,
+                             out=out.ranks)
+        torch.cuda.synchronize()
+        assert send.untouched() and out.untouched()
+        assert same(send.ranks, own[1].ranks) and same(out.ranks, own[2].ranks)
+
+
 @pytest.mark.parametrize("ranks,rows,cols,dtype", [(8, 64, 8192, "bf16"), (5, 3, 777, "fp16"),
                                                    (32, 2, 4096, "fp32")])
 def test_kept_sum_has_the_bits_of_the_all_reduce(comm, ranks, rows, cols, dtype):
@@ -299,6 +323,61 @@ def test_matmul_special_values(comm, rows, n, k):
     hit = torch.zeros((rows, n), dtype=torch.bool)
     hit[1], hit[2], hit[:, n - 1] = True, True, True
     assert got[hit].isnan().all() and torch.equal(got[~hit], clean[~hit])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+def test_matmul_special_values_where_k_is_shared(comm, dtype):
+    """Few tiles and a long k, so that several workgroups share a tile's sums: a
+    NaN or an infinity of one rank takes its row, in every rank's output."""
+    a, sa, b, sb = matmul_inputs(8, 5, 40, 4096, 13)
+    b = b.float().abs().clamp_min(1.0).to(E4M3)  # an infinity times these is one
+    a = a.float().abs().clamp_min(1.0).to(E4M3)
+    clean = run_matmul(comm, a, sa, b, sb, DT[dtype], True)[0].cpu()
+    a = a.float()
+    a[6, 1, 4095] = float("nan")
+    sa[3, 17, 2] = float("inf")
+    sa[0, 0, 4] = float("-inf")
+    for out in run_matmul(comm, a.to(E4M3), sa, b, sb, DT[dtype], True):
+        out = out.cpu()
+        assert out[1].isnan().all() and (out[2] == float("inf")).all()
+        assert (out[4] == float("-inf")).all()
+        assert same([out[0], out[3]], [clean[0], clean[3]])
+
+
+def test_matmul_with_shared_k_in_graphs_and_on_two_streams(comm):
+    """The partial sums of workgroups that share a tile's k are the call's own:
+    two captured graphs and eager calls on two streams do not disturb one another."""
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    sets, graphs, want = [], [], []
+    for i, (rows, n, k, dtype) in enumerate([(3, 72, 4096, torch.bfloat16),
+                                             (40, 66, 2064, torch.float32)]):
+        planes = [Planes(8, *t.shape[1:], t.dtype).fill(t)
+                  for t in matmul_inputs(8, rows, n, k, 30 + i)]
+        out = Planes(8, rows, n, dtype)
+        sets.append((planes, out))
+        note(f"shared k {rows}x{n}x{k} {dtype}")
+        call = comm.prepare_matmul_scaled(*[p.ranks for p in planes], out.ranks, reduce=True,
+                                          stream=streams[i])
+        call()
+        torch.cuda.synchronize()
+        want.append([t.clone() for t in out.ranks])
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            comm.matmul_scaled(*[p.ranks for p in planes], out.ranks, reduce=True)
+        graphs.append((graph, call))
+    for turn in range(4):
+        for (_, out), stream in zip(sets, streams):
+            out.raw.fill_(POISON)
+        torch.cuda.synchronize()
+        for (graph, call), stream in zip(graphs, streams):
+            if turn % 2 == 0:
+                with torch.cuda.stream(stream):
+                    graph.replay()
+            else:
+                call()
+        torch.cuda.synchronize()
+        for (_, out), w in zip(sets, want):
+            assert same(out.ranks, w)
 
 
 def test_matmul_is_repeatable(comm):
