@@ -172,19 +172,24 @@ uint64_t ceil_div(uint64_t a, uint64_t b) { return (a + b - 1) / b; }
 //
 // for Q = ceil(W) workgroups a compute unit (W of them on average) of S steps
 // (blocks of k to a wave): a step takes `alone` where nothing else is on the
-// compute unit and `full` a workgroup where it is filled; the rate is 5 MB/us,
-// less where inputs that no cache keeps (from 64 MB) have to come through a
-// part of the compute units (64 x 8192 x 8 x 3584 summed: 58 us with one
-// workgroup a compute unit, 77 with one on every second) or where most of a
-// tile's rows are past the last one.  In a summed form workgroups may share a
-// tile's k too (block_matmul_mid.hip), at the price of a second kernel.
+// compute unit and `full` a workgroup where it is filled.  Inputs of up to 64
+// MB may still be in a cache from the call before; larger ones (the weights of
+// a decode step, read once a step) come from memory, where a step's loads take
+// longer and what counts is how many are under way: these have numbers of
+// their own, a rate of 6.4 MB/us, and less where some compute units have no
+// workgroup.  (With the numbers of cached inputs, 8 x 16 x 8192 x 3584 summed
+// went to two waves a tile and 58 us in place of four and 41, 8 x 4 x 7168 x
+// 8192 to 91 in place of 79.)  In a summed form workgroups may share a tile's k
+// too (block_matmul_mid.hip), at the price of a second kernel.
 //
-// The numbers were fitted to 900 measured shapes on MI355X (3 to 8192 rows, 64
-// to 8192 columns, k 128 to 8192, 1 to 8 ranks, each rank's product and the
-// sum; 8 to 19 % off in the mean): the kernel chosen by them takes 1.03 times
-// the fastest one's time in the mean, over 300 other shapes and with k shared
-// among workgroups 1.05 times.  What they tell apart, for example (us, bfloat16
-// out):
+// The numbers were fitted on MI355X to 900 shapes measured with the same inputs
+// call after call (3 to 8192 rows, 64 to 8192 columns, k 128 to 8192, 1 to 8
+// ranks, each rank's product and the sum; 8 to 19 % off in the mean) and, for
+// more than 64 MB, to 3700 with 600 MB of inputs in turn (10 % off).  The kernel
+// chosen by them takes 1.05 times the fastest one's time in the mean over 300
+// other shapes of the first kind, 1.02 times over 1200 of the second up to 400
+// rows and 1.003 times above.  What they tell apart, for example (us, bfloat16
+// out, the same inputs):
 //
 //                                    64x32   64x64   128x128  256x256
 //     1 rank,    64 x 8192 x 8192     14      17       52       85
@@ -213,18 +218,32 @@ constexpr Choice kChoice32[kChoices - 1] = {
     {64, 32, 2, 3, 3.71f, 0.66f, 0.58f, 0.0f},  {64, 64, 4, 1, 2.35f, 1.20f, 1.37f, 2.31f},
     {64, 64, 2, 2, 4.07f, 1.06f, 0.81f, 0.48f}, {128, 128, 1, 2, 4.22f, 1.21f, 0.81f, 0.0f}};
 
+// For inputs from memory.
+constexpr Choice kMemory16[kChoices] = {
+    {32, 32, 8, 1, 5.05f, 0.94f, 1.00f, 2.10f}, {32, 32, 4, 2, 7.18f, 0.48f, 0.51f, 0.16f},
+    {32, 32, 2, 4, 7.43f, 0.45f, 0.28f, 0.20f}, {64, 32, 4, 1, 3.15f, 0.68f, 0.74f, 2.35f},
+    {64, 32, 2, 3, 6.69f, 0.53f, 0.43f, 0.05f}, {64, 64, 4, 1, 5.14f, 0.93f, 1.01f, 3.89f},
+    {64, 64, 2, 2, 10.43f, 0.65f, 0.69f, 0.0f}, {128, 128, 1, 2, 8.23f, 1.11f, 0.78f, 0.88f},
+    {256, 256, 1, 1, 3.65f, 1.81f, 1.81f, 5.06f}};
+constexpr Choice kMemory32[kChoices - 1] = {
+    {32, 32, 8, 1, 5.76f, 0.97f, 1.04f, 2.30f},  {32, 32, 4, 2, 7.58f, 0.59f, 0.52f, 0.39f},
+    {32, 32, 2, 4, 10.96f, 0.49f, 0.28f, 0.07f}, {64, 32, 4, 1, 4.10f, 0.72f, 0.77f, 2.75f},
+    {64, 32, 2, 3, 10.88f, 0.59f, 0.46f, 0.0f},  {64, 64, 4, 1, 6.36f, 1.09f, 1.19f, 4.86f},
+    {64, 64, 2, 2, 12.37f, 0.96f, 0.84f, 0.23f}, {128, 128, 1, 2, 7.18f, 1.53f, 1.05f, 2.16f}};
+
 hipError_t launch_matmul(const MatmulArgs &args, int out_dtype, bool reduce, int cu_count,
                          hipStream_t stream)
 {
     // (a launch has fewer than 2^32 threads)
     const double most = 4.0e9;
     const bool exact = out_dtype == kFp32;
-    const Choice *choices = exact ? kChoice32 : kChoice16;
     const Choice *best = nullptr;
     uint32_t best_split = 1;
     double best_us = 0.0;
     const double ranks = args.nranks, steps = (double)args.kblocks * (reduce ? ranks : 1.0);
     const double read = ((double)args.rows + args.n) * args.k * ranks * 1e-6;
+    const bool memory = read > 64.0;
+    const Choice *choices = memory ? (exact ? kMemory32 : kMemory16) : (exact ? kChoice32 : kChoice16);
     // (what is written is the same for all, but that sums are read again)
     const double join = 3.0 + (double)args.rows * args.n * ranks * (exact ? 4.0 : 2.0) * 0.1e-6;
     const uint32_t splits = reduce ? matmul_most_split(out_dtype, args.nranks) : 1u;
@@ -237,8 +256,8 @@ hipError_t launch_matmul(const MatmulArgs &args, int out_dtype, bool reduce, int
             const double s = ceil(steps / (c.waves * split));
             if (q * cu_count * 64.0 * (c.rows == 256u ? 8.0 : c.rows == 128u ? 4.0 : c.waves) > most)
                 continue;
-            const double rate = (read > 64.0 ? 5.0 * fmin(1.0, 1.3 * w) : 5.0) *
-                                fmin(1.0, 0.5 + (double)args.rows / c.rows);
+            const double rate = memory ? 6.4 * fmin(1.0, 2.0 * w)
+                                       : 5.0 * fmin(1.0, 0.5 + (double)args.rows / c.rows);
             const double us = c.base + c.each * q + (split > 1u ? join : 0.0) +
                               fmax(fmax(c.alone * ceil(q / c.resident) * s, c.full * w * s), read / rate);
             if (best == nullptr || us < best_us) {
