@@ -11,8 +11,8 @@
 // row tile, applied with a fused multiply-add to the running sums.  (Four
 // 16x16x128 instructions in place of two 32x32x64 ones: 2 % slower.)
 //
-// On MI355X 8 x (4096 x 7168 x 8192) takes 1740 to 1780 us on random values,
-// 2.16 to 2.21 PFLOP/s, and 1416 us, 2.72 PFLOP/s, on constant ones: the
+// On MI355X 8 x (4096 x 7168 x 8192) takes 1740 to 1840 us on random values,
+// 2.09 to 2.21 PFLOP/s, and 1416 us, 2.72 PFLOP/s, on constant ones: the
 // card's power sets the clock (1.5 to 1.8 against 2.3 GHz).  Of copies on
 // random values, one without the scaling took 12 % less, one without the LDS
 // reads 8 %, one without the loads 12 %.  The instructions alone reach 4.1
