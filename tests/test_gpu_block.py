@@ -309,6 +309,16 @@ def test_matmul(comm, ranks, rows, n, k, dtype, reduce):
             assert (bits(out[r].cpu()) == bits(out[0].cpu())).all()
 
 
+@pytest.mark.parametrize("reduce", [False, True], ids=["each", "reduce"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("ranks,rows,n,k", [(8, 60, 2090, 4112), (8, 140, 1030, 8192),
+                                            (8, 200, 2050, 4112), (8, 4, 4100, 2064)])
+def test_matmul_from_memory(comm, ranks, rows, n, k, dtype, reduce):
+    """More than 64 MB of inputs: other tiles, and other numbers of workgroups to
+    share k, than smaller ones take."""
+    test_matmul(comm, ranks, rows, n, k, dtype, reduce)
+
+
 @pytest.mark.parametrize("rows,n,k", [(3, 40, 272), (100, 200, 400), (300, 520, 1040)])
 def test_matmul_special_values(comm, rows, n, k):
     """A NaN in an activation takes its row alone, one in a weight its column,
