@@ -76,7 +76,7 @@ __global__ __launch_bounds__(256) void gate_quant(GateArgs p)
                     y[e] = silu(y[e]) * f[e];
             }
             const float s = scale_of(max_block<T>(max_bits(y)));
-            const Eights<E> q = to_eights(y, 1.0f / s);
+            const Eights<E> q = to_eights(y, s);
             if (row < p.rows && col < p.cols) {
                 if (col + E <= p.cols)
                     store_eights<NT>(out + row * p.cols + col, q);

@@ -206,7 +206,7 @@ __global__ __launch_bounds__(1024) void norm_rows(NormArgs p)
             if constexpr (EIGHT) {
                 // all lanes of a scale take part; those past the row hold 0
                 const float s = scale_of(max_block<T>(max_bits(y)));
-                const Eights<E> q = to_eights(y, 1.0f / s);
+                const Eights<E> q = to_eights(y, s);
                 if (n != 0) {
                     const uint64_t sat = (uint64_t)(col[v] / AR_SCALE_BLOCK) * p.rows + row;
                     for (uint32_t r = share; r < p.nranks; r += p.split) {

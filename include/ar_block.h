@@ -28,8 +28,8 @@
  *       [ceil(n / 128)][ceil(k / 128)].
  *
  * Quantisation of a block of values y:
- *     s = max(max|y| / 448, 2^-126);  q = y * (1 / s) rounded to nearest even
- * (1 / s and its product with y are rounded to binary32 first).
+ *     s = max(max|y| / 448, 2^-126);  q = y / s rounded to nearest even
+ * (both quotients are rounded to binary32 first).
  * A block that holds a NaN has the scale NaN; one that holds an infinity and
  * no NaN the scale infinity, with which its finite values become 0 and its
  * infinities NaN.  A block of zeros has the scale 2^-126.
