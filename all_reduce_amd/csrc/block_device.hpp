@@ -150,13 +150,28 @@ __device__ inline uint32_t max_block(uint32_t x)
     return x;
 }
 
-// The sum over a wave, in every lane, in a fixed order.
-__device__ inline float sum64(float x)
+template <int CTRL>
+__device__ inline double lane_move(double x)
 {
-    x += __builtin_bit_cast(float, lane_move<0x128>(__builtin_bit_cast(uint32_t, x)));
-    x += __builtin_bit_cast(float, lane_move<0x124>(__builtin_bit_cast(uint32_t, x)));
-    x += __builtin_bit_cast(float, lane_move<0x122>(__builtin_bit_cast(uint32_t, x)));
-    x += __builtin_bit_cast(float, lane_move<0x121>(__builtin_bit_cast(uint32_t, x)));
+    const uint64_t b = __builtin_bit_cast(uint64_t, x);
+    return __builtin_bit_cast(double, (uint64_t)lane_move<CTRL>((uint32_t)(b >> 32)) << 32 |
+                                          lane_move<CTRL>((uint32_t)b));
+}
+
+template <int CTRL>
+__device__ inline float lane_move(float x)
+{
+    return __builtin_bit_cast(float, lane_move<CTRL>(__builtin_bit_cast(uint32_t, x)));
+}
+
+// The sum over a wave, in every lane, in a fixed order.
+template <typename F>
+__device__ inline F sum64(F x)
+{
+    x += lane_move<0x128>(x);
+    x += lane_move<0x124>(x);
+    x += lane_move<0x122>(x);
+    x += lane_move<0x121>(x);
     x += __shfl_xor(x, 16);
     x += __shfl_xor(x, 32);
     return x;

@@ -12,11 +12,16 @@
 // and each stores to its share of the ranks: a row's stores are more bytes
 // than its reads and take longer than reading it again from the cache.
 //
+// The sum of squares is binary32 where that holds the mean; rows beyond 1e18
+// and, where eps does not cover them, below 1e-12 take it again in binary64,
+// which loses no square of a finite h.  (A binary64 sum for every row: 64 rows
+// of 8 ranks x 8192 take 7.4 in place of 7.2 us.)
+//
 // It is bound by memory: R + 1 reads and 2 R writes a column at two or three
 // operations each.  On MI355X 8 x 8192 x 8192 bfloat16 with residual takes
 // 650 us (5.2 TB/s; a large copy runs at 5.1), 16 x 1024 x 7168 float32 with
 // an 8-bit output 211 us (5.1 TB/s).  In a graph one row of 8 x 8192 takes
-// 4.4 us (5.5 with one workgroup a row) and 64 rows 7.0, bound by a row's chain
+// 4.4 us (5.5 with one workgroup a row) and 64 rows 7.2, bound by a row's chain
 // of loads, sum and stores.
 #include <type_traits>
 
@@ -59,6 +64,17 @@ __device__ inline void add_ranks(const NormArgs &p, uint32_t r0, uint64_t row_at
         }
 }
 
+// 1 / sqrt(m) for m in 2^-100 .. 2^126, with one rounding but for 2^-45 of it:
+// the root's reciprocal, off by e / 2 of itself with e = 1 - m r r.  So h times
+// it rounds as often as h divided by a rounded root.
+__device__ inline float inverse_root(float m)
+{
+    const float r = 1.0f / __builtin_sqrtf(m);
+    const float mr = m * r, low = __builtin_fmaf(m, r, -mr);
+    const float e = __builtin_fmaf(-low, r, __builtin_fmaf(-mr, r, 1.0f));
+    return __builtin_fmaf(0.5f * r, e, r);
+}
+
 // V: pieces a lane holds (lane i holds pieces i, i + threads, ..).  EIGHT:
 // 8-bit output with scales.  NT: non-temporal accesses.  RAGGED: cols is not a
 // multiple of a piece's.
@@ -68,6 +84,7 @@ __global__ __launch_bounds__(1024) void norm_rows(NormArgs p)
     constexpr uint32_t E = kPiece<T>;
     constexpr uint32_t kBatch = 8 / V;  // ranks whose loads are under way at once: 8 pieces a lane
     __shared__ float part[2][16];
+    __shared__ double wide[16];
     const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
     const uint32_t waves = blockDim.x >> 6;
     // The tables of where to store are touched here: their first use costs a
@@ -181,7 +198,36 @@ __global__ __launch_bounds__(1024) void norm_rows(NormArgs p)
         float total = 0.0f;
         for (uint32_t w = 0; w < waves; ++w)
             total += part[turn][w];
-        const float inv = 1.0f / __builtin_sqrtf(total / (float)p.cols + p.eps);
+        // (the same in every lane of the workgroup)
+        const float mean = __builtin_bit_cast(
+            float, __builtin_amdgcn_readfirstlane(
+                       __builtin_bit_cast(int, total / (float)p.cols + p.eps)));
+        float inv;
+        int up = 0;
+        if (mean >= 0x1p-80f && mean <= 0x1p120f) {
+            inv = inverse_root(mean);
+        } else {
+            // h * inv is scaled by 2^-up and 2^up, with which the root lies in
+            // [0.7, 1.5).  (`wide` is written again only behind the next row's
+            // barrier, which every wave reaches after it has read it here.)
+            double square = 0.0;
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+#pragma unroll
+                for (uint32_t e = 0; e < E; ++e)
+                    square = __builtin_fma((double)h[v][e], (double)h[v][e], square);
+            square = sum64(square);
+            if (lane == 0)
+                wide[wave] = square;
+            __syncthreads();
+            double sum = 0.0;
+            for (uint32_t w = 0; w < waves; ++w)
+                sum += wide[w];
+            sum = sum / (double)p.cols + (double)p.eps;
+            up = __builtin_amdgcn_frexp_exp(sum) >> 1;  // (0 for 0, infinity and NaN)
+            const float m = (float)__builtin_ldexp(sum, -2 * up);
+            inv = m > 0.0f && m < __builtin_inff() ? inverse_root(m) : 1.0f / __builtin_sqrtf(m);
+        }
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const bool full = !RAGGED || col[v] + E <= p.cols;
@@ -199,6 +245,10 @@ __global__ __launch_bounds__(1024) void norm_rows(NormArgs p)
             float y[E], f[E];
             if constexpr (!kEarly)
                 weight[v] = load_weight(v);
+            if (up != 0)
+#pragma unroll
+                for (uint32_t e = 0; e < E; ++e)
+                    h[v][e] = __builtin_ldexpf(h[v][e], -up);
             widen_piece<T>(weight[v], f);
 #pragma unroll
             for (uint32_t e = 0; e < E; ++e)

@@ -67,9 +67,9 @@ extern "C" {
  *     out_r[t][i] = y, or 8-bit values and scales of y
  *
  * The norm is taken of h before its rounding to the element type.  The sum of
- * squares is binary32: a row whose squares overflow it gives zeros, and one
- * that holds an infinity zeros but NaN at the infinity; a row with a NaN is
- * NaN, and so is a row of zeros with eps 0.
+ * squares is binary32, or binary64 for rows whose mean that does not hold, so
+ * that rows of any finite values have a norm.  A row that holds an infinity gives zeros but NaN at the infinity; a
+ * row with a NaN is NaN, and so is a row of zeros with eps 0.
  *
  *  sendbufs     host array of nranks device pointers, each [rows, cols] dense.
  *  residual     device pointer, [rows, cols] dense: the residual stream, which

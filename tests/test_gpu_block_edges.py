@@ -7,7 +7,8 @@ import torch
 import all_reduce_amd as ar
 import block_ref as ref
 from gpu_util import note
-from test_gpu_block import DT, E4M3, Planes, comm, draw  # noqa: F401  (comm is a fixture)
+from test_gpu_block import (DT, E4M3, Planes, check_eight, comm, draw,  # noqa: F401  (comm is a fixture)
+                            run_norm)
 
 pytestmark = pytest.mark.gpu
 
@@ -34,3 +35,61 @@ def test_quantisation_is_the_quotient(comm, rows, cols, dtype):
     q = (y / s.unsqueeze(-1)).flatten(1)[:, :cols].to(E4M3)
     off = out.ranks[0].cpu().float() != q.float()
     assert not off.any(), f"{int(off.sum())} of {off.numel()} values"
+
+
+# ---- norm ------------------------------------------------------------------------
+@pytest.mark.parametrize("quant", [False, True], ids=["same", "eight"])
+@pytest.mark.parametrize("dtype,sizes", [("bf16", (1e-38, 1e-30, 1e-15, 1.0, 1e15, 1e25, 1e37)),
+                                         ("fp32", (1e-41, 1e-30, 1e-15, 1.0, 1e15, 1e25, 1e37)),
+                                         ("fp16", (1e-7, 1e-5, 1.0, 3e3))])
+@pytest.mark.parametrize("eps", [0.0, 1e-5])
+@pytest.mark.parametrize("ranks,cols", [(1, 700), (3, 8192), (2, 24577)])
+def test_norm_of_rows_of_any_size(comm, ranks, cols, eps, dtype, sizes, quant):
+    """Rows whose squares would leave binary32 above or below, and the type's
+    smallest values, have the norm of the definition."""
+    x = draw((ranks, len(sizes), cols), 81) * torch.tensor(sizes).view(1, -1, 1)
+    x = x.to(DT[dtype])
+    w = (draw((cols,), 82) * 0.2 + 1).to(DT[dtype])
+    kept, out, scales = run_norm(comm, x, None, w, eps, quant, True)
+    h, h_tol, y, y_tol = ref.norm(x, None, w, eps)
+    # a quotient and a product below 2^-126 round to a multiple of 2^-149
+    y_tol = y_tol + 2.0 ** -150 * (1 + w.double().abs())
+    for r in range(ranks):
+        ref.assert_within(kept[r], h, ref.rounded(h, h_tol, x.dtype), f"h rank {r}")
+        if quant:
+            check_eight(out[r], scales[r], y, y_tol, f"rank {r}")
+        else:
+            ref.assert_within(out[r], y, ref.rounded(y, y_tol, x.dtype), f"out rank {r}")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_norm_of_one_large_value(comm, dtype):
+    """One value of 2^100 in a row of ones: sqrt(cols) there, and what is left of
+    the others is small and not zero."""
+    x = torch.ones((1, 2, 512), dtype=DT[dtype])
+    x[0, 1, 77] = 2.0 ** 100
+    _, out, _ = run_norm(comm, x, None, torch.ones(512, dtype=DT[dtype]), 0.0, False, False)
+    # 2^100 / sqrt(2^200 / 512) and 1 / sqrt(2^200 / 512), correctly rounded
+    far = torch.tensor(512.0, dtype=torch.float64).sqrt()
+    want = torch.full((512,), 2.0 ** -100, dtype=torch.float64) * far
+    want[77] = far
+    assert torch.equal(out[0][0].cpu().float(), torch.ones(512))
+    # the root and the quotient round once each, the output once
+    tol = want * (4 * ref.U) + want * ref.HALF_STEP[DT[dtype]]
+    ref.assert_within(out[0][1], want, tol, "large")
+
+
+def test_norm_rounds_as_often_as_the_division(comm):
+    """float32 rows of 64 values alike but for their signs: their sum of squares
+    and its mean are exact, so an output has the rounding of eps added (halved
+    by the root), of the inverse root, of its product with h and of the weight's
+    product: 3.5 units of 2^-24 (and 2^-45, with which the root is computed)."""
+    g = torch.Generator("cpu").manual_seed(83)
+    size = torch.randint(1 << 10, 1 << 11, (4000, 1), generator=g).float()  # squares of 22 bits
+    x = (size * (torch.randint(0, 2, (4000, 64), generator=g) * 2 - 1)).unsqueeze(0)
+    w = draw((64,), 84) * 0.2 + 1
+    eps = 0.3
+    _, out, _ = run_norm(comm, x, None, w, eps, False, False)
+    d = x[0].double()
+    y = d / (d.square().mean(-1, keepdim=True) + torch.tensor(eps).double()).sqrt() * w.double()
+    ref.assert_within(out[0], y, y.abs() * (3.5 * ref.U + 2.0 ** -40), "float32")
