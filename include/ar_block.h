@@ -101,7 +101,7 @@ typedef enum { arActNone = 0, arActSiLU = 1 } arActivation_t;
  *
  *     arActSiLU:  y = g / (1 + exp(-g)) * u, in binary32, with an input row
  *                 holding g in its first `cols` columns and u in the next
- *                 (0 for g below -87.3);
+ *                 (g = -infinity gives NaN, as the formula does);
  *     arActNone:  y = x, an input row holds `cols` columns;
  *     out_r, scales_r = 8-bit values and scales of y.
  *

@@ -93,3 +93,48 @@ def test_norm_rounds_as_often_as_the_division(comm):
     d = x[0].double()
     y = d / (d.square().mean(-1, keepdim=True) + torch.tensor(eps).double()).sqrt() * w.double()
     ref.assert_within(out[0], y, y.abs() * (3.5 * ref.U + 2.0 ** -40), "float32")
+
+
+# ---- gate ------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+def test_gate_far_below_zero(comm, dtype):
+    """Gates whose exponential is below the type's range times an `up` that
+    brings the product back into it, each row a block of its own; among them
+    both sides of every border, and the 8-bit values and scales of the
+    definition."""
+    gates = [-60.0, -79.9, -80.0, -80.25, -87.0, -87.5, -88.0, -88.75, -90.0, -100.0, -104.0,
+             -110.0, -125.5, -150.0, -170.0, -174.5, -190.0, -199.0, -210.0, -399.0, -401.0, -6e4]
+    ups = [1.0, -1.0, 1e4, -6e4] + ([1e30, -3e38, 1e-20] if dtype != "fp16" else [])
+    rows = [(g, u) for g in gates for u in ups]
+    x = torch.zeros((1, len(rows), 256))
+    for i, (g, u) in enumerate(rows):
+        x[0, i, :128] = torch.linspace(g, g * 1.01, 128)
+        x[0, i, 128:] = torch.linspace(u, u * 0.25, 128)
+    x = x.to(DT[dtype])
+    note(f"gate far below zero {dtype}")
+    src = Planes(1, len(rows), 256, DT[dtype]).fill(x)
+    out, scales = Planes(1, len(rows), 128, E4M3), Planes(1, 1, len(rows), torch.float32)
+    comm.gate_quant(src.ranks, out.ranks, scales.ranks)
+    torch.cuda.synchronize()
+    assert src.untouched() and out.untouched() and scales.untouched()
+    y, tol = ref.gate(x[0], "silu")
+    # results below 2^-126 round to multiples of 2^-149, once or (with the
+    # product before it) twice
+    check_eight(out.ranks[0], scales.ranks[0], y, tol + 2.0 ** -149, "far")
+
+
+def test_gate_infinities(comm):
+    """Plus infinity passes through, minus infinity divides by an infinity."""
+    inf = float("inf")
+    x = torch.ones((1, 3, 256))
+    x[0, 0, 5], x[0, 1, 5], x[0, 2, 128 + 5] = inf, -inf, inf
+    x[0, 2, 5] = -100.0
+    src, out = x.cuda(), torch.empty((3, 128), dtype=E4M3, device="cuda:0")
+    scales = torch.empty((1, 3), device="cuda:0")
+    comm.gate_quant([src[0]], [out], [scales])
+    torch.cuda.synchronize()
+    s, q = scales[0].cpu(), out.float().cpu()
+    assert s[0] == inf and s[1].isnan() and s[2] == inf
+    assert q[0, 5].isnan() and q[1].isnan().all() and q[2, 5].isnan()
+    keep = torch.arange(128) != 5
+    assert (q[0][keep] == 0).all() and (q[2][keep] == 0).all()
