@@ -263,6 +263,8 @@ arResult_t arMatmulScaled(const void *const *abufs, const float *const *ascales,
         return reject(arInvalidArgument, "rows and n must be at most 2^30");
     if (rows * n > ((size_t)1 << 38))
         return reject(arInvalidArgument, "rows * n must be at most 2^38");
+    if (!ar::matmul_fits(rows, n, dtype))
+        return reject(arUnsupported, "more tiles than a launch holds");
     Ranges mem;
     if (!mem.add_ranks(abufs, nranks, rows * k, false) ||
         !mem.add_ranks((const void *const *)ascales, nranks,

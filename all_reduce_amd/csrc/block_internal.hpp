@@ -58,6 +58,17 @@ hipError_t launch_gate(const GateArgs &args, int dtype, int act, int nranks, int
                        hipStream_t stream);
 hipError_t launch_matmul(const MatmulArgs &args, int out_dtype, bool reduce, int cu_count,
                          hipStream_t stream);
+// What it launches: tiles of rows x cols (16 x 16: the kernel for one or two
+// rows; from 128 x 128 on the ones for many), the waves that share a tile's k
+// and the workgroups that do.  False where no kernel's launch holds the tiles;
+// it then takes the ranks in two launches.  One rank's tiles (or all, summed)
+// fit where matmul_fits says so.
+struct MatmulChoice {
+    uint32_t rows, cols, waves, split;
+};
+bool choose_matmul(const MatmulArgs &args, int out_dtype, bool reduce, int cu_count,
+                   MatmulChoice *choice);
+bool matmul_fits(uint64_t rows, uint64_t n, int out_dtype);
 // Its kernels for a batch of rows (block_matmul_mid.hip; mt, nt: tiles of 32
 // rows and columns, 1 and 1, 2 and 1 or 2 and 2) and for many
 // (block_matmul_tile.hip; tiles of 256 x 256 or 128 x 128).  Their 32-bit

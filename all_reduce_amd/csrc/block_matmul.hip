@@ -231,11 +231,34 @@ constexpr Choice kMemory32[kChoices - 1] = {
     {64, 32, 2, 3, 10.88f, 0.59f, 0.46f, 0.0f},  {64, 64, 4, 1, 6.36f, 1.09f, 1.19f, 4.86f},
     {64, 64, 2, 2, 12.37f, 0.96f, 0.84f, 0.23f}, {128, 128, 1, 2, 7.18f, 1.53f, 1.05f, 2.16f}};
 
-hipError_t launch_matmul(const MatmulArgs &args, int out_dtype, bool reduce, int cu_count,
-                         hipStream_t stream)
+namespace {
+
+// A launch has fewer than 2^32 threads.
+constexpr double kMostThreads = 4.0e9;
+
+double tiles_of(const Choice &c, uint64_t rows, uint64_t n)
 {
-    // (a launch has fewer than 2^32 threads)
-    const double most = 4.0e9;
+    return (double)(ceil_div(rows, c.rows) * ceil_div(n, c.cols));
+}
+
+bool fits(const Choice &c, double tiles)
+{
+    return tiles * 64.0 * (c.rows == 256u ? 8.0 : c.rows == 128u ? 4.0 : c.waves) <= kMostThreads;
+}
+
+}  // namespace
+
+bool matmul_fits(uint64_t rows, uint64_t n, int out_dtype)
+{
+    for (int i = 0; i < (out_dtype == kFp32 ? kChoices - 1 : kChoices); ++i)
+        if (fits(kChoice16[i], tiles_of(kChoice16[i], rows, n)))
+            return true;
+    return false;
+}
+
+bool choose_matmul(const MatmulArgs &args, int out_dtype, bool reduce, int cu_count,
+                   MatmulChoice *choice)
+{
     const bool exact = out_dtype == kFp32;
     const Choice *best = nullptr;
     uint32_t best_split = 1;
@@ -249,13 +272,12 @@ hipError_t launch_matmul(const MatmulArgs &args, int out_dtype, bool reduce, int
     const uint32_t splits = reduce ? matmul_most_split(out_dtype, args.nranks) : 1u;
     for (int i = 0; i < (exact ? kChoices - 1 : kChoices); ++i) {
         const Choice &c = choices[i];
-        const double tiles = (double)(ceil_div(args.rows, c.rows) * ceil_div(args.n, c.cols)) *
-                             (reduce ? 1.0 : ranks);
+        const double tiles = tiles_of(c, args.rows, args.n) * (reduce ? 1.0 : ranks);
         for (uint32_t split = 1; split <= (c.rows < 128u ? splits : 1u); split *= 2u) {
+            if (!fits(c, tiles * split))
+                continue;
             const double w = tiles * split / cu_count, q = ceil(w);
             const double s = ceil(steps / (c.waves * split));
-            if (q * cu_count * 64.0 * (c.rows == 256u ? 8.0 : c.rows == 128u ? 4.0 : c.waves) > most)
-                continue;
             const double rate = memory ? 6.4 * fmin(1.0, 2.0 * w)
                                        : 5.0 * fmin(1.0, 0.5 + (double)args.rows / c.rows);
             const double us = c.base + c.each * q + (split > 1u ? join : 0.0) +
@@ -270,19 +292,52 @@ hipError_t launch_matmul(const MatmulArgs &args, int out_dtype, bool reduce, int
     // One or two rows take the kernel made for them, unless sharing k among
     // workgroups wins (8 x (1 x 512 x 8192) summed, for example: 14 in place of
     // 41 us).
-    if (args.rows <= 2 && best_split == 1u && 32.0 * args.n * args.nranks < most) {
+    if (args.rows <= 2 && best_split == 1u && 32.0 * args.n * args.nranks < kMostThreads) {
+        *choice = {16u, 16u, kRowsWaves, 1u};
+        return true;
+    }
+    if (best == nullptr)
+        return false;
+    *choice = {best->rows, best->cols, best->waves, best_split};
+    return true;
+}
+
+hipError_t launch_matmul(const MatmulArgs &args, int out_dtype, bool reduce, int cu_count,
+                         hipStream_t stream)
+{
+    MatmulChoice c;
+    if (!choose_matmul(args, out_dtype, reduce, cu_count, &c)) {
+        // Too many tiles for one launch: half of the ranks, and the others.
+        // (One rank's fit: the entry point has asked matmul_fits.)
+        if (reduce || args.nranks == 1)
+            return hipErrorInvalidConfiguration;
+        const uint32_t half = args.nranks / 2u;
+        MatmulArgs part = args;
+        part.nranks = half;
+        const hipError_t e = launch_matmul(part, out_dtype, reduce, cu_count, stream);
+        if (e != hipSuccess)
+            return e;
+        part.nranks = args.nranks - half;
+        for (uint32_t r = 0; r < part.nranks; ++r) {
+            part.a[r] = args.a[half + r];
+            part.sa[r] = args.sa[half + r];
+            part.b[r] = args.b[half + r];
+            part.sb[r] = args.sb[half + r];
+            part.out[r] = args.out[half + r];
+        }
+        return launch_matmul(part, out_dtype, reduce, cu_count, stream);
+    }
+    if (c.rows == 16u) {
         switch (out_dtype) {
         case kBf16: return enqueue_rows<Bf16>(args, reduce, stream);
         case kFp16: return enqueue_rows<Fp16>(args, reduce, stream);
         default: return enqueue_rows<Fp32>(args, reduce, stream);
         }
     }
-    if (best == nullptr)
-        return hipErrorInvalidConfiguration;
-    if (best->rows >= 128u)
-        return launch_matmul_tile(args, out_dtype, reduce, best->rows == 256u, stream);
-    return launch_matmul_mid(args, out_dtype, reduce, (int)best->rows / 32, (int)best->cols / 32,
-                             best->waves, best_split, stream);
+    if (c.rows >= 128u)
+        return launch_matmul_tile(args, out_dtype, reduce, c.rows == 256u, stream);
+    return launch_matmul_mid(args, out_dtype, reduce, (int)c.rows / 32, (int)c.cols / 32, c.waves,
+                             c.split, stream);
 }
 
 }  // namespace ar

@@ -139,6 +139,8 @@ arResult_t arGateQuant(const void *const *inbufs, void *const *outbufs, float *c
  *                  runs).
  *  k               a multiple of 16 in 16 .. 2^23 (else arUnsupported).
  *  outDtype        arBfloat16, arFloat16 or arFloat32 (else arUnsupported).
+ *  rows, n         where ceil(rows / 128) * ceil(n / 128) is above 15000000 a
+ *                  launch may not hold the tiles (arUnsupported).
  * Rules (arInvalidArgument when broken): no NULL pointer; every pointer
  * 16-byte aligned; rows and n at most 2^30 and rows * n at most 2^38; no
  * written range overlaps another written or read one (inputs may be shared

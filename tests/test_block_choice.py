@@ -1,0 +1,44 @@
+"""The product's sizes on the host: what no launch holds is refused before
+anything else is looked at.  No GPU is needed."""
+import json
+import subprocess
+import sys
+
+import pytest
+
+import all_reduce_amd as ar
+from test_block_host import CHILD, MM, ROOT
+
+# (label, changes to a valid call, code, log): 16 bytes of k, so that weights
+# and outputs have room between the made-up addresses
+CASES = [
+    ("1 row of 2^30", dict(rows=1, n=1 << 30), "arInvalidArgument", "NULL comm"),
+    ("256 rows of 2^30", dict(rows=256, n=1 << 30), "arInvalidArgument", "NULL comm"),
+    ("2^30 rows of 1", dict(rows=1 << 30, n=1), "arInvalidArgument", "NULL comm"),
+    ("2^19 rows of 2^19", dict(rows=1 << 19, n=1 << 19), "arInvalidArgument", "NULL comm"),
+    ("257 rows of 2^29.99, summed", dict(rows=257, n=(1 << 38) // 257, reduce=1), "arUnsupported", "launch"),
+    ("2^19 rows of 2^19 floats", dict(rows=1 << 19, n=1 << 19, out_dtype=2), "arUnsupported", "launch"),
+    ("128 rows of 2^30 floats", dict(rows=128, n=1 << 30, out_dtype=2), "arInvalidArgument", "NULL comm"),
+    ("15000000 tiles of floats", dict(rows=128 * 3000, n=128 * 5000, out_dtype=2), "arInvalidArgument", "NULL comm"),
+]
+
+
+@pytest.fixture(scope="module")
+def results():
+    tb = 1 << 42
+    at = lambda i: (1 << 44) + i * tb  # noqa: E731
+    base = dict(MM, abufs=[at(0), at(1)], ascales=[at(2), at(3)], bbufs=[at(4), at(5)], bscales=[at(6), at(7)],
+                outbufs=[at(8), at(9)], k=16)
+    calls = [(label, "arMatmulScaled", dict(base, **kw)) for label, kw, _, _ in CASES]
+    res = subprocess.run([sys.executable, "-c", CHILD, str(ROOT), json.dumps(calls)], capture_output=True,
+                         text=True, env={"AR_DEBUG": "1", "PATH": "/usr/bin:/bin"}, timeout=120)
+    assert res.returncode == 0, res.stderr
+    codes = dict(json.loads(line) for line in res.stdout.splitlines())
+    logs = dict(part.split("\n", 1) for part in res.stderr.split("@@")[1:])
+    return codes, logs
+
+
+@pytest.mark.parametrize("label,kw,code,why", CASES, ids=[c[0] for c in CASES])
+def test_tiles_of_a_launch(results, label, kw, code, why):
+    codes, logs = results
+    assert codes[label] == ar.arResult[code] and why in logs[label], (codes[label], logs[label])

@@ -138,3 +138,28 @@ def test_gate_infinities(comm):
     assert q[0, 5].isnan() and q[1].isnan().all() and q[2, 5].isnan()
     keep = torch.arange(128) != 5
     assert (q[0][keep] == 0).all() and (q[2][keep] == 0).all()
+
+
+# ---- product ---------------------------------------------------------------------
+def test_matmul_of_more_tiles_than_a_launch(comm):
+    """Two ranks of 2^30 columns that share their weights: each has a launch."""
+    n, k = 1 << 30, 16
+    note(f"matmul 2 x (1 x {n} x {k})")
+    g = torch.Generator("cuda").manual_seed(9)
+    b = torch.empty((n, k), dtype=torch.uint8, device="cuda:0")
+    for part in b.split(1 << 26):
+        part.random_(0, 0x7F, generator=g)  # 0 .. 448
+    b = b.view(E4M3)
+    sb = torch.rand((n // 128, 1), generator=g, device="cuda:0").add_(0.5)
+    a = [draw((1, k), 90 + r, scale=50.0).to(E4M3).cuda() for r in range(2)]
+    sa = [torch.full((1, 1), 0.5 + r, device="cuda:0") for r in range(2)]
+    out = [torch.full((1, n), float("nan"), dtype=torch.bfloat16, device="cuda:0") for _ in range(2)]
+    comm.matmul_scaled(a, sa, [b, b], [sb, sb], out)
+    torch.cuda.synchronize()
+    at = torch.cat([torch.tensor([0, 127, 128, n // 2 - 1, n // 2, n - 1]),
+                    torch.randint(0, n, (2000,), generator=torch.Generator().manual_seed(91))])
+    for r in range(2):
+        c, tol, _ = ref.matmul(a[r].cpu(), sa[r].cpu(), b[at.cuda()].cpu(), sb[(at // 128).cuda()].cpu(),
+                               torch.bfloat16, columns=at)
+        ref.assert_within(out[r][:, at.cuda()], c, ref.rounded(c, tol, torch.bfloat16), f"rank {r}")
+        assert not out[r].isnan().any()
