@@ -295,4 +295,27 @@ arResult_t arMatmulScaled(const void *const *abufs, const float *const *ascales,
                                       (hipStream_t)stream));
 }
 
+// For tests, on the host: which kernel arMatmulScaled launches for a call of
+// these sizes on a card of `cu_count` compute units: tile rows and columns (16
+// x 16: the kernel for one or two rows), waves that share a tile's k, workgroups
+// that do.  0 where the call would be split or refused.
+int ar_block_matmul_choice(size_t rows, size_t n, size_t k, int outDtype, int reduce, int nranks,
+                           int cu_count, int choice[4])
+{
+    ar::MatmulArgs args = {};
+    args.rows = (uint32_t)rows;
+    args.n = (uint32_t)n;
+    args.k = (uint32_t)k;
+    args.kblocks = (uint32_t)scale_blocks(k);
+    args.nranks = (uint32_t)nranks;
+    ar::MatmulChoice c;
+    if (!ar::choose_matmul(args, outDtype, reduce != 0, cu_count, &c))
+        return 0;
+    choice[0] = (int)c.rows;
+    choice[1] = (int)c.cols;
+    choice[2] = (int)c.waves;
+    choice[3] = (int)c.split;
+    return 1;
+}
+
 }  // extern "C"

@@ -1,12 +1,16 @@
 """The product's sizes on the host: what no launch holds is refused before
-anything else is looked at.  No GPU is needed."""
+anything else is looked at, and the sizes that the GPU tests list take the
+kernels that they are listed for.  No GPU is needed."""
+import ctypes
 import json
+import random
 import subprocess
 import sys
 
 import pytest
 
 import all_reduce_amd as ar
+from block_shapes import CUS, KERNELS
 from test_block_host import CHILD, MM, ROOT
 
 # (label, changes to a valid call, code, log): 16 bytes of k, so that weights
@@ -42,3 +46,45 @@ def results():
 def test_tiles_of_a_launch(results, label, kw, code, why):
     codes, logs = results
     assert codes[label] == ar.arResult[code] and why in logs[label], (codes[label], logs[label])
+
+
+def choice(ranks, rows, n, k, dtype, reduce, cus):
+    out = (ctypes.c_int * 4)()
+    assert ar.library().ar_block_matmul_choice(
+        ctypes.c_size_t(rows), ctypes.c_size_t(n), ctypes.c_size_t(k), int(dtype), reduce, ranks, cus, out) == 1
+    return tuple(out)
+
+
+def form(shared, reduce):
+    return "shared" if shared > 1 else "sum" if reduce else "each"
+
+
+@pytest.mark.parametrize("kernel,form_,bits,shapes", KERNELS, ids=str)
+def test_listed_sizes_take_their_kernels(kernel, form_, bits, shapes):
+    for dtype in ((0, 1) if bits == 16 else (2,)):
+        for ranks, rows, n, k in shapes:
+            *got, shared = choice(ranks, rows, n, k, dtype, int(form_ != "each"), CUS)
+            assert (tuple(got), form(shared, form_ != "each")) == (kernel, form_), (ranks, rows, n, k)
+
+
+def test_every_kernel_is_listed():
+    """Whatever a call may take, over sizes of all kinds, is in the list, with
+    whole and with ragged k."""
+    listed = {(kernel, form_, bits): shapes for kernel, form_, bits, shapes in KERNELS}
+    for shapes in listed.values():
+        assert any(k % 128 for *_, k in shapes)
+    rng, taken = random.Random(1), set()
+    for _ in range(60000):
+        ranks = rng.choice([1, 2, 3, 4, 6, 8, 16, 32])
+        rows, n, k = (int(2 ** rng.uniform(0, 13)) for _ in range(3))
+        dtype, reduce = rng.choice([0, 2]), rng.randrange(2)
+        *got, shared = choice(ranks, rows, n, 16 * -(-k // 16), dtype, reduce, CUS)
+        taken.add((tuple(got), form(shared, reduce), 32 if dtype == 2 else 16))
+    assert taken == set(listed), taken ^ set(listed)
+
+
+def test_no_choice_where_no_launch_holds_the_tiles():
+    out = (ctypes.c_int * 4)()
+    args = [ctypes.c_size_t(v) for v in (1, 1 << 30, 16)]
+    assert ar.library().ar_block_matmul_choice(*args, 0, 0, 2, CUS, out) == 0
+    assert ar.library().ar_block_matmul_choice(*args, 0, 0, 1, CUS, out) == 1
