@@ -7,8 +7,8 @@ import torch
 import all_reduce_amd as ar
 import block_ref as ref
 from gpu_util import note
-from test_gpu_block import (DT, E4M3, Planes, check_eight, comm, draw,  # noqa: F401  (comm is a fixture)
-                            run_norm)
+from test_gpu_block import (DT, E4M3, Planes, check_eight, check_norm, comm,  # noqa: F401  (a fixture)
+                            draw, run_norm)
 
 pytestmark = pytest.mark.gpu
 
@@ -163,3 +163,90 @@ def test_matmul_of_more_tiles_than_a_launch(comm):
                                torch.bfloat16, columns=at)
         ref.assert_within(out[r][:, at.cuda()], c, ref.rounded(c, tol, torch.bfloat16), f"rank {r}")
         assert not out[r].isnan().any()
+
+
+# ---- kernels for more than 64 MiB ----------------------------------------------
+def some_rows(rows, gen):
+    return torch.cat([torch.tensor([0, 1, rows - 2, rows - 1]), torch.randint(0, rows, (40,), generator=gen)])
+
+
+@pytest.mark.parametrize("quant", [False, True], ids=["same", "eight"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("ranks,rows,cols", [
+    # one, two, four and (float32) eight pieces a lane, in rows of whole pieces
+    # and not; 3 and 7 ranks leave remainders in every batch of loads
+    (3, 200_000, 65), (3, 120_000, 96), (3, 4000, 5001), (3, 4001, 5000), (7, 300, 12_345), (3, 700, 16_392),
+    (3, 500, 32_763), (3, 499, 32_768)])
+def test_norm_beyond_the_caches(comm, ranks, rows, cols, dtype, quant):
+    g = torch.Generator("cpu").manual_seed(rows + cols)
+    base = draw((997, cols), rows, DT[dtype])
+    note(f"norm beyond the caches R={ranks} {rows}x{cols} {dtype} {quant}")
+    send = Planes(ranks, rows, cols, DT[dtype])
+    for r, t in enumerate(send.ranks):  # rank r's row i: row (i + 100 r) % 997 of `base`
+        at = (torch.arange(rows) + 100 * r) % 997
+        t.copy_(base.cuda()[at.cuda()])
+    res = Planes(1, rows, cols, DT[dtype])
+    res.ranks[0].copy_(base.cuda()[((torch.arange(rows) + 500) % 997).cuda()])
+    w = (draw((cols,), 85) * 0.2 + 1).to(DT[dtype])
+    kept, out = Planes(ranks, rows, cols, DT[dtype]), Planes(ranks, rows, cols, E4M3 if quant else DT[dtype])
+    scales = Planes(ranks, ref.blocks(cols), rows, torch.float32) if quant else None
+    assert ranks * rows * cols * (2 * send.es + out.es) > 64 << 20
+    comm.all_reduce_norm(send.ranks, w.cuda(), 1e-5, res.ranks[0], kept.ranks, out.ranks,
+                         scales.ranks if quant else None)
+    torch.cuda.synchronize()
+    for p in (send, res, kept, out, scales):
+        assert p is None or p.untouched()
+    i = some_rows(rows, g)
+    x = torch.stack([base[(i + 100 * r) % 997] for r in range(ranks)])
+    check_norm(x, base[(i + 500) % 997], w, 1e-5, [t[i.cuda()] for t in kept.ranks], [t[i.cuda()] for t in out.ranks],
+               [t[:, i.cuda()] for t in scales.ranks] if quant else None, "beyond")
+    for p in (kept, out, scales):  # every rank has the same, every row
+        for t in p.ranks[1:] if p else ():
+            assert torch.equal(t.view(torch.uint8), p.ranks[0].view(torch.uint8))
+    # rows repeat after 997: all of them are like the first 997
+    for p in (kept, out):
+        t = p.ranks[0].view(torch.uint8)
+        for at in range(997, rows, 997):
+            assert torch.equal(t[at:at + 997], t[:min(997, rows - at)])
+    if quant:
+        t = scales.ranks[0]
+        for at in range(997, rows, 997):
+            assert torch.equal(t[:, at:at + 997], t[:, :min(997, rows - at)])
+
+
+@pytest.mark.parametrize("act", ["silu", "none"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("ranks,rows,cols", [
+    # blocks that are no multiple of four a group of lanes, last pieces of one
+    # element and of all but one, rows that are no multiple of a workgroup's
+    (2, 36_001, 520), (2, 18_001, 1001), (2, 14_003, 1289), (1, 40_007, 1152), (3, 90_001, 129), (2, 15, 1_200_007)])
+def test_gate_beyond_the_caches(comm, ranks, rows, cols, dtype, act):
+    g = torch.Generator("cuda").manual_seed(rows + cols)
+    wide = 2 * cols if act == "silu" else cols
+    note(f"gate beyond the caches R={ranks} {rows}x{cols} {dtype} {act}")
+    src = Planes(ranks, rows, wide, DT[dtype])
+    for t in src.ranks:
+        for part in t.split(1 << 13):
+            part.copy_(torch.randn(part.shape, generator=g, device="cuda").mul_(3))
+        if act == "silu":  # a few rows of gates far below zero, large values beside them
+            far = torch.arange(rows // 7, rows, max(1, rows // 5), device="cuda")
+            t[far, :cols] = -90.0
+            t[far, cols:] *= 1e3
+    out, scales = Planes(ranks, rows, cols, E4M3), Planes(ranks, ref.blocks(cols), rows, torch.float32)
+    assert ranks * rows * (wide * src.es + cols) > 64 << 20
+    comm.gate_quant(src.ranks, out.ranks, scales.ranks, act=act)
+    torch.cuda.synchronize()
+    assert src.untouched() and out.untouched() and scales.untouched()
+    i = some_rows(rows, torch.Generator("cpu").manual_seed(1)) if rows > 100 else torch.arange(rows)
+    i = torch.cat([i, torch.arange(rows // 7, rows, max(1, rows // 5))])
+    for r in range(ranks):
+        y, tol = ref.gate(src.ranks[r][i.cuda()].cpu(), act)
+        check_eight(out.ranks[r][i.cuda()], scales.ranks[r][:, i.cuda()], y, tol + 2.0 ** -149, f"rank {r}")
+        # all rows, coarsely: one step of e4m3
+        for at in range(0, rows, 1 << 13):
+            x = src.ranks[r][at:at + (1 << 13)].double()
+            if act == "silu":
+                x = x[:, :cols] * torch.sigmoid(x[:, :cols]) * x[:, cols:]
+            s = scales.ranks[r][:, at:at + (1 << 13)].double().t().repeat_interleave(128, 1)[:, :cols]
+            q = out.ranks[r][at:at + (1 << 13)].double()
+            assert ((q * s - x).abs() <= x.abs() * 2.0 ** -3 + s * 2.0 ** -9).all(), f"rank {r} rows from {at}"
