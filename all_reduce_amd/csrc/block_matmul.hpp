@@ -89,13 +89,13 @@ __device__ inline i32x8 pieces(const char *base, uint32_t at)
 
 // 16 bytes a lane from base + off to LDS at `to` + 16 * lane (`base` and `to`
 // are the same in every lane).  The compiler does not see the load: whoever
-// reads the bytes waits for vmcnt first.  (It never keeps a value in m0.)
+// reads the bytes waits for vmcnt first.
 __device__ inline void to_lds(const char *base, uint32_t off, uint32_t to)
 {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
                  :
                  : "s"(to), "v"(off), "s"(base)
-                 : "memory");
+                 : "memory", "m0");
 }
 
 // Four bytes a lane from an address of its own to LDS at `to` + 4 * lane.
@@ -104,7 +104,7 @@ __device__ inline void to_lds4(const char *at, uint32_t to)
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off"
                  :
                  : "s"(to), "v"(at)
-                 : "memory");
+                 : "memory", "m0");
 }
 
 // Waits until at most N of the wave's loads are under way.

@@ -4,6 +4,7 @@ kernels that they are listed for.  No GPU is needed."""
 import ctypes
 import json
 import random
+import re
 import subprocess
 import sys
 
@@ -88,3 +89,13 @@ def test_no_choice_where_no_launch_holds_the_tiles():
     args = [ctypes.c_size_t(v) for v in (1, 1 << 30, 16)]
     assert ar.library().ar_block_matmul_choice(*args, 0, 0, 2, CUS, out) == 0
     assert ar.library().ar_block_matmul_choice(*args, 0, 0, 1, CUS, out) == 1
+
+
+def test_inline_assembly_names_the_registers_it_writes():
+    """An asm statement that sets m0 says so: the compiler may keep a value there."""
+    statements = [s for f in sorted((ROOT / "all_reduce_amd" / "csrc").glob("*.h*"))
+                  for s in re.findall(r"\basm\b[^;]*;", f.read_text())]
+    setting = [s for s in statements if re.search(r"s_mov_b32 m0,", s)]
+    assert setting
+    for s in setting:
+        assert '"m0"' in s.rsplit(":", 1)[1], s
