@@ -198,33 +198,30 @@ __device__ inline float scale_of(uint32_t m)
     return s < kScaleMin ? kScaleMin : s;  // keeps NaN
 }
 
-// y / s, by s's reciprocal and one correction: the remainder is one fused
-// multiply-add, so what is rounded at the end is within 2^-46 of the quotient
-// (the product with the reciprocal alone is up to 2^-23 off).  An infinite
-// divisor (reciprocal 0) has no remainder: finite values give 0, infinite ones
-// NaN.
-struct Divisor {
-    float by, inv;
+// 1 / s in two parts, so that y / s is a product and a fused multiply-add,
+// within 2^-46 before its one rounding (the product with 1 / s alone is up to
+// 2^-23 off).  An infinite s gives 0 for finite values and NaN for infinite ones.
+struct Reciprocal {
+    float high, low;
 };
 
-__device__ inline Divisor divisor(float s)
+__device__ inline Reciprocal reciprocal(float s)
 {
-    const float inv = 1.0f / s;
-    return {inv == 0.0f ? 0.0f : s, inv};
+    const float high = 1.0f / s;
+    const float low = high * __builtin_fmaf(-high, s, 1.0f);
+    return {high, high == 0.0f ? 0.0f : low};
 }
 
-__device__ inline float quotient(float y, Divisor d)
+__device__ inline float quotient(float y, Reciprocal r)
 {
-    const float q = y * d.inv;
-    return __builtin_fmaf(__builtin_fmaf(-q, d.by, y), d.inv, q);
+    return __builtin_fmaf(y, r.high, y * r.low);
 }
 
 // The e4m3 values of y / s, rounded to nearest even, four to a word.  |y| / s
 // is at most 448 but for a few units in the last place, which round back to
-// 448, so the conversion's overflow is never reached.  (Of normally distributed
-// bfloat16 values one in 2000 is a tie between two e4m3 values or within a unit
-// of one: y * (1 / s) took it to the other side.  The correction's two
-// instructions a value cost nothing that shows: both kernels wait for memory.)
+// 448, so the conversion's overflow is never reached.  (Ties between two e4m3
+// values are common where y has few bits: y * (1 / s) took one of 2000 normal
+// bfloat16 values to the other side.)
 template <int N>
 struct Eights {
     uint32_t w[N / 4];
@@ -233,13 +230,13 @@ struct Eights {
 template <int N>
 __device__ inline Eights<N> to_eights(const float (&y)[N], float s)
 {
-    const Divisor d = divisor(s);
+    const Reciprocal r = reciprocal(s);
     Eights<N> q;
 #pragma unroll
     for (int i = 0; i < N / 4; ++i) {
         int w = 0;
-        w = __builtin_amdgcn_cvt_pk_fp8_f32(quotient(y[4 * i], d), quotient(y[4 * i + 1], d), w, false);
-        w = __builtin_amdgcn_cvt_pk_fp8_f32(quotient(y[4 * i + 2], d), quotient(y[4 * i + 3], d), w, true);
+        w = __builtin_amdgcn_cvt_pk_fp8_f32(quotient(y[4 * i], r), quotient(y[4 * i + 1], r), w, false);
+        w = __builtin_amdgcn_cvt_pk_fp8_f32(quotient(y[4 * i + 2], r), quotient(y[4 * i + 3], r), w, true);
         q.w[i] = (uint32_t)w;
     }
     return q;
