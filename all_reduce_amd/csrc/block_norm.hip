@@ -204,8 +204,10 @@ __global__ __launch_bounds__(1024) void norm_rows(NormArgs p)
                        __builtin_bit_cast(int, total / (float)p.cols + p.eps)));
         float inv;
         int up = 0;
-        if (mean >= 0x1p-80f && mean <= 0x1p120f) {
-            inv = inverse_root(mean);
+        if (std::is_same<T, Fp16>::value || (mean >= 0x1p-80f && mean <= 0x1p120f)) {
+            // (33 float16 values and their squares stay in range, but for
+            // infinities; of a row of zeros without eps NaN is to come)
+            inv = mean < __builtin_inff() ? inverse_root(mean) : 1.0f / __builtin_sqrtf(mean);
         } else {
             // h * inv is scaled by 2^-up and 2^up, with which the root lies in
             // [0.7, 1.5).  (`wide` is written again only behind the next row's

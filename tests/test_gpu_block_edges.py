@@ -79,6 +79,23 @@ def test_norm_of_one_large_value(comm, dtype):
     ref.assert_within(out[0][1], want, tol, "large")
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("eps", [1e-42, 3e38])
+def test_norm_with_eps_at_the_ends(comm, dtype, eps):
+    """The smallest and the largest eps: rows of zeros stay zero, others are
+    divided by the root of the sum."""
+    x = draw((2, 3, 300), 86, DT[dtype])
+    x[:, 1] = 0
+    w = (draw((300,), 87) * 0.2 + 1).to(DT[dtype])
+    eps = torch.tensor(eps).item()  # as binary32
+    _, out, _ = run_norm(comm, x, None, w, eps, False, False)
+    _, _, y, y_tol = ref.norm(x, None, w, eps)
+    y_tol = y_tol + 2.0 ** -150 * (1 + w.double().abs())
+    for t in out:
+        assert (t[1] == 0).all()
+        ref.assert_within(t[[0, 2]], y[[0, 2]], ref.rounded(y, y_tol, DT[dtype])[[0, 2]], "eps")
+
+
 def test_norm_rounds_as_often_as_the_division(comm):
     """float32 rows of 64 values alike but for their signs: their sum of squares
     and its mean are exact, so an output has the rounding of eps added (halved
