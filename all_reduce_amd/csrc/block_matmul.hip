@@ -164,7 +164,7 @@ uint64_t ceil_div(uint64_t a, uint64_t b) { return (a + b - 1) / b; }
 
 }  // namespace
 
-// The kernels for three rows and more: tiles of rows x columns whose `waves`
+// The kernels for any number of rows: tiles of rows x columns whose `waves`
 // share k, `resident` workgroups to a compute unit, and the time they take (us)
 //
 //     base + each * Q + MB written / 4
@@ -289,9 +289,10 @@ bool choose_matmul(const MatmulArgs &args, int out_dtype, bool reduce, int cu_co
             }
         }
     }
-    // One or two rows take the kernel made for them, unless sharing k among
-    // workgroups wins (8 x (1 x 512 x 8192) summed, for example: 14 in place of
-    // 41 us).
+    // One or two rows take the kernel made for them, but where the model would
+    // have workgroups share k: it has few columns there, and too few workgroups
+    // (8 x (1 x 512 x 8192) summed: 14 in place of 41 us).  The model does not
+    // know that kernel's own time.
     if (args.rows <= 2 && best_split == 1u && 32.0 * args.n * args.nranks < kMostThreads) {
         *choice = {16u, 16u, kRowsWaves, 1u};
         return true;

@@ -1,5 +1,5 @@
 // block_matmul_mid.hip -- the block-scaled 8-bit product for a decode batch
-// (three rows to a few hundred).
+// (three rows to a few hundred; one or two where workgroups share k).
 //
 // It is bound by reading the weights, so each weight byte goes through a
 // compute unit once a tile of rows, and the reads are kept deep: a wave has a

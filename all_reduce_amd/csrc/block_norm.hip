@@ -19,9 +19,9 @@
 //
 // It is bound by memory: R + 1 reads and 2 R writes a column at two or three
 // operations each.  On MI355X 8 x 8192 x 8192 bfloat16 with residual takes
-// 650 us (5.2 TB/s; a large copy runs at 5.1), 16 x 1024 x 7168 float32 with
-// an 8-bit output 211 us (5.1 TB/s).  In a graph one row of 8 x 8192 takes
-// 4.4 us (5.5 with one workgroup a row) and 64 rows 7.2, bound by a row's chain
+// 656 us (5.1 TB/s; a large copy runs at 5.1), 16 x 1024 x 7168 float32 with
+// an 8-bit output 210 us (5.2 TB/s).  In a graph one row of 8 x 8192 takes
+// 4.4 us (5.5 with one workgroup a row) and 64 rows 6.9, bound by a row's chain
 // of loads, sum and stores.
 #include <type_traits>
 
