@@ -200,7 +200,8 @@ __device__ inline float scale_of(uint32_t m)
 
 // 1 / s in two parts, so that y / s is a product and a fused multiply-add,
 // within 2^-46 before its one rounding (the product with 1 / s alone is up to
-// 2^-23 off).  An infinite s gives 0 for finite values and NaN for infinite ones.
+// 2^-23 off; above s = 2^100 the low part has fewer bits, down to 2^-30).  An
+// infinite s gives 0 for finite values and NaN for infinite ones.
 struct Reciprocal {
     float high, low;
 };

@@ -34,8 +34,8 @@ __device__ inline bf16x8 widen_eight(i32x8 x, int s)
 // one's leading bit, and the groups' sums are added in binary32.  Measured on
 // MI355X: normal inputs come out 1.4e-5 off in the 2-norm (a binary32 sum is
 // 1e-7 off).  That is far below an output's rounding to 16 bits (up to 2^-8 and
-// 2^-11 of a value), so 16-bit outputs take it; a binary32 output (EXACT) would show it,
-// so there the values are widened to bfloat16, which holds them exactly, and
+// 2^-11 of a value), so 16-bit outputs take it; a binary32 output (EXACT) would
+// show it, so there the values are widened to bfloat16, which holds them exactly, and
 // multiplied at that type's rate, a third of the 8-bit one (1320 against 4460
 // TFLOP/s of instructions alone), to binary32 sums 1e-8 off.
 template <bool EXACT>

@@ -29,7 +29,8 @@
  *
  * Quantisation of a block of values y:
  *     s = max(max|y| / 448, 2^-126);  q = y / s rounded to nearest even
- * (both quotients are rounded to binary32 first).
+ * (both quotients are rounded to binary32 first; the second may be a unit off in
+ * blocks whose scale is above 2^100).
  * A block that holds a NaN has the scale NaN; one that holds an infinity and
  * no NaN the scale infinity, with which its finite values become 0 and its
  * infinities NaN.  A block of zeros has the scale 2^-126.
@@ -68,8 +69,9 @@ extern "C" {
  *
  * The norm is taken of h before its rounding to the element type.  The sum of
  * squares is binary32, or binary64 for rows whose mean that does not hold, so
- * that rows of any finite values have a norm.  A row that holds an infinity gives zeros but NaN at the infinity; a
- * row with a NaN is NaN, and so is a row of zeros with eps 0.
+ * that rows of any finite values have a norm.  A row that holds an infinity
+ * gives zeros but NaN at the infinity; a row with a NaN is NaN, and so is a row
+ * of zeros with eps 0.
  *
  *  sendbufs     host array of nranks device pointers, each [rows, cols] dense.
  *  residual     device pointer, [rows, cols] dense: the residual stream, which
@@ -126,11 +128,12 @@ arResult_t arGateQuant(const void *const *inbufs, void *const *outbufs, float *c
  * with binary32 sums and one rounding to outDtype.  The order of a sum follows
  * from rows, n, k, outDtype, reduce, nranks and the card's number of compute
  * units, never from values or from other calls.  as * bs is rounded to binary32
- * before the block's sum is multiplied by it.  Where outDtype is arFloat32 every product is
- * exact; for the 16-bit types the matrix instruction adds eight products at a
- * time after cutting each, toward zero, at 2^-13 of the leading bit of the
- * largest of them, which on normally distributed values leaves the sums
- * 1.4e-5 off (the rounding to bfloat16 or float16 leaves 1.7e-3 or 2.1e-4).
+ * before the block's sum is multiplied by it.
+ * Where outDtype is arFloat32 every product is exact; for the 16-bit types the
+ * matrix instruction adds eight products at a time after cutting each, toward
+ * zero, at 2^-13 of the leading bit of the largest of them, which on normally
+ * distributed values leaves the sums 1.4e-5 off (the rounding to bfloat16 or
+ * float16 leaves 1.7e-3 or 2.1e-4).
  *
  *  abufs, ascales  host arrays of nranks device pointers: activations
  *                  [rows, k] of 8-bit values, dense, and [ceil(k / 128)][rows].

@@ -37,6 +37,20 @@ def test_quantisation_is_the_quotient(comm, rows, cols, dtype):
     assert not off.any(), f"{int(off.sum())} of {off.numel()} values"
 
 
+@pytest.mark.parametrize("dtype,size", [("bf16", 6e37), ("fp32", 6e37), ("bf16", 1e-36), ("bf16", 1e-39),
+                                        ("fp32", 1e-36), ("fp32", 1e-43), ("fp16", 1e-7), ("fp16", 1e4)])
+def test_quantisation_at_the_ends_of_a_type(comm, dtype, size):
+    """The largest scales, and values that the smallest one holds as few steps."""
+    x = (draw((300, 520), 92).clamp(-5, 5) * size).to(DT[dtype])
+    note(f"quantisation {dtype} {size}")
+    src = Planes(1, 300, 520, DT[dtype]).fill([x])
+    out, scales = Planes(1, 300, 520, E4M3), Planes(1, 5, 300, torch.float32)
+    comm.gate_quant(src.ranks, out.ranks, scales.ranks, act="none")
+    torch.cuda.synchronize()
+    assert src.untouched() and out.untouched() and scales.untouched()
+    check_eight(out.ranks[0], scales.ranks[0], x.double(), torch.zeros_like(x, dtype=torch.float64), "ends")
+
+
 # ---- norm ------------------------------------------------------------------------
 @pytest.mark.parametrize("quant", [False, True], ids=["same", "eight"])
 @pytest.mark.parametrize("dtype,sizes", [("bf16", (1e-38, 1e-30, 1e-15, 1.0, 1e15, 1e25, 1e37)),
