@@ -1,8 +1,8 @@
 """Python binding of the MI355X sum all-reduce over R simulated ranks, and of
-the operators around it in a tensor-parallel layer.
+the operators around it in a tensor-parallel layer, its key-value cache among them.
 
-The functions named ``ar*`` are the C ABI of ``include/ar_allreduce.h`` and
-``include/ar_block.h``, one for one, over ctypes: arguments are marshalled and
+The functions named ``ar*`` are the C ABI of ``include/ar_allreduce.h``,
+``include/ar_block.h`` and ``include/ar_cache.h``, one for one, over ctypes: arguments are marshalled and
 the result code is returned, nothing else happens here.  :class:`Comm` and :func:`rank_buffers`
 are conveniences on top for torch tensors; torch supplies device memory and
 streams only.  Every step of the all-reduce runs in the HIP kernels of
@@ -19,6 +19,7 @@ from typing import Sequence
 LIBRARY = Path(__file__).resolve().parent / "_lib" / "libar_allreduce.so"
 HEADER = Path(__file__).resolve().parent.parent / "include" / "ar_allreduce.h"
 BLOCK_HEADER = HEADER.with_name("ar_block.h")
+CACHE_HEADER = HEADER.with_name("ar_cache.h")
 
 
 class arResult(IntEnum):
@@ -73,6 +74,7 @@ class arActivation(IntEnum):
 
 AR_SCALE_BLOCK = 128
 AR_NORM_MAX_COLS = 32768
+AR_CACHE_MAX_DIM = 256
 
 AR_MAX_RANKS = 32
 AR_NOALLOC_SCRATCH_BYTES = 64 << 20
@@ -93,6 +95,14 @@ class arLaunchInfo(ctypes.Structure):
                 ("staged", ctypes.c_int), ("packetPayloadBytes", ctypes.c_int)]
 
 
+class arCacheLayout(ctypes.Structure):
+    """Mirror of arCacheLayout_t."""
+    _fields_ = [("pages", ctypes.c_size_t), ("pageTokens", ctypes.c_size_t),
+                ("heads", ctypes.c_size_t), ("dim", ctypes.c_size_t),
+                ("pageStride", ctypes.c_size_t), ("headStride", ctypes.c_size_t),
+                ("tokenStride", ctypes.c_size_t)]
+
+
 class ArError(RuntimeError):
     def __init__(self, code: int, where: str):
         self.code = arResult(code)
@@ -111,7 +121,7 @@ def library() -> ctypes.CDLL:
         raise RuntimeError(f"{LIBRARY} is missing: build it with `python -m all_reduce_amd.build`")
     lib = ctypes.CDLL(str(LIBRARY))
     vp, i32, i64, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
-    pvp = ctypes.POINTER(vp)
+    pvp, layout = ctypes.POINTER(vp), ctypes.POINTER(arCacheLayout)
     sig = {
         "arCommCreate": ([ctypes.POINTER(vp), i32, i32, sz], i32),
         "arCommDestroy": ([vp], i32),
@@ -130,6 +140,11 @@ def library() -> ctypes.CDLL:
                             i32),
         "arGateQuant": ([pvp, pvp, pvp, sz, sz, i32, i32, i32, vp, vp], i32),
         "arMatmulScaled": ([pvp, pvp, pvp, pvp, pvp, sz, sz, sz, i32, i32, i32, vp, vp], i32),
+        "arCacheWrite": ([pvp, pvp, sz, vp, sz, layout, pvp, pvp, pvp, pvp, i32, i32, vp, vp], i32),
+        "arCacheRead": ([vp, sz, layout, pvp, pvp, pvp, pvp, pvp, pvp, sz, i32, i32, vp, vp], i32),
+        "arCacheAttention": ([pvp, sz, layout, pvp, pvp, pvp, pvp, vp, sz, vp, sz, sz,
+                              ctypes.c_float, sz, pvp, pvp, pvp, vp, sz, i32, i32, vp, vp], i32),
+        "arCacheAttentionWorkspace": ([sz, vp, ctypes.POINTER(sz)], i32),
         "arGetErrorString": ([i32], ctypes.c_char_p),
         "arGetVersion": ([], i32),
     }
@@ -264,6 +279,47 @@ def arMatmulScaled(abufs, ascales, bbufs, bscales, outbufs, rows: int, n: int, k
         _pointer_array(bbufs, nranks), _pointer_array(bscales, nranks),
         _pointer_array(outbufs, nranks), rows, n, k, int(out_dtype), int(reduce), nranks, comm,
         stream)
+
+
+def arCacheWrite(keys, values, row_stride: int, slots, tokens: int, cache, key_pages, value_pages,
+                 key_scales, value_scales, dtype: int, nranks: int, comm, stream) -> int:
+    """Device pointers as integers, sequences of them for the rank tables;
+    ``cache`` an arCacheLayout; ``None`` passes NULL."""
+    return library().arCacheWrite(
+        _pointer_array(keys, nranks), _pointer_array(values, nranks), row_stride, slots, tokens,
+        cache, _pointer_array(key_pages, nranks), _pointer_array(value_pages, nranks),
+        _pointer_array(key_scales, nranks), _pointer_array(value_scales, nranks), int(dtype),
+        nranks, comm, stream)
+
+
+def arCacheRead(slots, tokens: int, cache, key_pages, value_pages, key_scales, value_scales, keys,
+                values, row_stride: int, dtype: int, nranks: int, comm, stream) -> int:
+    """As arCacheWrite."""
+    return library().arCacheRead(
+        slots, tokens, cache, _pointer_array(key_pages, nranks),
+        _pointer_array(value_pages, nranks), _pointer_array(key_scales, nranks),
+        _pointer_array(value_scales, nranks), _pointer_array(keys, nranks),
+        _pointer_array(values, nranks), row_stride, int(dtype), nranks, comm, stream)
+
+
+def arCacheAttention(queries, query_stride: int, cache, key_pages, value_pages, key_scales,
+                     value_scales, page_table, table_pages: int, lengths, seqs: int, heads: int,
+                     scale: float, window: int, outbufs, out_scales, lse, workspace,
+                     workspace_bytes: int, dtype: int, nranks: int, comm, stream) -> int:
+    """As arCacheWrite."""
+    return library().arCacheAttention(
+        _pointer_array(queries, nranks), query_stride, cache, _pointer_array(key_pages, nranks),
+        _pointer_array(value_pages, nranks), _pointer_array(key_scales, nranks),
+        _pointer_array(value_scales, nranks), page_table, table_pages, lengths, seqs, heads, scale,
+        window, _pointer_array(outbufs, nranks), _pointer_array(out_scales, nranks),
+        _pointer_array(lse, nranks), workspace, workspace_bytes, int(dtype), nranks, comm, stream)
+
+
+def arCacheAttentionWorkspace(dim: int, comm):
+    """Returns (result code, bytes)."""
+    n = ctypes.c_size_t(0)
+    r = library().arCacheAttentionWorkspace(dim, comm, ctypes.byref(n))
+    return r, n.value
 
 
 # ---- torch conveniences ---------------------------------------------------
@@ -540,6 +596,184 @@ class Comm:
             _rank_table(a), _rank_table(a_scales), _rank_table(b), _rank_table(b_scales),
             _rank_table(out), rows, cols, k, int(dtype_code(dtype)), int(bool(reduce)), n),
             self._stream(stream), (a, a_scales, b, b_scales, out))
+
+    def cache_write(self, keys, values, slots, key_pages, value_pages, key_scales=None,
+                    value_scales=None, stream=None):
+        """New tokens' keys and values into the paged cache (see arCacheWrite).
+        Lists of one tensor a rank: ``keys`` and ``values`` [tokens, heads, dim],
+        which may be parts of the wider rows of a product; ``key_pages`` and
+        ``value_pages`` [pages, heads, tokens of a page, dim] in any order of memory
+        whose last dimension is dense, of the element type, or torch.float8_e4m3fn
+        with ``key_scales`` and ``value_scales`` float32 [pages, heads, tokens of a
+        page].  ``slots``, int64 [tokens], is the ranks' common one; tokens whose
+        slot is negative are skipped."""
+        self.prepare_cache_write(keys, values, slots, key_pages, value_pages, key_scales,
+                                 value_scales, stream)()
+
+    def prepare_cache_write(self, keys, values, slots, key_pages, value_pages, key_scales=None,
+                            value_scales=None, stream=None) -> "PreparedCall":
+        """``cache_write`` with its arguments marshalled once (see ``prepare``)."""
+        dtype, n = self._rows(keys, "keys").dtype, len(keys)
+        layout = self._pages(key_pages, value_pages, key_scales, value_scales, n, dtype)
+        stride = self._check_rows(keys, values, slots, layout, dtype)
+        return PreparedCall(self, "arCacheWrite", (
+            _rank_table(keys), _rank_table(values), stride, slots.data_ptr(), slots.numel(), layout,
+            _rank_table(key_pages), _rank_table(value_pages), _rank_table(key_scales),
+            _rank_table(value_scales), int(dtype_code(dtype)), n), self._stream(stream),
+            (keys, values, slots, key_pages, value_pages, key_scales, value_scales))
+
+    def cache_read(self, slots, key_pages, value_pages, keys, values, key_scales=None,
+                   value_scales=None, stream=None):
+        """The cached rows of ``slots`` into ``keys`` and ``values`` (see arCacheRead;
+        shapes as for ``cache_write``).  Rows whose slot is negative are left as
+        they were.  Returns ``(keys, values)``."""
+        self.prepare_cache_read(slots, key_pages, value_pages, keys, values, key_scales,
+                                value_scales, stream)()
+        return keys, values
+
+    def prepare_cache_read(self, slots, key_pages, value_pages, keys, values, key_scales=None,
+                           value_scales=None, stream=None) -> "PreparedCall":
+        """``cache_read`` with its arguments marshalled once (see ``prepare``)."""
+        dtype, n = self._rows(keys, "keys").dtype, len(keys)
+        layout = self._pages(key_pages, value_pages, key_scales, value_scales, n, dtype)
+        stride = self._check_rows(keys, values, slots, layout, dtype)
+        return PreparedCall(self, "arCacheRead", (
+            slots.data_ptr(), slots.numel(), layout, _rank_table(key_pages),
+            _rank_table(value_pages), _rank_table(key_scales), _rank_table(value_scales),
+            _rank_table(keys), _rank_table(values), stride, int(dtype_code(dtype)), n),
+            self._stream(stream),
+            (keys, values, slots, key_pages, value_pages, key_scales, value_scales))
+
+    def cache_attention(self, queries, key_pages, value_pages, page_table, lengths, out,
+                        key_scales=None, value_scales=None, scale: float | None = None,
+                        window: int = 0, out_scales=None, lse=None, workspace=None, stream=None):
+        """Attention of one new token a sequence over the paged cache (see
+        arCacheAttention).  Lists of one tensor a rank: ``queries`` [seqs, heads,
+        dim], which may be parts of the wider rows of a product; the cache as for
+        ``cache_write``; ``out`` [seqs, heads, dim] of the element type, or
+        torch.float8_e4m3fn with ``out_scales`` float32 [heads * dim / 128, seqs];
+        ``lse`` (or None: not wanted) float32 [seqs, heads].  ``page_table`` int32
+        [seqs, pages of a sequence] and ``lengths`` int32 [seqs] are the ranks'
+        common ones.  ``scale``: 1 / sqrt(dim) if None; ``window``: attend to the
+        last tokens alone, 0: to all.  ``workspace``: one of ``cache_workspace``
+        that no other call uses at the same time; None: one of the call's own.
+        Returns ``out``."""
+        self.prepare_cache_attention(queries, key_pages, value_pages, page_table, lengths, out,
+                                     key_scales, value_scales, scale, window, out_scales, lse,
+                                     workspace, stream)()
+        return out
+
+    def prepare_cache_attention(self, queries, key_pages, value_pages, page_table, lengths, out,
+                                key_scales=None, value_scales=None, scale: float | None = None,
+                                window: int = 0, out_scales=None, lse=None, workspace=None,
+                                stream=None) -> "PreparedCall":
+        """``cache_attention`` with its arguments marshalled once (see ``prepare``).
+        The workspace is part of the prepared call, so calls that may run at once
+        need to be prepared apart."""
+        torch = _torch()
+        first, n = self._rows(queries, "queries"), len(queries)
+        dtype = first.dtype
+        seqs, heads, dim = first.shape
+        layout = self._pages(key_pages, value_pages, key_scales, value_scales, n, dtype)
+        if layout.dim != dim:
+            raise ValueError(f"queries of {dim}, cache of {layout.dim}")
+        stride = self._strided("queries", queries, n, (seqs, heads, dim), dtype)
+        self._check("out", out, n, (seqs, heads, dim), dtype if out_scales is None else torch.float8_e4m3fn)
+        if out_scales is not None:
+            self._check("out_scales", out_scales, n, (scale_blocks(heads * dim), seqs), torch.float32)
+        if lse is not None:
+            self._check("lse", lse, n, (seqs, heads), torch.float32)
+        if page_table.dim() != 2:
+            raise ValueError("page_table: need [seqs, pages of a sequence]")
+        self._check("page_table", [page_table], 1, (seqs, page_table.shape[1]), torch.int32)
+        self._check("lengths", [lengths], 1, (seqs,), torch.int32)
+        if workspace is None:
+            workspace = self.cache_workspace(dim, stream)
+        elif workspace.device != self.device or not workspace.is_contiguous():
+            raise ValueError("the workspace must be a contiguous tensor on the communicator's device")
+        return PreparedCall(self, "arCacheAttention", (
+            _rank_table(queries), stride, layout, _rank_table(key_pages), _rank_table(value_pages),
+            _rank_table(key_scales), _rank_table(value_scales), page_table.data_ptr(),
+            page_table.shape[1], lengths.data_ptr(), seqs, heads,
+            float(dim ** -0.5 if scale is None else scale), int(window), _rank_table(out),
+            _rank_table(out_scales), _rank_table(lse), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), int(dtype_code(dtype)), n),
+            self._stream(stream), (queries, key_pages, value_pages, key_scales, value_scales,
+                                   page_table, lengths, out, out_scales, lse, workspace))
+
+    def cache_workspace(self, dim: int, stream=None):
+        """A workspace for ``cache_attention`` with heads of ``dim``, ready on
+        ``stream`` (default: the current one).  Calls one after the other may share
+        it; calls that may run at once need one each."""
+        torch = _torch()
+        r, n = arCacheAttentionWorkspace(dim, self.handle)
+        if r != 0:
+            raise ArError(r, "arCacheAttentionWorkspace")
+        with torch.cuda.stream(torch.cuda.current_stream(self.device) if stream is None else stream):
+            return torch.zeros(n, dtype=torch.uint8, device=self.device)
+
+    @staticmethod
+    def _rows(tensors, name):
+        """The first of a list of [rows, heads, dim] tensors."""
+        if not tensors or tensors[0].dim() != 3:
+            raise ValueError(f"{name}: need one three-dimensional tensor per rank")
+        return tensors[0]
+
+    def _strided(self, name, tensors, count, shape, dtype, stride=None):
+        """Checks [rows, heads, dim] tensors with dense rows; returns the elements
+        from one row to the next, the same for all (``stride`` if given)."""
+        if len(tensors) != count:
+            raise ValueError(f"{name}: need {count} tensors, got {len(tensors)}")
+        rows, heads, dim = shape
+        if stride is None:
+            stride = tensors[0].stride(0) if rows > 1 else heads * dim
+        want = (stride, dim, 1)
+        for t in tensors:
+            if t.device != self.device:
+                raise ValueError(f"{name}: tensor on {t.device}, communicator on {self.device}")
+            if tuple(t.shape) != shape or t.dtype != dtype:
+                raise ValueError(f"{name}: need {shape} of {dtype}, got {tuple(t.shape)} of "
+                                 f"{t.dtype}")
+            if any(n > 1 and a != b for n, a, b in zip(shape, t.stride(), want)):
+                raise ValueError(f"{name}: need dense rows, equally far apart in all tensors")
+        return stride
+
+    def _check_rows(self, keys, values, slots, layout, dtype):
+        """Checks the rows of a write or read; returns their stride."""
+        torch = _torch()
+        if slots.dim() != 1:
+            raise ValueError("slots: need [tokens]")
+        self._check("slots", [slots], 1, (slots.shape[0],), torch.int64)
+        shape = (slots.shape[0], layout.heads, layout.dim)
+        stride = self._strided("keys", keys, len(keys), shape, dtype)
+        return self._strided("values", values, len(keys), shape, dtype, stride)
+
+    def _pages(self, key_pages, value_pages, key_scales, value_scales, count, dtype):
+        """Checks a cache's tensors; returns its layout."""
+        torch = _torch()
+        if (key_scales is None) != (value_scales is None):
+            raise ValueError("need scales of keys and of values, or of neither")
+        if not key_pages or key_pages[0].dim() != 4:
+            raise ValueError("key_pages: need one four-dimensional tensor per rank")
+        shape, strides = tuple(key_pages[0].shape), key_pages[0].stride()
+        want = dtype if key_scales is None else torch.float8_e4m3fn
+        for name, tensors in (("key_pages", key_pages), ("value_pages", value_pages)):
+            if len(tensors) != count:
+                raise ValueError(f"{name}: need {count} tensors, got {len(tensors)}")
+            for t in tensors:
+                if t.device != self.device:
+                    raise ValueError(f"{name}: tensor on {t.device}, communicator on {self.device}")
+                if tuple(t.shape) != shape or t.dtype != want:
+                    raise ValueError(f"{name}: need {shape} of {want}, got {tuple(t.shape)} of "
+                                     f"{t.dtype}")
+                if t.stride(3) != 1 or any(n > 1 and a != b
+                                           for n, a, b in zip(shape, t.stride(), strides)):
+                    raise ValueError(f"{name}: need dense rows and the same strides in all tensors")
+        if key_scales is not None:
+            self._check("key_scales", key_scales, count, shape[:3], torch.float32)
+            self._check("value_scales", value_scales, count, shape[:3], torch.float32)
+        pages, heads, tokens, dim = shape
+        return arCacheLayout(pages, tokens, heads, dim, strides[0], strides[1], strides[2])
 
     @staticmethod
     def _matrix(tensors):

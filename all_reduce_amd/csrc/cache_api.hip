@@ -1,0 +1,285 @@
+// cache_api.hip -- the entry points declared in include/ar_cache.h: argument
+// checks on the host without touching the device, then one launch on the
+// caller's stream.
+#include <math.h>
+
+#include "api_checks.hpp"
+#include "cache_internal.hpp"
+
+using namespace ar;
+
+namespace {
+
+typedef unsigned __int128 u128;
+
+constexpr size_t kMostHeads = 4096, kMostSeqs = 65536;
+
+// The layout in the kernels' form, and the elements from a pool's first to its
+// last.  Strides of which there is only one step do not count.
+arResult_t check_layout(const arCacheLayout_t *c, size_t page_bytes, CacheShape *shape,
+                        size_t *span)
+{
+    if (c == nullptr)
+        return reject(arInvalidArgument, "NULL cache layout");
+    if (c->dim < 16 || c->dim > AR_CACHE_MAX_DIM || c->dim % 16 != 0)
+        return reject(arUnsupported, "dim must be a multiple of 16 in 16..256");
+    if (c->heads < 1 || c->heads > kMostHeads)
+        return reject(arUnsupported, "cache heads must be in 1..4096");
+    if (c->pages < 1 || c->pageTokens < 1 || c->pages > INT32_MAX || c->pageTokens > INT32_MAX ||
+        c->pages * c->pageTokens > INT32_MAX)
+        return reject(arInvalidArgument, "pages * pageTokens must be in 1..2^31 - 1");
+    struct Step {
+        size_t count, stride;
+    } steps[3] = {{c->pages, c->pageStride}, {c->heads, c->headStride}, {c->pageTokens, c->tokenStride}};
+    std::sort(steps, steps + 3, [](const Step &a, const Step &b) { return a.stride < b.stride; });
+    u128 extent = c->dim;
+    for (const Step &s : steps) {
+        if (s.count == 1)
+            continue;
+        if (s.stride % (16 / page_bytes) != 0)
+            return reject(arInvalidArgument, "cache strides must be multiples of 16 bytes");
+        if (s.stride < extent)
+            return reject(arInvalidArgument, "rows of the cache overlap");
+        extent += (u128)(s.count - 1) * s.stride;
+        if (extent > SIZE_MAX >> 4)
+            return reject(arInvalidArgument, "cache too large");
+    }
+    shape->page_stride = c->pages > 1 ? c->pageStride : 0;
+    shape->head_stride = c->heads > 1 ? c->headStride : 0;
+    shape->token_stride = c->pageTokens > 1 ? c->tokenStride : 0;
+    shape->pages = (uint32_t)c->pages;
+    shape->page_tokens = (uint32_t)c->pageTokens;
+    shape->heads = (uint32_t)c->heads;
+    shape->dim = (uint32_t)c->dim;
+    *span = (size_t)extent;
+    return arSuccess;
+}
+
+// Rows of `heads` * dim elements `stride` apart: the elements from the first to
+// the last.
+arResult_t check_rows(size_t rows, size_t row, size_t stride, int dtype, size_t *span)
+{
+    if (stride < row || stride % (16 / elem_bytes(dtype)) != 0)
+        return reject(arInvalidArgument, "a row stride must hold a row and be a multiple of 16 bytes");
+    const u128 most = (u128)(rows - 1) * stride + row;
+    if (most > SIZE_MAX >> 4)
+        return reject(arInvalidArgument, "too many rows");
+    *span = (size_t)most;
+    return arSuccess;
+}
+
+// The ranges of a rank's keys and values, written both, which may be parts of
+// the same blocks: `inner` bytes of each of `count` blocks `stride` apart.
+bool add_pair(Ranges *mem, const void *a, const void *b, size_t bytes, size_t inner, size_t stride,
+              size_t count)
+{
+    const uintptr_t lo = std::min((uintptr_t)a, (uintptr_t)b), hi = std::max((uintptr_t)a, (uintptr_t)b);
+    const size_t apart = hi - lo;
+    if (lo != 0 && count > 1 && (lo & 15u) == 0 && (hi & 15u) == 0 && apart < bytes &&
+        apart >= inner && apart + inner <= stride)
+        return mem->add((const void *)lo, apart + bytes, true);
+    return mem->add(a, bytes, true) && mem->add(b, bytes, true);
+}
+
+struct Copy {
+    const void *const *rows[2];
+    const void *const *pages[2];
+    const float *const *scales[2];
+};
+
+// arCacheWrite and arCacheRead: `write` says which side is written.
+arResult_t copy(const Copy &c, bool write, size_t row_stride, const int64_t *slots, size_t tokens,
+                const arCacheLayout_t *cache, arDataType_t dtype_arg, int nranks, arComm_t comm,
+                arStream_t stream)
+{
+    const int dtype = raw(dtype_arg);
+    if (!is_dtype(dtype))
+        return reject(arUnsupported, "dtype must be bf16, fp16 or fp32");
+    if (nranks < 1 || nranks > AR_MAX_RANKS)
+        return reject(arUnsupported, "nranks must be in 1..32");
+    const bool eight = c.scales[0] != nullptr;
+    if (eight != (c.scales[1] != nullptr))
+        return reject(arInvalidArgument, "scales of keys and of values, or of neither");
+    const size_t page_bytes = eight ? 1 : elem_bytes(dtype);
+    CacheCopyArgs args = {};
+    size_t span, row_span;
+    arResult_t r = check_layout(cache, page_bytes, &args.cache, &span);
+    if (r != arSuccess)
+        return r;
+    if (tokens == 0)
+        return arSuccess;
+    if (tokens > INT32_MAX)
+        return reject(arInvalidArgument, "tokens must be below 2^31");
+    const size_t row = cache->heads * cache->dim, es = elem_bytes(dtype);
+    r = check_rows(tokens, row, row_stride, dtype, &row_span);
+    if (r != arSuccess)
+        return r;
+    for (int i = 0; i < 2; ++i)
+        if (c.rows[i] == nullptr || c.pages[i] == nullptr)
+            return reject(arInvalidArgument, "NULL buffer array");
+    Ranges mem;
+    const size_t places = cache->pages * cache->pageTokens * cache->heads;
+    // what keys take of a page, if pages are the outermost step
+    const size_t page_span = span - (cache->pages - 1) * args.cache.page_stride;
+    bool ok = mem.add(slots, tokens * sizeof(int64_t), false, 8);
+    for (int i = 0; i < nranks && ok; ++i) {
+        if (write) {
+            ok = mem.add(c.rows[0][i], row_span * es, false) &&
+                 mem.add(c.rows[1][i], row_span * es, false) &&
+                 add_pair(&mem, c.pages[0][i], c.pages[1][i], span * page_bytes,
+                          page_span * page_bytes, cache->pageStride * page_bytes, cache->pages);
+        } else {
+            ok = mem.add(c.pages[0][i], span * page_bytes, false) &&
+                 mem.add(c.pages[1][i], span * page_bytes, false) &&
+                 add_pair(&mem, c.rows[0][i], c.rows[1][i], row_span * es, row * es,
+                          row_stride * es, tokens);
+        }
+        for (int k = 0; k < 2 && eight && ok; ++k)
+            ok = mem.add(c.scales[k][i], places * sizeof(float), write);
+    }
+    if (!ok || !mem.disjoint())
+        return reject(arInvalidArgument, mem.why());
+    r = check_comm(comm);
+    if (r != arSuccess)
+        return r;
+    for (int i = 0; i < nranks; ++i)
+        for (int k = 0; k < 2; ++k) {
+            args.rows[k][i] = (char *)c.rows[k][i];
+            args.pages[k][i] = (char *)c.pages[k][i];
+            args.scales[k][i] = eight ? (float *)c.scales[k][i] : nullptr;
+        }
+    args.slots = slots;
+    args.row_stride = row_stride;
+    args.tokens = (uint32_t)tokens;
+    return launched(write ? launch_cache_write(args, dtype, eight, nranks, comm->cu_count, (hipStream_t)stream)
+                          : launch_cache_read(args, dtype, eight, nranks, comm->cu_count, (hipStream_t)stream));
+}
+
+}  // namespace
+
+extern "C" {
+
+arResult_t arCacheWrite(const void *const *keys, const void *const *values, size_t rowStride,
+                        const int64_t *slots, size_t tokens, const arCacheLayout_t *cache,
+                        void *const *keyPages, void *const *valuePages, float *const *keyScales,
+                        float *const *valueScales, arDataType_t dtype, int nranks, arComm_t comm,
+                        arStream_t stream)
+{
+    return copy({{keys, values}, {keyPages, valuePages}, {keyScales, valueScales}}, true, rowStride,
+                slots, tokens, cache, dtype, nranks, comm, stream);
+}
+
+arResult_t arCacheRead(const int64_t *slots, size_t tokens, const arCacheLayout_t *cache,
+                       const void *const *keyPages, const void *const *valuePages,
+                       const float *const *keyScales, const float *const *valueScales,
+                       void *const *keys, void *const *values, size_t rowStride,
+                       arDataType_t dtype, int nranks, arComm_t comm, arStream_t stream)
+{
+    return copy({{keys, values}, {keyPages, valuePages}, {keyScales, valueScales}}, false, rowStride,
+                slots, tokens, cache, dtype, nranks, comm, stream);
+}
+
+arResult_t arCacheAttention(const void *const *queries, size_t queryStride,
+                            const arCacheLayout_t *cache, const void *const *keyPages,
+                            const void *const *valuePages, const float *const *keyScales,
+                            const float *const *valueScales, const int32_t *pageTable,
+                            size_t tablePages, const int32_t *lengths, size_t seqs, size_t heads,
+                            float scale, size_t window, void *const *outbufs,
+                            float *const *outScales, float *const *lse, void *workspace,
+                            size_t workspaceBytes, arDataType_t dtype_arg, int nranks,
+                            arComm_t comm, arStream_t stream)
+{
+    const int dtype = raw(dtype_arg);
+    if (!is_dtype(dtype))
+        return reject(arUnsupported, "dtype must be bf16, fp16 or fp32");
+    if (nranks < 1 || nranks > AR_MAX_RANKS)
+        return reject(arUnsupported, "nranks must be in 1..32");
+    const bool eight = keyScales != nullptr, eight_out = outScales != nullptr;
+    if (eight != (valueScales != nullptr))
+        return reject(arInvalidArgument, "scales of keys and of values, or of neither");
+    const size_t es = elem_bytes(dtype), page_bytes = eight ? 1 : es;
+    CacheAttentionArgs args = {};
+    size_t span, q_span;
+    arResult_t r = check_layout(cache, page_bytes, &args.cache, &span);
+    if (r != arSuccess)
+        return r;
+    if (heads < 1 || heads > kMostHeads || heads % cache->heads != 0)
+        return reject(arUnsupported, "heads must be a multiple of the cache's, at most 4096");
+    if (eight_out && cache->dim % AR_SCALE_BLOCK != 0)
+        return reject(arUnsupported, "8-bit outputs need heads of 128 or 256");
+    if (!isfinite(scale))
+        return reject(arInvalidArgument, "scale must be finite");
+    if (seqs == 0)
+        return arSuccess;
+    if (seqs > kMostSeqs)
+        return reject(arUnsupported, "seqs must be at most 65536");
+    if (tablePages < 1 || tablePages > INT32_MAX)
+        return reject(arInvalidArgument, "tablePages must be in 1..2^31 - 1");
+    const size_t row = heads * cache->dim;
+    r = check_rows(seqs, row, queryStride, dtype, &q_span);
+    if (r != arSuccess)
+        return r;
+    if (queries == nullptr || keyPages == nullptr || valuePages == nullptr || outbufs == nullptr)
+        return reject(arInvalidArgument, "NULL buffer array");
+    Ranges mem;
+    const size_t places = cache->pages * cache->pageTokens * cache->heads;
+    bool ok = mem.add(pageTable, seqs * tablePages * sizeof(int32_t), false, 4) &&
+              mem.add(lengths, seqs * sizeof(int32_t), false, 4) &&
+              mem.add(workspace, workspaceBytes, true) &&
+              mem.add_ranks(queries, nranks, q_span * es, false) &&
+              mem.add_ranks(keyPages, nranks, span * page_bytes, false) &&
+              mem.add_ranks(valuePages, nranks, span * page_bytes, false) &&
+              mem.add_ranks(outbufs, nranks, seqs * row * (eight_out ? 1 : es), true);
+    if (eight)
+        ok = ok && mem.add_ranks((const void *const *)keyScales, nranks, places * sizeof(float), false) &&
+             mem.add_ranks((const void *const *)valueScales, nranks, places * sizeof(float), false);
+    if (eight_out)
+        ok = ok && mem.add_ranks((const void *const *)outScales, nranks,
+                                 scale_blocks(row) * seqs * sizeof(float), true);
+    if (lse != nullptr)
+        ok = ok && mem.add_ranks((const void *const *)lse, nranks, seqs * heads * sizeof(float), true);
+    if (!ok || !mem.disjoint())
+        return reject(arInvalidArgument, mem.why());
+    r = check_comm(comm);
+    if (r != arSuccess)
+        return r;
+    if (workspaceBytes < cache_attention_workspace(args.cache.dim, comm->cu_count))
+        return reject(arInvalidArgument, "workspace too small");
+    for (int i = 0; i < nranks; ++i) {
+        args.q[i] = (const char *)queries[i];
+        args.keys[i] = (const char *)keyPages[i];
+        args.values[i] = (const char *)valuePages[i];
+        args.key_scales[i] = eight ? keyScales[i] : nullptr;
+        args.value_scales[i] = eight ? valueScales[i] : nullptr;
+        args.out[i] = (char *)outbufs[i];
+        args.out_scales[i] = eight_out ? outScales[i] : nullptr;
+        args.lse[i] = lse != nullptr ? lse[i] : nullptr;
+    }
+    args.table = pageTable;
+    args.lengths = lengths;
+    args.q_stride = queryStride;
+    args.table_pages = tablePages;
+    args.window = window;
+    args.work = (char *)workspace;
+    args.seqs = (uint32_t)seqs;
+    args.heads = (uint32_t)heads;
+    args.nranks = (uint32_t)nranks;
+    args.has_lse = lse != nullptr;
+    args.scale = scale;
+    return launched(launch_cache_attention(args, dtype, eight, eight_out, comm->cu_count,
+                                           (hipStream_t)stream));
+}
+
+arResult_t arCacheAttentionWorkspace(size_t dim, arComm_t comm, size_t *bytes)
+{
+    if (bytes == nullptr)
+        return reject(arInvalidArgument, "NULL result");
+    if (dim < 16 || dim > AR_CACHE_MAX_DIM || dim % 16 != 0)
+        return reject(arUnsupported, "dim must be a multiple of 16 in 16..256");
+    if (comm == nullptr)
+        return reject(arInvalidArgument, "NULL comm");
+    *bytes = (size_t)cache_attention_workspace((uint32_t)dim, comm->cu_count);
+    return arSuccess;
+}
+
+}  // extern "C"

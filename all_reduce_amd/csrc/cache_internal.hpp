@@ -1,0 +1,81 @@
+// cache_internal.hpp -- what the entry points of ar_cache.h and their kernel
+// files share.
+#pragma once
+
+#include "ar_cache.h"
+#include "ar_internal.hpp"
+
+namespace ar {
+
+// A cache's layout as the kernels take it: strides in elements.
+struct CacheShape {
+    uint64_t page_stride, head_stride, token_stride;
+    uint32_t pages, page_tokens;
+    uint32_t heads;
+    uint32_t dim;
+    // Element offset of place `o` of page `p` of a head.
+    __host__ __device__ uint64_t at(uint32_t p, uint32_t o, uint32_t head) const
+    {
+        return p * page_stride + o * token_stride + head * head_stride;
+    }
+    // The same among the scales.
+    __host__ __device__ uint64_t scale_at(uint32_t p, uint32_t o, uint32_t head) const
+    {
+        return ((uint64_t)p * heads + head) * page_tokens + o;
+    }
+    // A slot's page and place; false for a number that is none of the cache's.
+    __host__ __device__ bool place(int64_t slot, uint32_t *p, uint32_t *o) const
+    {
+        if (slot < 0 || slot >= (int64_t)pages * page_tokens)
+            return false;
+        *p = (uint32_t)slot / page_tokens;
+        *o = (uint32_t)slot % page_tokens;
+        return true;
+    }
+};
+
+// Rank tables by value in the kernel arguments, as in block_internal.hpp.
+// arCacheWrite: from rows into pages; arCacheRead: from pages into rows.
+struct CacheCopyArgs {
+    char *rows[2][AR_MAX_RANKS];    // keys, values
+    char *pages[2][AR_MAX_RANKS];
+    float *scales[2][AR_MAX_RANKS]; // unused where the cache has the element type
+    const int64_t *slots;
+    CacheShape cache;
+    uint64_t row_stride;            // elements
+    uint32_t tokens;
+};
+
+struct CacheAttentionArgs {
+    const char *q[AR_MAX_RANKS];
+    const char *keys[AR_MAX_RANKS];
+    const char *values[AR_MAX_RANKS];
+    const float *key_scales[AR_MAX_RANKS];
+    const float *value_scales[AR_MAX_RANKS];
+    char *out[AR_MAX_RANKS];
+    float *out_scales[AR_MAX_RANKS];  // unused without an 8-bit output
+    float *lse[AR_MAX_RANKS];         // unused where has_lse is 0
+    const int32_t *table;
+    const int32_t *lengths;
+    CacheShape cache;
+    uint64_t q_stride;  // elements
+    uint64_t table_pages;
+    uint64_t window;    // 0: all
+    char *work;
+    uint32_t seqs;
+    uint32_t heads;     // query heads
+    uint32_t nranks;
+    uint32_t has_lse;
+    float scale;
+};
+
+// Launchers: validate nothing (the entry points did).
+hipError_t launch_cache_write(const CacheCopyArgs &args, int dtype, bool eight, int nranks,
+                              int cu_count, hipStream_t stream);
+hipError_t launch_cache_read(const CacheCopyArgs &args, int dtype, bool eight, int nranks,
+                             int cu_count, hipStream_t stream);
+hipError_t launch_cache_attention(const CacheAttentionArgs &args, int dtype, bool eight,
+                                  bool eight_out, int cu_count, hipStream_t stream);
+uint64_t cache_attention_workspace(uint32_t dim, int cu_count);
+
+}  // namespace ar
