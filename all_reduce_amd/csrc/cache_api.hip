@@ -5,6 +5,7 @@
 
 #include "api_checks.hpp"
 #include "cache_internal.hpp"
+#include "cache_plan.hpp"
 
 using namespace ar;
 
@@ -51,6 +52,7 @@ arResult_t check_layout(const arCacheLayout_t *c, size_t page_bytes, CacheShape 
     shape->page_tokens = (uint32_t)c->pageTokens;
     shape->heads = (uint32_t)c->heads;
     shape->dim = (uint32_t)c->dim;
+    shape->set_division();
     *span = (size_t)extent;
     return arSuccess;
 }
@@ -280,6 +282,67 @@ arResult_t arCacheAttentionWorkspace(size_t dim, arComm_t comm, size_t *bytes)
         return reject(arInvalidArgument, "NULL comm");
     *bytes = (size_t)cache_attention_workspace((uint32_t)dim, comm->cu_count);
     return arSuccess;
+}
+
+// For tests, on the host: the pieces of workgroup `block`'s share of an attention
+// whose lengths are known, as the kernel walks them (cache_plan.hpp).  Twelve
+// numbers a piece: unit group, sequence, first step, step after the last, steps of
+// the unit, first token, token after the last, slot of partial sums, counter of the
+// group and workgroups in it, counter of the unit and groups in it.  Returns the
+// number of pieces, of which `most` are written.
+size_t ar_cache_attention_share(const int32_t *lengths, size_t seqs, size_t capacity, size_t window,
+                                uint32_t step, uint32_t units, uint32_t grid, uint32_t block,
+                                uint64_t (*pieces)[12], size_t most)
+{
+    uint32_t first, end;
+    auto steps_at = [&](size_t i) {
+        attended(lengths[i], capacity, window, &first, &end);
+        return steps_of(first, end, step);
+    };
+    uint64_t each = 0;
+    for (size_t i = 0; i < seqs; ++i)
+        each += steps_at(i);
+    const CachePlan plan(each * units, grid, 1u);
+    const uint32_t share = plan.share(block);
+    if (share == ~0u)
+        return 0;
+    const uint64_t begin = plan.start(share);
+    uint64_t left = plan.start(share + 1u) - begin, unit = divide(begin, each), at = begin - unit * each;
+    size_t seq = 0, count = 0;
+    for (uint32_t x = steps_at(seq); at >= x; x = steps_at(++seq))
+        at -= x;
+    uint64_t step0 = at, here = begin - step0;
+    for (;;) {
+        const uint64_t steps = steps_at(seq);
+        const uint64_t step1 = left < steps - step0 ? step0 + left : steps;
+        const CacheJoin join = {plan.owner(here), plan.owner(here + steps - 1u)};
+        const uint64_t piece[12] = {
+            unit, seq, step0, step1, steps, first + step0 * step, step1 == steps ? end : first + step1 * step,
+            join.slot(share), join.group_counter(share), join.last(share) - join.first(share) + 1u,
+            join.unit_counter(), join.groups()};
+        if (count < most)
+            memcpy(pieces[count], piece, sizeof piece);
+        ++count;
+        left -= step1 - step0;
+        if (left == 0)
+            return count;
+        here += steps;
+        step0 = 0;
+        if (++seq == seqs) {
+            seq = 0;
+            ++unit;
+        }
+    }
+}
+
+// For tests, on the host: the page and place of a slot; 0 for one of no cache.
+int ar_cache_place(size_t pages, size_t page_tokens, int64_t slot, uint32_t at[2])
+{
+    CacheShape shape = {};
+    shape.pages = (uint32_t)pages;
+    shape.page_tokens = (uint32_t)page_tokens;
+    shape.set_division();
+    return shape.place(slot, &at[0], &at[1]);
 }
 
 }  // extern "C"

@@ -13,6 +13,24 @@ struct CacheShape {
     uint32_t pages, page_tokens;
     uint32_t heads;
     uint32_t dim;
+    uint32_t page_mul, page_shift;  // see set_division
+
+    // t / page_tokens for t below 2^31 is (t * mul) >> (32 + shift), with mul the
+    // quotient 2^(31 + s) / page_tokens rounded up, 2^s the power of two from
+    // page_tokens on and shift = s - 1: mul * page_tokens exceeds 2^(31 + s) by at
+    // most 2^s, which t below 2^31 does not raise to a whole.
+    void set_division()
+    {
+        uint32_t s = 0;
+        while (((uint64_t)1 << s) < page_tokens)
+            ++s;
+        page_mul = s == 0 ? 0 : (uint32_t)(((uint64_t)1 << (31 + s)) / page_tokens + 1);
+        page_shift = s == 0 ? 0 : s - 1;
+    }
+    __host__ __device__ uint32_t page_of(uint32_t t) const
+    {
+        return page_mul == 0 ? t : (uint32_t)((uint64_t)t * page_mul >> 32) >> page_shift;
+    }
     // Element offset of place `o` of page `p` of a head.
     __host__ __device__ uint64_t at(uint32_t p, uint32_t o, uint32_t head) const
     {
@@ -28,8 +46,8 @@ struct CacheShape {
     {
         if (slot < 0 || slot >= (int64_t)pages * page_tokens)
             return false;
-        *p = (uint32_t)slot / page_tokens;
-        *o = (uint32_t)slot % page_tokens;
+        *p = page_of((uint32_t)slot);
+        *o = (uint32_t)slot - *p * page_tokens;
         return true;
     }
 };
