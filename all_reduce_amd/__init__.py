@@ -144,7 +144,7 @@ def library() -> ctypes.CDLL:
         "arCacheRead": ([vp, sz, layout, pvp, pvp, pvp, pvp, pvp, pvp, sz, i32, i32, vp, vp], i32),
         "arCacheAttention": ([pvp, sz, layout, pvp, pvp, pvp, pvp, vp, sz, vp, sz, sz,
                               ctypes.c_float, sz, pvp, pvp, pvp, vp, sz, i32, i32, vp, vp], i32),
-        "arCacheAttentionWorkspace": ([sz, vp, ctypes.POINTER(sz)], i32),
+        "arCacheAttentionWorkspace": ([sz, sz, vp, ctypes.POINTER(sz)], i32),
         "arGetErrorString": ([i32], ctypes.c_char_p),
         "arGetVersion": ([], i32),
     }
@@ -315,10 +315,10 @@ def arCacheAttention(queries, query_stride: int, cache, key_pages, value_pages, 
         _pointer_array(lse, nranks), workspace, workspace_bytes, int(dtype), nranks, comm, stream)
 
 
-def arCacheAttentionWorkspace(dim: int, comm):
+def arCacheAttentionWorkspace(dim: int, group: int, comm):
     """Returns (result code, bytes)."""
     n = ctypes.c_size_t(0)
-    r = library().arCacheAttentionWorkspace(dim, comm, ctypes.byref(n))
+    r = library().arCacheAttentionWorkspace(dim, group, comm, ctypes.byref(n))
     return r, n.value
 
 
@@ -688,7 +688,7 @@ class Comm:
         self._check("page_table", [page_table], 1, (seqs, page_table.shape[1]), torch.int32)
         self._check("lengths", [lengths], 1, (seqs,), torch.int32)
         if workspace is None:
-            workspace = self.cache_workspace(dim, stream)
+            workspace = self.cache_workspace(dim, max(1, heads // layout.heads), stream)
         elif workspace.device != self.device or not workspace.is_contiguous():
             raise ValueError("the workspace must be a contiguous tensor on the communicator's device")
         return PreparedCall(self, "arCacheAttention", (
@@ -701,12 +701,13 @@ class Comm:
             self._stream(stream), (queries, key_pages, value_pages, key_scales, value_scales,
                                    page_table, lengths, out, out_scales, lse, workspace))
 
-    def cache_workspace(self, dim: int, stream=None):
-        """A workspace for ``cache_attention`` with heads of ``dim``, ready on
-        ``stream`` (default: the current one).  Calls one after the other may share
-        it; calls that may run at once need one each."""
+    def cache_workspace(self, dim: int, group: int, stream=None):
+        """A workspace for ``cache_attention`` with heads of ``dim`` and ``group``
+        query heads to a key-value head (or fewer of either), ready on ``stream``
+        (default: the current one).  Calls one after the other may share it; calls
+        that may run at once need one each."""
         torch = _torch()
-        r, n = arCacheAttentionWorkspace(dim, self.handle)
+        r, n = arCacheAttentionWorkspace(dim, group, self.handle)
         if r != 0:
             raise ArError(r, "arCacheAttentionWorkspace")
         with torch.cuda.stream(torch.cuda.current_stream(self.device) if stream is None else stream):

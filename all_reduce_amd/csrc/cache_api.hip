@@ -215,6 +215,8 @@ arResult_t arCacheAttention(const void *const *queries, size_t queryStride,
         return arSuccess;
     if (seqs > kMostSeqs)
         return reject(arUnsupported, "seqs must be at most 65536");
+    if (seqs * heads * (size_t)nranks > (size_t)1 << 30)
+        return reject(arUnsupported, "seqs * heads * nranks must be at most 2^30");
     if (tablePages < 1 || tablePages > INT32_MAX)
         return reject(arInvalidArgument, "tablePages must be in 1..2^31 - 1");
     const size_t row = heads * cache->dim;
@@ -245,7 +247,8 @@ arResult_t arCacheAttention(const void *const *queries, size_t queryStride,
     r = check_comm(comm);
     if (r != arSuccess)
         return r;
-    if (workspaceBytes < cache_attention_workspace(args.cache.dim, comm->cu_count))
+    if (workspaceBytes < cache_attention_workspace(args.cache.dim, (uint32_t)(heads / cache->heads),
+                                                   comm->cu_count))
         return reject(arInvalidArgument, "workspace too small");
     for (int i = 0; i < nranks; ++i) {
         args.q[i] = (const char *)queries[i];
@@ -263,8 +266,10 @@ arResult_t arCacheAttention(const void *const *queries, size_t queryStride,
     args.table_pages = tablePages;
     args.window = window;
     args.work = (char *)workspace;
+    args.slots = (float *)((char *)workspace + cache_attention_counters(comm->cu_count));
     args.seqs = (uint32_t)seqs;
     args.heads = (uint32_t)heads;
+    args.group = (uint32_t)(heads / cache->heads);
     args.nranks = (uint32_t)nranks;
     args.has_lse = lse != nullptr;
     args.scale = scale;
@@ -272,54 +277,73 @@ arResult_t arCacheAttention(const void *const *queries, size_t queryStride,
                                            (hipStream_t)stream));
 }
 
-arResult_t arCacheAttentionWorkspace(size_t dim, arComm_t comm, size_t *bytes)
+arResult_t arCacheAttentionWorkspace(size_t dim, size_t group, arComm_t comm, size_t *bytes)
 {
     if (bytes == nullptr)
         return reject(arInvalidArgument, "NULL result");
     if (dim < 16 || dim > AR_CACHE_MAX_DIM || dim % 16 != 0)
         return reject(arUnsupported, "dim must be a multiple of 16 in 16..256");
+    if (group < 1 || group > kMostHeads)
+        return reject(arUnsupported, "group must be in 1..4096");
     if (comm == nullptr)
         return reject(arInvalidArgument, "NULL comm");
-    *bytes = (size_t)cache_attention_workspace((uint32_t)dim, comm->cu_count);
+    *bytes = (size_t)cache_attention_workspace((uint32_t)dim, (uint32_t)group, comm->cu_count);
     return arSuccess;
 }
 
-// For tests, on the host: the pieces of workgroup `block`'s share of an attention
-// whose lengths are known, as the kernel walks them (cache_plan.hpp).  Twelve
-// numbers a piece: unit group, sequence, first step, step after the last, steps of
-// the unit, first token, token after the last, slot of partial sums, counter of the
-// group and workgroups in it, counter of the unit and groups in it.  Returns the
+// For tests, on the host: the pieces of the share of team `team` of workgroup `block`
+// of an attention whose lengths are known, as the kernel walks them (cache_plan.hpp).
+// 2^tokens: of a wave's tile.  Thirteen numbers a piece: rank, sequence, key-value head
+// and tile of query heads, first step, step after the last, steps of the unit, first
+// token, token after the last, slot of partial sums, counter of the group and teams in
+// it, counter of the unit and groups in it.  `teams`: waves of a team, waves that take
+// the same tokens, tiles of query heads, tokens of a pass and of a step.  Returns the
 // number of pieces, of which `most` are written.
 size_t ar_cache_attention_share(const int32_t *lengths, size_t seqs, size_t capacity, size_t window,
-                                uint32_t step, uint32_t units, uint32_t grid, uint32_t block,
-                                uint64_t (*pieces)[12], size_t most)
+                                uint32_t tokens, uint32_t ranks, uint32_t heads, uint32_t group,
+                                uint32_t grid, uint32_t block, uint32_t team, uint32_t teams[5],
+                                uint32_t (*pieces)[13], size_t most)
 {
     uint32_t first, end;
+    const uint32_t passes = passes_of_a_step(seqs, ranks, heads, group, tokens,
+                                             window != 0 && window < capacity ? window : capacity);
+    uint32_t of_all = 0;
+    for (size_t i = 0; i < seqs; ++i) {
+        attended(lengths[i], capacity, window, &first, &end);
+        of_all += tiles_of(first, end, tokens);
+    }
+    CacheTeams t(group, tokens, passes, false);
+    const bool alone = waves_alone((uint32_t)seqs * ranks * heads * t.tiles, grid, of_all, (uint32_t)seqs);
+    if (alone)
+        t = CacheTeams(group, tokens, passes + passes_alone(of_all, (uint32_t)seqs), true);
+    const uint32_t across = heads * t.tiles;
     auto steps_at = [&](size_t i) {
         attended(lengths[i], capacity, window, &first, &end);
-        return steps_of(first, end, step);
+        return steps_of(first, end, t.shift);
     };
-    uint64_t each = 0;
+    uint32_t row = 0;
     for (size_t i = 0; i < seqs; ++i)
-        each += steps_at(i);
-    const CachePlan plan(each * units, grid, 1u);
-    const uint32_t share = plan.share(block);
+        row += steps_at(i) * across;
+    const uint32_t told[5] = {t.waves, t.side, t.tiles, t.pass, 1u << t.shift};
+    memcpy(teams, told, sizeof told);
+    const CachePlan plan(row * ranks, alone ? grid * 4u : grid);
+    const uint32_t share = team < 4u / t.waves ? plan.share(block, team, grid) : ~0u;
     if (share == ~0u)
         return 0;
-    const uint64_t begin = plan.start(share);
-    uint64_t left = plan.start(share + 1u) - begin, unit = divide(begin, each), at = begin - unit * each;
-    size_t seq = 0, count = 0;
-    for (uint32_t x = steps_at(seq); at >= x; x = steps_at(++seq))
+    const uint32_t begin = plan.start(share);
+    uint32_t left = plan.start(share + 1u) - begin, rank = begin / row, at = begin % row, seq = 0;
+    size_t count = 0;
+    for (uint32_t x = steps_at(seq) * across; at >= x; x = steps_at(++seq) * across)
         at -= x;
-    uint64_t step0 = at, here = begin - step0;
+    uint32_t unit = at / steps_at(seq), step0 = at % steps_at(seq), here = begin - step0;
     for (;;) {
-        const uint64_t steps = steps_at(seq);
-        const uint64_t step1 = left < steps - step0 ? step0 + left : steps;
+        const uint32_t steps = steps_at(seq);
+        const uint32_t step1 = left < steps - step0 ? step0 + left : steps;
         const CacheJoin join = {plan.owner(here), plan.owner(here + steps - 1u)};
-        const uint64_t piece[12] = {
-            unit, seq, step0, step1, steps, first + step0 * step, step1 == steps ? end : first + step1 * step,
-            join.slot(share), join.group_counter(share), join.last(share) - join.first(share) + 1u,
-            join.unit_counter(), join.groups()};
+        const uint32_t piece[13] = {
+            rank, seq, unit, step0, step1, steps, first + (step0 << t.shift),
+            step1 == steps ? end : first + (step1 << t.shift), join.slot(share), join.group_counter(share),
+            join.last(share) - join.first(share) + 1u, join.unit_counter(), join.groups()};
         if (count < most)
             memcpy(pieces[count], piece, sizeof piece);
         ++count;
@@ -328,11 +352,22 @@ size_t ar_cache_attention_share(const int32_t *lengths, size_t seqs, size_t capa
             return count;
         here += steps;
         step0 = 0;
-        if (++seq == seqs) {
-            seq = 0;
-            ++unit;
+        if (++unit == across) {
+            unit = 0;
+            if (++seq == seqs) {
+                seq = 0;
+                ++rank;
+            }
         }
     }
+}
+
+// For tests, on the host: the slot of part i of what team w joins in `stage` for a unit
+// of teams w0 .. w1.
+uint32_t ar_cache_attention_part(uint32_t w0, uint32_t w1, uint32_t w, uint32_t stage, uint32_t i)
+{
+    const CacheJoin::Parts parts = CacheJoin{w0, w1}.parts(w, stage);
+    return i == 0 ? parts.first : parts.next + (i - 1u) * parts.by;
 }
 
 // For tests, on the host: the page and place of a slot; 0 for one of no cache.

@@ -4,10 +4,19 @@
 
 namespace ar {
 
-uint64_t cache_attention_workspace(uint32_t dim, int cu_count)
+// Counters, in the same place whatever call uses the workspace, then two slots a team.
+// (A wave that is a team has at most 16 queries, four together at most 64.)
+uint64_t cache_attention_counters(int cu_count)
 {
-    const uint64_t most = attend_most(2, cu_count);
-    return most * 16u + most * 2u * attend_slot(padded_dim(dim)) * sizeof(float);
+    return (uint64_t)attend_most(2, cu_count) * kAttendWaves * 4u * sizeof(uint32_t);
+}
+
+uint64_t cache_attention_workspace(uint32_t dim, uint32_t group, int cu_count)
+{
+    const uint64_t teams = (uint64_t)attend_most(2, cu_count) * kAttendWaves;
+    const uint32_t queries = group < kTileQueries ? group : kTileQueries;
+    return cache_attention_counters(cu_count) +
+           teams * 2u * queries * (padded_dim(dim) + 2u) * sizeof(float);
 }
 
 hipError_t launch_cache_attention(const CacheAttentionArgs &args, int dtype, bool eight,

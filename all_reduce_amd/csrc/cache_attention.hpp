@@ -46,8 +46,8 @@ constexpr uint32_t kAttendWaves = 4, kAttendThreads = 64 * kAttendWaves;
 // Queries a workgroup takes at once.
 constexpr uint32_t kTileQueries = 16;
 
-// Floats of a slot of partial sums: [16][DP] sums, 16 pairs of reference and sum of weights.
-constexpr uint32_t attend_slot(uint32_t dp) { return kTileQueries * (dp + 2u); }
+// A slot of partial sums: [queries][DP] sums, then as many pairs of reference and sum
+// of weights.
 
 constexpr uint32_t padded_dim(uint32_t dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
 
@@ -120,12 +120,14 @@ struct Tile {
     // A float32 cache of 256 takes one group of 16 tokens a tile: two would not
     // leave registers.
     static constexpr int kGroups = kWide && DP == 256 ? 1 : 2;
-    static constexpr uint32_t kTokens = 16 * kGroups;
+    static constexpr uint32_t kTokenShift = kGroups == 1 ? 4 : 5;
+    static constexpr uint32_t kTokens = 1u << kTokenShift;
     static constexpr int kE = 16 / kBytes;                    // values in 16 bytes
     static constexpr int kKeyLoads = DP / (4 * kE);           // a group of 16 tokens
     static constexpr int kVE = EIGHT ? DP / 16 : (DP / 16 < kE ? DP / 16 : kE);  // values a load
     static constexpr int kVH = DP / (16 * kVE);               // loads a token
     static constexpr int kVW = kVE * kBytes / 4;              // words a load
+    typedef uint32_t Words __attribute__((ext_vector_type(kVW)));
     using KeyType = std::conditional_t<T::kId == Fp16::kId, Fp16, Bf16>;
     using ValueType = std::conditional_t<!EIGHT && T::kId == Fp16::kId, Fp16, Bf16>;
     static constexpr int kQueryParts = EIGHT && T::kBytes == 4 ? 3 : 1;
@@ -189,7 +191,7 @@ struct Tile {
         }
     }
 
-    template <bool EXACT>
+    template <bool EXACT, bool NT>
     __device__ void load_keys(const char *const (&row)[kGroups], uint32_t g, uint32_t dim)
     {
 #pragma unroll
@@ -197,13 +199,13 @@ struct Tile {
 #pragma unroll
             for (int s = 0; s < kKeyLoads; ++s) {
                 if (EXACT || key_dim(s, g) < dim)
-                    k[gr][s] = load_piece<false>(row[gr] + s * 64);
+                    k[gr][s] = load_piece<NT>(row[gr] + s * 64);
                 else
                     k[gr][s] = u32x4{0, 0, 0, 0};
             }
     }
 
-    template <bool EXACT>
+    template <bool EXACT, bool NT>
     __device__ void load_values(const char *const (&row)[kGroups][4], uint32_t n, uint32_t dim)
     {
 #pragma unroll
@@ -213,9 +215,11 @@ struct Tile {
 #pragma unroll
                 for (int h = 0; h < kVH; ++h) {
                     // (columns past dim are stored nowhere)
-                    if (EXACT || value_dim(h, n) < dim)
-                        __builtin_memcpy(v[gr][i][h], __builtin_assume_aligned(row[gr][i] + h * 16 * kVE * kBytes, kVE * kBytes),
-                                         kVE * kBytes);
+                    if (EXACT || value_dim(h, n) < dim) {
+                        const Words *from = (const Words *)(row[gr][i] + h * 16 * kVE * kBytes);
+                        const Words x = NT ? __builtin_nontemporal_load(from) : *from;
+                        __builtin_memcpy(v[gr][i][h], &x, sizeof x);
+                    }
                 }
     }
 
@@ -333,13 +337,29 @@ struct Tile {
     }
 };
 
+// A matrix instruction's result is ready some issue slots after it, for which the
+// compiler fills in waits; of a branch that is taken in between it counts too few
+// (binary32 scores read behind one came out with old values in their last register).
+// So no branch follows such instructions before these waits.
+__device__ inline void matrix_done()
+{
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+template <int N>
+__device__ inline void matrix_done(f32x4 (&c)[N])
+{
+    if constexpr (N == 1)
+        asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7" : "+v"(c[0]));
+    else
+        asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7" : "+v"(c[0]), "+v"(c[1]));
+    static_assert(N <= 2, "");
+}
+
 // A value that is the same in every lane, in a scalar register.
 __device__ inline uint32_t uniform(uint32_t x) { return __builtin_amdgcn_readfirstlane(x); }
-
-__device__ inline uint64_t uniform(uint64_t x)
-{
-    return (uint64_t)uniform((uint32_t)(x >> 32)) << 32 | uniform((uint32_t)x);
-}
 
 // A sum of the lanes that hold a query, in each of them.
 __device__ inline float sum_query(float x)
@@ -360,8 +380,8 @@ __device__ inline float max_query(float x)
 // store of this scope has reached the memory that all of them see when its wave's
 // counter says that it is done, and a load of this scope reads there.  (With
 // ordinary accesses between fences, which write back and drop whole caches, one
-// sequence of 1000 tokens x 8 ranks took 16.3 us in place of @A, 29 odd ones 142 in
-// place of @B.)
+// sequence of 1000 tokens x 8 ranks took 16.3 us in place of 9.6, 29 odd ones 142 in
+// place of 22.)
 __device__ inline void share_pair(float *to, float a, float b)
 {
     const f32x2 v = {a, b};
@@ -379,100 +399,188 @@ __device__ inline void shared_stores_done()
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 }
 
+// The inclusive sum over the lanes up to this one.
+__device__ inline uint32_t scan64(uint32_t x)
+{
+    x += lane_move<0x111>(x);  // within rows of 16: 1, 2, 4 and 8 lanes on
+    x += lane_move<0x112>(x);
+    x += lane_move<0x114>(x);
+    x += lane_move<0x118>(x);
+    x += __builtin_amdgcn_update_dpp(0u, x, 0x142, 0xa, 0xf, false);  // the row before's last
+    x += __builtin_amdgcn_update_dpp(0u, x, 0x143, 0xc, 0xf, false);  // the half before's
+    return x;
+}
+
+// Parts of a sum that are loaded at once.
+constexpr uint32_t kJoinLoads = 4;
+
+// Sequences that a wave has in its lanes.
+constexpr uint32_t kSmallBatch = 64;
+
+// What a workgroup has in LDS.
+template <typename X, int DP>
+struct AttendShared {
+    uint64_t rows[kAttendWaves][X::kTokens];      // a tile's rows: byte offsets in a pool
+    float scales[kAttendWaves][2][X::kTokens];    // a tile's scales, of keys and of values
+    float sums[kAttendWaves][kTileQueries][DP + 4];
+    float refs[kAttendWaves][kTileQueries], weights[kAttendWaves][kTileQueries];
+    uint32_t bad[kAttendWaves], last;
+    uint32_t found[kAttendWaves][2];
+};
+
+// (The code is kept short, with one copy of everything: a call of few tokens runs
+// through it once, from memory.  Loading eight parts of a sum at once, not four, is 1 KB
+// more and took 0.6 us longer where two are joined.)
 template <typename T, bool EIGHT, int DP, bool EXACT, bool EIGHT_OUT>
 __global__ __launch_bounds__(kAttendThreads, (Tile<T, EIGHT, DP>::kPerCu)) void cache_attend(CacheAttentionArgs p)
 {
     typedef Tile<T, EIGHT, DP> X;
-    constexpr uint32_t kStep = X::kTokens * kAttendWaves;
-    constexpr uint32_t kRow = DP + 4;  // floats of a query's sums in LDS
-    // a tile's rows (byte offsets in a pool) and scales, of the next tile
-    __shared__ uint64_t rows_at[kAttendWaves][X::kTokens];
-    __shared__ float scales_at[EIGHT ? kAttendWaves : 1][2][X::kTokens];
-    __shared__ __align__(16) float sums[kAttendWaves][kTileQueries][kRow];
-    __shared__ float refs[kAttendWaves][kTileQueries], weights[kAttendWaves][kTileQueries];
-    __shared__ uint32_t flags[kAttendWaves];
-    __shared__ uint64_t found[6];
-
-    const uint32_t lane = threadIdx.x & 63u;
-    const uint32_t wave = uniform(threadIdx.x >> 6);
+    __shared__ __align__(16) AttendShared<X, DP> lds;
+    const uint32_t lane = threadIdx.x & 63u, wave = uniform(threadIdx.x >> 6);
     const uint32_t n = lane & 15u, g = lane >> 4;
     const uint32_t dim = EXACT ? (uint32_t)DP : p.cache.dim;
-    const uint32_t group = p.heads / p.cache.heads;
-    const uint32_t tiles = (group + kTileQueries - 1u) / kTileQueries;
+    const uint32_t group = p.group;
     const uint64_t capacity = p.table_pages * p.cache.page_tokens;
-
-    // ---- this workgroup's share -----------------------------------------------
-    auto steps_at = [&](uint32_t seq) {
-        uint32_t first, end;
-        attended(p.lengths[seq], capacity, p.window, &first, &end);
-        return steps_of(first, end, kStep);
-    };
-    const uint32_t chunk = (p.seqs + kAttendThreads - 1u) / kAttendThreads;
-    const uint32_t from = threadIdx.x * chunk, to = from + chunk < p.seqs ? from + chunk : p.seqs;
-    uint64_t mine = 0;
-    for (uint32_t s = from; s < to; ++s)
-        mine += steps_at(s);
-    uint64_t before = mine;
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-        const uint64_t x = (uint64_t)__shfl_up((unsigned long long)before, d);
-        before += lane >= (uint32_t)d ? x : 0u;
-    }
-    if (lane == 63)
-        found[wave] = before;
-    __syncthreads();
-    before -= mine;
-    uint64_t each = 0;  // steps of all sequences
-#pragma unroll
-    for (uint32_t w = 0; w < kAttendWaves; ++w) {
-        before += w < wave ? found[w] : 0u;
-        each += found[w];
-    }
-    each = uniform(each);
-    const uint32_t units = p.nranks * p.cache.heads * tiles;
-    const CachePlan plan(each * units, gridDim.x, 1u);
-    const uint32_t share = plan.share(blockIdx.x);
-    if (share == ~0u)
-        return;
-    const uint64_t begin = plan.start(share);
-    uint64_t left = plan.start(share + 1u) - begin;
-    uint32_t unit = (uint32_t)divide(begin, each);
-    const uint64_t at = begin - unit * each;
-    if (at >= before && at < before + mine) {
-        uint64_t b = before;
-        uint32_t s = from;
-        for (uint32_t x = steps_at(s); at - b >= x; x = steps_at(s)) {
-            b += x;
-            ++s;
-        }
-        found[4] = s;
-        found[5] = at - b;
-    }
-    __syncthreads();
-    uint32_t seq = uniform((uint32_t)found[4]);
-    uint32_t step0 = uniform((uint32_t)found[5]);
-    uint64_t here = begin - step0;  // the unit's first step
-
     const float factor = p.scale * kLog2e;
     uint32_t *counters = (uint32_t *)p.work;
-    float *slots = (float *)(p.work + (uint64_t)gridDim.x * 16u);
+
+    // ---- this team's share of the row of all steps ---------------------------------
+    // A small batch: a lane has a sequence, and every wave all of them.  Else a thread
+    // has some, and the workgroup all.
+    const bool small = p.seqs <= kSmallBatch;
+    const int32_t lane_length = small && lane < p.seqs ? p.lengths[lane] : 0;
+    // The pointer tables' first use costs a trip to memory, on the way beside this one.
+    touch(p.q);
+    touch(p.keys);
+    touch(p.values);
+    touch(p.out);
+    if constexpr (EIGHT) {
+        touch(p.key_scales);
+        touch(p.value_scales);
+    }
+    auto length_of = [&](uint32_t seq) {  // (the same in every lane)
+        return small ? __builtin_amdgcn_readlane(lane_length, seq) : p.lengths[seq];
+    };
+    const uint32_t chunk = (p.seqs + kAttendThreads - 1u) / kAttendThreads;
+    const uint32_t from = small ? lane : threadIdx.x * chunk;
+    const uint32_t to = small ? lane + 1u : from + chunk;
+    // What `of` says of all sequences' tokens; `before`: of those before the lane's.
+    auto sum_up = [&](auto of, uint32_t &mine, uint32_t &before) {
+        mine = 0;
+        for (uint32_t s = from; s < to && s < p.seqs; ++s) {
+            uint32_t first, end;
+            attended(small ? lane_length : p.lengths[s], capacity, p.window, &first, &end);
+            mine += of(first, end);
+        }
+        before = scan64(mine);
+        uint32_t all = __builtin_amdgcn_readlane(before, 63);
+        before -= mine;
+        if (!small) {
+            __syncthreads();
+            if (lane == 0)
+                lds.found[wave][0] = all;
+            __syncthreads();
+            all = 0;
+            for (uint32_t w = 0; w < kAttendWaves; ++w) {
+                before += w < wave ? lds.found[w][0] : 0u;
+                all += lds.found[w][0];
+            }
+            all = uniform(all);
+        }
+        return all;
+    };
+    CacheTeams teams(group, X::kTokenShift, p.passes, false);
+    bool alone = false;
+    uint32_t mine, before;
+    const uint32_t units = p.seqs * p.nranks * p.cache.heads * teams.tiles;
+    if (units > gridDim.x) {
+        const uint32_t all = sum_up([&](uint32_t first, uint32_t end) { return tiles_of(first, end, X::kTokenShift); },
+                                    mine, before);
+        alone = waves_alone(units, gridDim.x, all, p.seqs);
+        if (alone)
+            teams = CacheTeams(group, X::kTokenShift, p.passes + passes_alone(all, p.seqs), true);
+    }
+    auto steps_in = [&](uint32_t first, uint32_t end) { return steps_of(first, end, teams.shift); };
+    auto steps_at = [&](int32_t length) {
+        uint32_t first, end;
+        attended(length, capacity, p.window, &first, &end);
+        return steps_in(first, end);
+    };
+    const uint32_t across = p.cache.heads * teams.tiles;  // units of a sequence and rank
+    const uint32_t row = sum_up(steps_in, mine, before) * across;  // steps of a rank
+    mine *= across;
+    before *= across;
+    // Non-temporal loads where all keys and values together are more than half of the
+    // last-level cache, which would not keep them: 64 x 8192 tokens x 8 ranks take 321
+    // in place of 355 us, but 256 of 67 tokens (70 MB, which the cache holds) 35 in place
+    // of 31.  Not where waves read the same tokens: 136 in place of 117 us for 32 windows
+    // of 4096 tokens x 4 ranks and 32 query heads of 256.
+    const bool stream = teams.side == 1u && ((uint64_t)row * p.nranks << teams.shift) * dim * (2u * X::kBytes) >= (uint64_t)128 << 20;
+    const CachePlan plan(row * p.nranks, alone ? gridDim.x * kAttendWaves : gridDim.x);
+    const uint32_t team = alone ? wave : 0u;
+    const uint32_t share = plan.share(blockIdx.x, team, gridDim.x);
+    const uint32_t begin = share == ~0u ? 0u : plan.start(share);
+    uint32_t left = share == ~0u ? 0u : plan.start(share + 1u) - begin;
+    uint32_t rank = p.nranks == 1u ? 0u : begin / row, seq, unit;
+    if (small) {
+        const uint32_t at = begin - rank * row;
+        seq = (uint32_t)__builtin_ctzll(__ballot(at >= before && at - before < mine));
+        unit = at - __builtin_amdgcn_readlane(before, seq);
+    } else {
+        __syncthreads();
+        for (uint32_t i = 0; i < (alone ? kAttendWaves : 1u); ++i) {
+            const uint32_t s = plan.share(blockIdx.x, i, gridDim.x);
+            const uint32_t at = s == ~0u ? 0u : plan.start(s) % row;
+            if (at >= before && at - before < mine) {
+                uint32_t b = before, e = from;
+                for (uint32_t x; x = steps_at(p.lengths[e]) * across, at - b >= x; ++e)
+                    b += x;
+                lds.found[i][0] = e;
+                lds.found[i][1] = at - b;
+            }
+        }
+        __syncthreads();
+        seq = uniform(lds.found[team][0]);
+        unit = uniform(lds.found[team][1]);
+    }
+    if (left == 0)  // (from here on waves that are alone meet no more)
+        return;
+    int32_t length = length_of(seq);
+    uint32_t step0 = unit;  // the sequence's step, until the unit's number is known
+    unit = across == 1u ? 0u : step0 / steps_at(length);
+    step0 -= unit * steps_at(length);
+    uint32_t here = begin - step0;  // the unit's first step in the row
+
+    const uint32_t wave0 = alone ? wave : 0u;                // the team's first
+    const uint32_t member = alone ? lane : threadIdx.x;      // lane of the team
+    const uint32_t beside = alone ? 0u : wave % teams.side;  // the wave's place among those on its tokens
+    const uint32_t behind = alone ? 0u : wave / teams.side;
+    const uint32_t most_queries = kTileQueries * teams.side < group ? kTileQueries * teams.side : group;
+    const uint32_t waves_deep = teams.waves / teams.side;
+    const uint32_t mine0 = beside * kTileQueries;            // the wave's queries among the team's
+    auto meet = [&] {
+        if (alone)
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        else
+            __syncthreads();
+    };
 
     for (;;) {
-        // ---- a piece: steps [step0, step1) of a unit --------------------------
-        const uint32_t rank = unit / (p.cache.heads * tiles);
-        const uint32_t kv = unit / tiles % p.cache.heads, tile = unit % tiles;
+        // ---- a piece: steps [step0, step1) of a unit ----------------------------
+        const uint32_t kv = teams.tiles == 1u ? unit : unit / teams.tiles, tile = unit - kv * teams.tiles;
         uint32_t first, end;
-        const int32_t length = p.lengths[seq];
         const bool fine = attended(length, capacity, p.window, &first, &end);
-        const uint32_t steps = steps_of(first, end, kStep);
-        const uint32_t step1 = left < steps - step0 ? step0 + (uint32_t)left : steps;
-        const uint32_t t1 = step1 == steps ? end : first + step1 * kStep;
-        const uint32_t queries = group - tile * kTileQueries < kTileQueries ? group - tile * kTileQueries : kTileQueries;
-        const uint32_t head0 = kv * group + tile * kTileQueries;
+        const uint32_t steps = steps_in(first, end);
+        const uint32_t step1 = left < steps - step0 ? step0 + left : steps;
+        const uint32_t t1 = step1 == steps ? end : first + (step1 << teams.shift);
+        const uint32_t query0 = tile * kTileQueries * teams.side;  // of the group
+        const uint32_t queries = group - query0 < most_queries ? group - query0 : most_queries;
+        const uint32_t head0 = kv * group + query0;
 
         X x;
-        x.template load_query<EXACT>(p.q[rank] + (seq * p.q_stride + (uint64_t)(head0 + n) * dim) * T::kBytes,
-                                     n < queries, g, dim);
+        x.template load_query<EXACT>(
+            p.q[rank] + (seq * p.q_stride + (uint64_t)(head0 + mine0 + n) * dim) * T::kBytes,
+            mine0 + n < queries, g, dim);
 #pragma unroll
         for (int t = 0; t < DP / 16; ++t)
             x.o[t] = f32x4{0, 0, 0, 0};
@@ -490,7 +598,8 @@ __global__ __launch_bounds__(kAttendThreads, (Tile<T, EIGHT, DP>::kPerCu)) void 
         const int32_t *table = p.table + seq * p.table_pages;
         const uint32_t mine_at = lane % X::kTokens;
         const uint32_t kd = X::key_dim(0, g) * X::kBytes, vd = X::value_dim(0, n) * X::kBytes;
-        uint32_t t0 = first + step0 * kStep + wave * X::kTokens;
+        uint32_t t0 = first + (step0 << teams.shift) + behind * X::kTokens;
+        const uint32_t tend = mine0 < queries ? t1 : 0u;  // a wave without queries has no tokens
 
         // page and place of the lane's token of the tile at t (past the end: none)
         auto look = [&](uint32_t t, uint32_t &place) {
@@ -513,272 +622,256 @@ __global__ __launch_bounds__(kAttendThreads, (Tile<T, EIGHT, DP>::kPerCu)) void 
                 page = 0;
                 place = 0;
             }
-            rows_at[wave][mine_at] = p.cache.at((uint32_t)page, place, kv) * X::kBytes;
+            lds.rows[wave][mine_at] = p.cache.at((uint32_t)page, place, kv) * X::kBytes;
             if constexpr (EIGHT)
                 scale_next = scales[p.cache.scale_at((uint32_t)page, place, kv)];
             __builtin_amdgcn_wave_barrier();
 #pragma unroll
             for (int gr = 0; gr < X::kGroups; ++gr) {
-                krow[gr] = keys + rows_at[wave][gr * 16 + n] + kd;
+                krow[gr] = keys + lds.rows[wave][gr * 16 + n] + kd;
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    vrow[gr][i] = values + rows_at[wave][gr * 16 + 4 * g + i] + vd;
+                    vrow[gr][i] = values + lds.rows[wave][gr * 16 + 4 * g + i] + vd;
             }
             __builtin_amdgcn_wave_barrier();
         };
-        if (t0 < t1) {
+        if (t0 < tend) {
             uint32_t place, place_next;
-            int32_t page = look(t0, place), page_next = look(t0 + kStep, place_next);
+            int32_t page = look(t0, place), page_next = look(t0 + teams.pass, place_next);
             rows(t0, page, place);
-            x.template load_keys<EXACT>(krow, g, dim);
-            x.template load_values<EXACT>(vrow, n, dim);
-            for (; t0 < t1; t0 += kStep) {
-                float ks[X::kGroups][4], vs[X::kGroups][4];
-                if constexpr (EIGHT) {
-                    scales_at[wave][lane / 32u][mine_at] = scale_next;
-                    __builtin_amdgcn_wave_barrier();
+            auto loop = [&](auto nt) {
+                constexpr bool NT = decltype(nt)::value;
+                x.template load_keys<EXACT, NT>(krow, g, dim);
+                x.template load_values<EXACT, NT>(vrow, n, dim);
+                for (; t0 < t1; t0 += teams.pass) {
+                    float ks[X::kGroups][4], vs[X::kGroups][4];
+                    if constexpr (EIGHT) {
+                        lds.scales[wave][lane / 32u][mine_at] = scale_next;
+                        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+                        for (int gr = 0; gr < X::kGroups; ++gr)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                ks[gr][i] = lds.scales[wave][0][gr * 16 + 4 * g + i];
+                                vs[gr][i] = lds.scales[wave][1][gr * 16 + 4 * g + i];
+                            }
+                        __builtin_amdgcn_wave_barrier();
+                    }
+                    rows(t0 + teams.pass, page_next, place_next);
+                    page_next = look(t0 + 2 * teams.pass, place_next);
+                    f32x4 s[X::kGroups];
+                    x.scores(s);
+                    matrix_done(s);
+                    // (also behind the last tile, where there is nothing to load: behind a branch the
+                    // compiler would wait for the keys where it needs the values)
+                    x.template load_keys<EXACT, NT>(krow, g, dim);
+                    float w[X::kGroups][4], most = -__builtin_inff();
 #pragma unroll
                     for (int gr = 0; gr < X::kGroups; ++gr)
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            ks[gr][i] = scales_at[wave][0][gr * 16 + 4 * g + i];
-                            vs[gr][i] = scales_at[wave][1][gr * 16 + 4 * g + i];
+                            float f = factor;
+                            if constexpr (EIGHT)
+                                f = f * ks[gr][i];
+                            w[gr][i] = s[gr][i] * f;
                         }
-                    __builtin_amdgcn_wave_barrier();
-                }
-                rows(t0 + kStep, page_next, place_next);
-                page_next = look(t0 + 2 * kStep, place_next);
-                f32x4 s[X::kGroups];
-                x.scores(s);
-                x.template load_keys<EXACT>(krow, g, dim);
-
-                const bool whole = t0 + X::kTokens <= t1;
-                float w[X::kGroups][4], most = -__builtin_inff();
+                    if (t0 + X::kTokens > t1) {
 #pragma unroll
-                for (int gr = 0; gr < X::kGroups; ++gr)
+                        for (int gr = 0; gr < X::kGroups; ++gr)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float c = factor;
-                        if constexpr (EIGHT)
-                            c = c * ks[gr][i];
-                        w[gr][i] = s[gr][i] * c;
+                            for (int i = 0; i < 4; ++i)
+                                if (t0 + gr * 16 + 4 * g + i >= t1) {
+                                    w[gr][i] = -__builtin_inff();
+                                    if constexpr (EIGHT)
+                                        vs[gr][i] = 0.0f;
+                                    x.drop_values(gr, i);
+                                }
                     }
-                if (!whole) {
 #pragma unroll
                     for (int gr = 0; gr < X::kGroups; ++gr)
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            if (t0 + gr * 16 + 4 * g + i >= t1) {
-                                w[gr][i] = -__builtin_inff();
-                                if constexpr (EIGHT)
-                                    vs[gr][i] = 0.0f;
-                                x.drop_values(gr, i);
-                            }
-                }
+                            most = w[gr][i] > most ? w[gr][i] : most;
+                    if (__ballot(most > ref + (X::kRoom - X::kBias)) != 0) {
+                        // (a NaN raises nothing; it reaches the sums by its own weight)
+                        most = max_query(most);
+                        const float next = most > ref ? most : ref;
+                        const float shift = next == -__builtin_inff() ? 0.0f : next;
+                        const float keep = __builtin_amdgcn_exp2f(ref - shift);
+                        sum = sum * keep;
 #pragma unroll
-                for (int gr = 0; gr < X::kGroups; ++gr)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        most = w[gr][i] > most ? w[gr][i] : most;
-                if (__ballot(most > ref + (X::kRoom - X::kBias)) != 0) {
-                    // (a NaN raises nothing; it reaches the sums by its own weight)
-                    const float next = max_query(most) > ref ? max_query(most) : ref;
-                    const float shift = next == -__builtin_inff() ? 0.0f : next;
-                    const float keep = __builtin_amdgcn_exp2f(ref - shift);
-                    sum = sum * keep;
-#pragma unroll
-                    for (int t = 0; t < DP / 16; ++t)
-                        x.o[t] = x.o[t] * keep;
-                    ref = next;
-                }
-                const float shift = (ref == -__builtin_inff() ? 0.0f : ref) - X::kBias;
-#pragma unroll
-                for (int gr = 0; gr < X::kGroups; ++gr)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        w[gr][i] = __builtin_amdgcn_exp2f(w[gr][i] - shift);
-                        sum += w[gr][i];
-                        if constexpr (EIGHT)
-                            w[gr][i] = w[gr][i] * vs[gr][i];
+                        for (int t = 0; t < DP / 16; ++t)
+                            x.o[t] = x.o[t] * keep;
+                        ref = next;
                     }
-                x.accumulate(w);
-                x.template load_values<EXACT>(vrow, n, dim);
-            }
+                    const float shift = (ref == -__builtin_inff() ? 0.0f : ref) - X::kBias;
+#pragma unroll
+                    for (int gr = 0; gr < X::kGroups; ++gr)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            w[gr][i] = __builtin_amdgcn_exp2f(w[gr][i] - shift);
+                            sum += w[gr][i];
+                            if constexpr (EIGHT)
+                                w[gr][i] = w[gr][i] * vs[gr][i];
+                        }
+                    x.accumulate(w);
+                    x.template load_values<EXACT, NT>(vrow, n, dim);
+                    matrix_done();
+                }
+            };
+            if (stream)
+                loop(std::true_type{});
+            else
+                loop(std::false_type{});
         }
 
-        // ---- the waves' sums together -----------------------------------------
+        // ---- the waves' sums to LDS -----------------------------------------------
         sum = sum_query(sum);
         if (g == 0) {
-            refs[wave][n] = ref;
-            weights[wave][n] = sum;
+            lds.refs[wave][n] = ref;
+            lds.weights[wave][n] = sum;
         }
         const bool any_bad = __ballot(bad) != 0;
         if (lane == 0)
-            flags[wave] = any_bad;
+            lds.bad[wave] = any_bad;
 #pragma unroll
         for (int t = 0; t < DP / 16; ++t)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                sums[wave][n][X::result_dim(t, g, i)] = x.o[t][i];
-        __syncthreads();
+                lds.sums[wave][n][X::result_dim(t, g, i)] = x.o[t][i];
+        meet();
 
-        // A thread takes eight dims of one query, or of two.
-        constexpr uint32_t kPieces = DP / 8, kAtOnce = kAttendThreads / kPieces;
-        constexpr uint32_t kTurns = (kTileQueries + kAtOnce - 1) / kAtOnce;
-        const uint32_t d0 = threadIdx.x % kPieces * 8u;
-        float top[kTurns], total[kTurns], y[kTurns][8];
+        // ---- and together: the waves', then, where several teams share the unit, those of
+        // a group of teams, then those of the groups; by the last team to arrive ---------
+        // A lane of the team takes eight dims of a query, then of another.
+        constexpr uint32_t kPieces = DP / 8;
+        const uint32_t d0 = member % kPieces * 8u;
+        const uint32_t slot_floats = most_queries * (DP + 2u);
+        const bool whole = step0 == 0 && step1 == steps;
+        const CacheJoin join = {whole ? share : plan.owner(here), whole ? share : plan.owner(here + steps - 1u)};
+        uint32_t stage = 0, parts = 0;  // slots of a sum
+        for (;;) {
+            const CacheJoin::Parts from_slots = join.parts(share, stage);
+            const bool done = stage == 0 ? whole : stage == 2 || join.groups() == 1u;
+            for (uint32_t q = member / kPieces; q < queries; q += 64u * teams.waves / kPieces) {
+                float top = -__builtin_inff(), total = 0.0f, y[8] = {};
+                // `count` parts of references r, sums of weights l and sums f
+                auto add = [&](auto parts_at_once, uint32_t count, const float *r, const float *l, const float (*f)[8]) {
+                    constexpr uint32_t N = decltype(parts_at_once)::value;
+                    const float last = top;
 #pragma unroll
-        for (uint32_t u = 0; u < kTurns; ++u) {
-            const uint32_t q = (threadIdx.x / kPieces + u * kAtOnce) % kTileQueries;
-            top[u] = -__builtin_inff();
-            total[u] = 0.0f;
-#pragma unroll
-            for (uint32_t w = 0; w < kAttendWaves; ++w)
-                top[u] = refs[w][q] > top[u] ? refs[w][q] : top[u];
-            const float shift = top[u] == -__builtin_inff() ? 0.0f : top[u];
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                y[u][e] = 0.0f;
-#pragma unroll
-            for (uint32_t w = 0; w < kAttendWaves; ++w) {
-                const float keep = __builtin_amdgcn_exp2f(refs[w][q] - shift);
-                total[u] += weights[w][q] * keep;
-                if (flags[w] != 0)
-                    total[u] = __builtin_nanf("");
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    y[u][e] += sums[w][q][d0 + e] * keep;
-            }
-        }
-
-        // ---- and the workgroups', where several share the unit ----------------
-        bool done = step0 == 0 && step1 == steps;
-        if (!done) {
-            const CacheJoin join = {plan.owner(here), plan.owner(here + steps - 1u)};
-            auto keep_slot = [&](uint32_t slot) {
-                float *to = slots + (uint64_t)slot * attend_slot(DP);
-#pragma unroll
-                for (uint32_t u = 0; u < kTurns; ++u) {
-                    const uint32_t q = threadIdx.x / kPieces + u * kAtOnce;
-                    if (q >= queries)
-                        continue;
-#pragma unroll
-                    for (int e = 0; e < 8; e += 2)
-                        share_pair(to + q * DP + d0 + e, y[u][e], y[u][e + 1]);
-                    if (d0 == 0)
-                        share_pair(to + kTileQueries * DP + 2 * q, top[u], total[u]);
-                }
-            };
-            // Whether this workgroup is the last of `count` to come here.
-            auto arrive = [&](uint32_t counter, uint32_t count) {
-                shared_stores_done();
-                __syncthreads();
-                if (threadIdx.x == 0) {
-                    const uint32_t old = __hip_atomic_fetch_add(counters + counter, 1u, __ATOMIC_RELAXED,
-                                                                __HIP_MEMORY_SCOPE_AGENT);
-                    flags[0] = old + 1u == count;
-                    if (old + 1u == count)
-                        __hip_atomic_store(counters + counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-                }
-                __syncthreads();
-                return flags[0] != 0;
-            };
-            // The slots' sums together, in order, four slots' loads under way at once.
-            auto add_slots = [&](auto slot_of, uint32_t count) {
-#pragma unroll
-                for (uint32_t u = 0; u < kTurns; ++u) {
-                    const uint32_t q = (threadIdx.x / kPieces + u * kAtOnce) % kTileQueries;
-                    top[u] = -__builtin_inff();
-                    total[u] = 0.0f;
+                    for (uint32_t j = 0; j < N; ++j)
+                        top = r[j] > top ? r[j] : top;
+                    const float shift = top == -__builtin_inff() ? 0.0f : top;
+                    const float a = __builtin_amdgcn_exp2f(last - shift);
+                    total = total * a;
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
-                        y[u][e] = 0.0f;
-                    if (q >= queries)
-                        continue;
-                    constexpr uint32_t kBatch = 4;
-                    for (uint32_t i = 0; i < count; i += kBatch) {
-                        f32x2 f[kBatch][4], s[kBatch];
+                        y[e] = y[e] * a;
 #pragma unroll
-                        for (uint32_t j = 0; j < kBatch; ++j) {
-                            // (past the last: the last again, without weight)
-                            const float *at = slots + (uint64_t)slot_of(i + j < count ? i + j : count - 1u) * attend_slot(DP);
-                            s[j] = shared_pair(at + kTileQueries * DP + 2 * q);
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                f[j][e] = shared_pair(at + q * DP + d0 + 2 * e);
-                        }
-#pragma unroll
-                        for (uint32_t j = 0; j < kBatch; ++j) {
-                            if (i + j >= count)
-                                break;
-                            const float next = s[j][0] > top[u] ? s[j][0] : top[u];
-                            const float shift = next == -__builtin_inff() ? 0.0f : next;
-                            const float a = __builtin_amdgcn_exp2f(top[u] - shift), b = __builtin_amdgcn_exp2f(s[j][0] - shift);
-                            top[u] = next;
-                            total[u] = total[u] * a + s[j][1] * b;
+                    for (uint32_t j = 0; j < N; ++j)
+                        if (j < count) {
+                            const float b = __builtin_amdgcn_exp2f(r[j] - shift);
+                            total += l[j] * b;
 #pragma unroll
                             for (int e = 0; e < 8; ++e)
-                                y[u][e] = y[u][e] * a + f[j][e / 2][e % 2] * b;
+                                y[e] += f[j][e] * b;
                         }
-                    }
-                }
-            };
-            keep_slot(join.slot(share));
-            const uint32_t f = join.first(share), l = join.last(share);
-            if (arrive(join.group_counter(share), l - f + 1u)) {
-                add_slots([&](uint32_t i) { return join.slot(f + i); }, l - f + 1u);
-                done = join.groups() == 1u;
-                if (!done) {
-                    __syncthreads();
-                    keep_slot(join.slot(f));
-                    if (arrive(join.unit_counter(), join.groups())) {
-                        const uint32_t g0 = join.w0 / kJoinGroup;
-                        add_slots([&](uint32_t i) { return join.slot(join.first((g0 + i) * kJoinGroup > join.w0 ? (g0 + i) * kJoinGroup : join.w0)); },
-                                  join.groups());
-                        done = true;
-                    }
-                }
-            }
-        }
-
-        // ---- the unit's results ------------------------------------------------
-        if (done) {
+                };
+                // All loads are under way at once; past the last part the last again, left out.
+                if (stage == 0) {
+                    float r[kAttendWaves], l[kAttendWaves], f[kAttendWaves][8];
 #pragma unroll
-            for (uint32_t u = 0; u < kTurns; ++u) {
-                const uint32_t q = threadIdx.x / kPieces + u * kAtOnce;
-                const bool there = q < queries && d0 < dim;
-                const uint64_t row = (uint64_t)seq * p.heads + head0 + q;
+                    for (uint32_t j = 0; j < kAttendWaves; ++j) {
+                        const uint32_t w = wave0 + q / kTileQueries + (j < waves_deep ? j : waves_deep - 1u) * teams.side;
+                        const uint32_t k = q % kTileQueries;
+                        r[j] = lds.refs[w][k];
+                        l[j] = lds.bad[w] != 0 ? __builtin_nanf("") : lds.weights[w][k];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            f[j][e] = lds.sums[w][k][d0 + e];
+                    }
+                    add(std::integral_constant<uint32_t, kAttendWaves>{}, waves_deep, r, l, f);
+                } else {
+                    for (uint32_t i = 0; i < parts; i += kJoinLoads) {
+                        float r[kJoinLoads], l[kJoinLoads], f[kJoinLoads][8];
+#pragma unroll
+                        for (uint32_t j = 0; j < kJoinLoads; ++j) {
+                            const uint32_t at = i + j < parts ? i + j : parts - 1u;
+                            const uint32_t part = at == 0 ? from_slots.first : from_slots.next + (at - 1u) * from_slots.by;
+                            const float *slot = p.slots + (uint64_t)part * slot_floats;
+                            const f32x2 s = shared_pair(slot + most_queries * DP + 2 * q);
+                            r[j] = s[0];
+                            l[j] = s[1];
+#pragma unroll
+                            for (int e = 0; e < 8; e += 2) {
+                                const f32x2 v = shared_pair(slot + q * DP + d0 + e);
+                                f[j][e] = v[0];
+                                f[j][e + 1] = v[1];
+                            }
+                        }
+                        add(std::integral_constant<uint32_t, kJoinLoads>{}, parts - i, r, l, f);
+                    }
+                }
+                if (!done) {
+                    // (a group's sums: in the place of its first, which this wave alone has read)
+                    float *slot = p.slots + (uint64_t)join.slot(stage == 0 ? share : join.first(share)) * slot_floats;
+#pragma unroll
+                    for (int e = 0; e < 8; e += 2)
+                        share_pair(slot + q * DP + d0 + e, y[e], y[e + 1]);
+                    if (d0 == 0)
+                        share_pair(slot + most_queries * DP + 2 * q, top, total);
+                    continue;
+                }
                 const bool empty = length == 0;
-                float r[8];
+                const uint64_t out_row = (uint64_t)seq * p.heads + head0 + q;
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    r[e] = empty ? 0.0f : y[u][e] / total[u];
-                if (p.has_lse != 0 && there && d0 == 0)
-                    p.lse[rank][row] = empty ? -__builtin_inff()
-                                             : ((top[u] == -__builtin_inff() ? 0.0f : top[u]) - X::kBias) * kLn2 +
-                                                   __builtin_logf(total[u]);
+                    y[e] = empty ? 0.0f : y[e] / total;
+                if (p.has_lse != 0 && d0 == 0)
+                    p.lse[rank][out_row] = empty ? -__builtin_inff()
+                                                 : ((top == -__builtin_inff() ? 0.0f : top) - X::kBias) * kLn2 +
+                                                       __builtin_logf(total);
                 if constexpr (EIGHT_OUT) {
                     // 16 neighbouring lanes hold the 128 columns of a scale
-                    const float s = scale_of(max16(max_bits(r)));
-                    const Eights<8> e = to_eights(r, s);
-                    if (there) {
-                        store_eights<false>(p.out[rank] + row * dim + d0, e);
-                        if (d0 % AR_SCALE_BLOCK == 0)
-                            p.out_scales[rank][((uint64_t)(head0 + q) * dim + d0) / AR_SCALE_BLOCK * p.seqs + seq] = s;
-                    }
-                } else if (there) {
-                    char *at_out = p.out[rank] + (row * dim + d0) * T::kBytes;
+                    const float s = scale_of(max16(max_bits(y)));
+                    store_eights<false>(p.out[rank] + out_row * dim + d0, to_eights(y, s));
+                    if (d0 % AR_SCALE_BLOCK == 0)
+                        p.out_scales[rank][((uint64_t)(head0 + q) * dim + d0) / AR_SCALE_BLOCK * p.seqs + seq] = s;
+                } else if (EXACT || d0 < dim) {
+                    char *at = p.out[rank] + (out_row * dim + d0) * T::kBytes;
                     constexpr int E = kPiece<T>;
 #pragma unroll
                     for (int i = 0; i < 8 / E; ++i) {
                         float f[E];
 #pragma unroll
                         for (int e = 0; e < E; ++e)
-                            f[e] = r[i * E + e];
-                        store_piece<false>(at_out + i * 16, narrow_piece<T>(f));
+                            f[e] = y[i * E + e];
+                        store_piece<false>(at + i * 16, narrow_piece<T>(f));
                     }
                 }
             }
+            if (done)
+                break;
+            // Whether this team is the last to come here.
+            const uint32_t counter = stage == 0 ? join.group_counter(share) : join.unit_counter();
+            const uint32_t count = stage == 0 ? join.last(share) - join.first(share) + 1u : join.groups();
+            shared_stores_done();
+            meet();
+            uint32_t last = 0;
+            if (member == 0) {
+                const uint32_t old = __hip_atomic_fetch_add(counters + counter, 1u, __ATOMIC_RELAXED,
+                                                            __HIP_MEMORY_SCOPE_AGENT);
+                last = old + 1u == count;
+                if (last != 0)
+                    __hip_atomic_store(counters + counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                lds.last = last;
+            }
+            meet();
+            if ((alone ? uniform(last) : uniform(lds.last)) == 0)
+                break;
+            ++stage;
+            parts = count;
         }
 
         left -= step1 - step0;
@@ -786,11 +879,15 @@ __global__ __launch_bounds__(kAttendThreads, (Tile<T, EIGHT, DP>::kPerCu)) void 
             return;
         here += steps;
         step0 = 0;
-        if (++seq == p.seqs) {
-            seq = 0;
-            ++unit;
+        if (++unit == across) {
+            unit = 0;
+            if (++seq == p.seqs) {
+                seq = 0;
+                ++rank;
+            }
+            length = length_of(seq);
         }
-        __syncthreads();  // the sums in LDS are read before the next piece's are written
+        meet();  // the sums in LDS are read before the next piece's are written
     }
 }
 
@@ -798,15 +895,16 @@ __global__ __launch_bounds__(kAttendThreads, (Tile<T, EIGHT, DP>::kPerCu)) void 
 inline uint32_t attend_most(int per_cu, int cu_count) { return (uint32_t)(per_cu * cu_count) / 8u * 8u; }
 
 template <typename T, bool EIGHT, int DP, bool EXACT, bool EIGHT_OUT>
-hipError_t enqueue_attend(const CacheAttentionArgs &args, int cu_count, hipStream_t stream)
+hipError_t enqueue_attend(CacheAttentionArgs args, int cu_count, hipStream_t stream)
 {
     typedef Tile<T, EIGHT, DP> X;
     const uint64_t capacity = args.table_pages * args.cache.page_tokens;
     const uint64_t tokens = args.window != 0 && args.window < capacity ? args.window : capacity;
-    const uint64_t steps = (tokens - 1u) / (X::kTokens * kAttendWaves) + 1u;
-    const uint32_t group = args.heads / args.cache.heads;
-    const uint64_t units = (uint64_t)args.nranks * args.cache.heads * args.seqs *
-                           ((group + kTileQueries - 1u) / kTileQueries);
+    args.passes = passes_of_a_step(args.seqs, args.nranks, args.cache.heads, args.group, X::kTokenShift, tokens);
+    // (a call of few steps has fewer workgroups)
+    const CacheTeams teams(args.group, X::kTokenShift, args.passes, false);
+    const uint64_t units = (uint64_t)args.nranks * args.cache.heads * args.seqs * teams.tiles;
+    const uint64_t steps = ((tokens - 1u) >> teams.shift) + 1u;
     uint64_t grid = attend_most(X::kPerCu, cu_count);
     if (steps < grid && units * steps < grid)
         grid = (units * steps + 7u) / 8u * 8u;

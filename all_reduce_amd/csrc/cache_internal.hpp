@@ -79,11 +79,14 @@ struct CacheAttentionArgs {
     uint64_t q_stride;  // elements
     uint64_t table_pages;
     uint64_t window;    // 0: all
-    char *work;
+    char *work;         // the workspace's counters
+    float *slots;       // its partial sums
     uint32_t seqs;
     uint32_t heads;     // query heads
+    uint32_t group;     // of a key-value head
     uint32_t nranks;
     uint32_t has_lse;
+    uint32_t passes;    // of a step, as a power of two (the launcher sets it)
     float scale;
 };
 
@@ -94,6 +97,9 @@ hipError_t launch_cache_read(const CacheCopyArgs &args, int dtype, bool eight, i
                              int cu_count, hipStream_t stream);
 hipError_t launch_cache_attention(const CacheAttentionArgs &args, int dtype, bool eight,
                                   bool eight_out, int cu_count, hipStream_t stream);
-uint64_t cache_attention_workspace(uint32_t dim, int cu_count);
+// Bytes of workspace for heads of `dim`, `group` query heads to a key-value head, and
+// of the counters it begins with.
+uint64_t cache_attention_workspace(uint32_t dim, uint32_t group, int cu_count);
+uint64_t cache_attention_counters(int cu_count);
 
 }  // namespace ar

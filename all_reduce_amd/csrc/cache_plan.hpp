@@ -2,30 +2,23 @@
 // for the kernel and for tests on the host.
 //
 // The host does not know the lengths (they change between replays of a graph),
-// so the grid is fixed and each workgroup finds its own share.  A unit is the
-// attention of 16 query heads (or fewer) of one key-value head of one rank over
-// one sequence; its work comes in steps of `step` tokens, at least one, so that
-// an empty sequence is visited too.  All units' steps stand in one row, unit
-// group (rank, key-value head, query tile) after unit group and sequence after
-// sequence, and are cut into equal shares of whole steps.  A share's first and
-// last piece may be parts of a unit: such a piece's sums wait in the
-// workspace, and the last of the unit's workgroups to arrive joins them.
-// Shares that are equal whatever the lengths are keep a batch of one long and
-// many short sequences as balanced as one of equal ones.
+// so the grid is fixed and each team of waves finds its own share.  A unit is the
+// attention of up to 16 query heads (64 where a team's waves share the tokens' keys
+// and values) of one key-value head of one rank over one sequence; its work comes in
+// steps of `step` tokens, at least one, so that an empty sequence is visited too.
+// All units' steps stand in one row, by rank, then sequence, then key-value head and
+// tile of query heads (heads that lie side by side in memory are read side by side),
+// and are cut into equal shares of whole steps.  A share's first
+// and last piece may be parts of a unit: such a piece's sums wait in the workspace,
+// and the last of the unit's teams to arrive joins them.  Shares that are equal
+// whatever the lengths are keep a batch of one long and many short sequences as
+// balanced as one of equal ones.
 #pragma once
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
 namespace ar {
-
-// a / b; the 32-bit quotient is several times cheaper.
-__host__ __device__ inline uint64_t divide(uint64_t a, uint64_t b)
-{
-    if (((a | b) >> 32) == 0)
-        return (uint32_t)a / (uint32_t)b;
-    return a / b;
-}
 
 // The tokens of a sequence that are attended to: [first, end).  False where the
 // length is none.
@@ -41,51 +34,115 @@ __host__ __device__ inline bool attended(int32_t length, uint64_t capacity, uint
     return true;
 }
 
-__host__ __device__ inline uint32_t steps_of(uint32_t first, uint32_t end, uint32_t step)
+// Steps of 2^shift tokens.
+__host__ __device__ inline uint32_t steps_of(uint32_t first, uint32_t end, uint32_t shift)
 {
     const uint32_t n = end - first;
-    return n == 0 ? 1u : (n - 1u) / step + 1u;
+    return n == 0 ? 1u : ((n - 1u) >> shift) + 1u;
 }
 
-// `total` steps over `sharers` workgroups, of which the first `extra` take one
-// more than `per`.
+// `total` steps over `sharers` teams, of which the first `extra` take one more than
+// `per`.  There are at most `teams`, a multiple of 8.
 struct CachePlan {
-    uint64_t per;
-    uint32_t extra, sharers;
-    __host__ __device__ CachePlan(uint64_t total, uint32_t grid, uint32_t least)
+    uint32_t per, extra, sharers;
+    __host__ __device__ CachePlan(uint32_t total, uint32_t teams)
     {
-        const uint64_t most = divide(total + least - 1u, least);
-        sharers = most < grid ? (uint32_t)most : grid;
-        per = divide(total, sharers);
-        extra = (uint32_t)(total - per * sharers);
+        // (divisions are long chains: a call of few steps has none)
+        sharers = total < teams ? total : teams;
+        per = total <= teams ? 1u : total / teams;
+        extra = total - per * sharers;
     }
-    __host__ __device__ uint64_t start(uint32_t w) const
+    __host__ __device__ uint32_t start(uint32_t w) const
     {
         return w * per + (w < extra ? w : extra);
     }
-    // The workgroup whose share holds step i.
-    __host__ __device__ uint32_t owner(uint64_t i) const
+    // The team whose share holds step i.
+    __host__ __device__ uint32_t owner(uint32_t i) const
     {
-        const uint64_t cut = (per + 1u) * extra;
-        return (uint32_t)(i < cut ? divide(i, per + 1u) : extra + divide(i - cut, per));
+        const uint32_t cut = (per + 1u) * extra;
+        if (i < cut)
+            return i / (per + 1u);
+        return extra + (per == 1u ? i - cut : (i - cut) / per);
     }
-    // The share of workgroup `block` of the grid, or ~0: none.  Workgroup b runs on
-    // XCD b % 8; shares that follow one another lie on one XCD, and few shares on
-    // all of them.
-    __host__ __device__ uint32_t share(uint32_t block) const
+    // The share of team `team` of workgroup `block`, or ~0: none.  Workgroup b runs on
+    // XCD b % 8; shares that follow one another lie on one XCD, and few shares on all
+    // of them, and on all their compute units before one has two.
+    __host__ __device__ uint32_t share(uint32_t block, uint32_t team, uint32_t grid) const
     {
-        const uint32_t each = (sharers + 7u) / 8u, w = block % 8u * each + block / 8u;
-        return block / 8u < each && w < sharers ? w : ~0u;
+        const uint32_t each = (sharers + 7u) / 8u, i = block / 8u + team * (grid / 8u);
+        const uint32_t w = block % 8u * each + i;
+        return i < each && w < sharers ? w : ~0u;
     }
 };
 
-// The workspace: counters first, then two slots of partial sums a workgroup, one
-// for the unit that its share begins inside, one for the unit that it ends inside.
-// Partial sums are joined in two steps, 16 consecutive workgroups first, so that
-// one long sequence is not joined by one workgroup alone.
+// How a launch's waves make teams.  Four waves of a workgroup share a unit's tokens;
+// with more than 16 query heads to a key-value head, two or all four of them take
+// the same tokens and 16 heads each, so that keys and values come from memory once
+// for 64.  Where there are more units than workgroups, and short ones, each wave is a
+// team, and its
+// steps are longer: a team's way into and out of a unit is a chain of loads that four
+// waves do not shorten.  On MI355X 2048 units of 33 tokens take 16 us that way and 25 with
+// four waves, of 133 tokens 37 and 44; of 333 tokens 110 and 79, so long sequences have
+// four.
+struct CacheTeams {
+    uint32_t waves;  // of a team
+    uint32_t side;   // waves that take the same tokens
+    uint32_t tiles;  // of 16 * side query heads: units of a sequence and key-value head
+    uint32_t pass;   // tokens that the team takes at once
+    uint32_t shift;  // 2^shift tokens are a step
+    // `tokens`: 2^tokens are a wave's tile; 2^passes of a step.
+    __host__ __device__ CacheTeams(uint32_t group, uint32_t tokens, uint32_t passes, bool alone)
+    {
+        const uint32_t t = (group + 15u) / 16u;
+        const uint32_t beside = alone || t == 1u ? 0u : t == 2u ? 1u : 2u, behind = alone ? 0u : 2u - beside;
+        waves = alone ? 1u : 4u;
+        side = 1u << beside;
+        tiles = (t + side - 1u) >> beside;
+        pass = 1u << (behind + tokens);
+        shift = behind + tokens + passes;
+    }
+};
+
+// Whether each wave is to be a team, for units of a batch whose sequences have `tiles`
+// tiles of tokens together; and the passes of its step, for most sequences a power of
+// two that takes all of them.
+__host__ __device__ inline bool waves_alone(uint32_t units, uint32_t grid, uint32_t tiles, uint32_t seqs)
+{
+    return units > grid && tiles <= 8u * seqs;
+}
+
+__host__ __device__ inline uint32_t passes_alone(uint32_t tiles, uint32_t seqs)
+{
+    return tiles <= seqs ? 2u : tiles <= 2u * seqs ? 3u : tiles <= 4u * seqs ? 4u : 5u;
+}
+
+// A sequence's part of `tiles` (no more than counts).
+__host__ __device__ inline uint32_t tiles_of(uint32_t first, uint32_t end, uint32_t tokens)
+{
+    const uint32_t n = steps_of(first, end, tokens);
+    return n < 1u << 12 ? n : 1u << 12;
+}
+
+// The smallest power of two of passes to a step (as its exponent) with which all steps
+// of a call can be counted in 31 bits whatever its lengths are: 0, but for calls of
+// extreme sizes.
+inline uint32_t passes_of_a_step(uint64_t seqs, uint64_t ranks, uint64_t heads, uint32_t group,
+                                 uint32_t tokens, uint64_t most_tokens)
+{
+    const uint64_t units = seqs * ranks * heads * ((group + 15u) / 16u);
+    uint32_t passes = 0;
+    while (units * ((most_tokens >> (tokens + passes)) + 1u) >= (uint64_t)1 << 31 && passes < 24u)
+        ++passes;
+    return passes;
+}
+
+// The workspace: counters first, then two slots of partial sums a team, one for
+// the unit that its share begins inside, one for the unit that it ends inside.
+// Partial sums are joined in two steps, 16 consecutive teams first, so that one
+// long sequence is not joined by one team alone.
 constexpr uint32_t kJoinGroup = 16;
 struct CacheJoin {
-    uint32_t w0, w1;  // the unit's first and last workgroup
+    uint32_t w0, w1;  // the unit's first and last team
     __host__ __device__ uint32_t slot(uint32_t w) const { return 2u * w + (w == w0 ? 1u : 0u); }
     // The group of w: its first and last member.
     __host__ __device__ uint32_t first(uint32_t w) const
@@ -99,14 +156,25 @@ struct CacheJoin {
         return g < w1 ? g : w1;
     }
     __host__ __device__ uint32_t groups() const { return w1 / kJoinGroup - w0 / kJoinGroup + 1u; }
-    // A workgroup begins at most one group inside its share (its last piece's unit
-    // starts there) and one as the first of 16; and at most one unit.
+    // A team begins at most one group inside its share (its last piece's unit starts
+    // there) and one as the first of 16; and at most one unit.
     __host__ __device__ uint32_t group_counter(uint32_t w) const
     {
         const uint32_t f = first(w);
         return 4u * f + (f == w0 ? 0u : 1u);
     }
     __host__ __device__ uint32_t unit_counter() const { return 4u * w0 + 2u; }
+    // The slots that w joins in stage 1, its group's teams', or 2, the groups': `first`,
+    // then `next`, next + `by` and so on.
+    struct Parts {
+        uint32_t first, next, by;
+    };
+    __host__ __device__ Parts parts(uint32_t w, uint32_t stage) const
+    {
+        const uint32_t f = stage == 1u ? first(w) : w0;
+        return {slot(f), 2u * (stage == 1u ? f + 1u : (w0 / kJoinGroup + 1u) * kJoinGroup),
+                stage == 1u ? 2u : 2u * kJoinGroup};
+    }
 };
 
 }  // namespace ar

@@ -104,7 +104,8 @@ arResult_t arCacheRead(const int64_t *slots, size_t tokens, const arCacheLayout_
  *
  * Scores, exponentials, sums and accumulators are binary32.  (The products of the
  * exponentials with values of 16 and 8 bits take the exponentials in two parts of
- * that type, or three for a float32 output, which hold 16, 22 or 24 bits of them.)
+ * that type, or three for a float32 output, which hold 16, 22 or 24 bits of them; an
+ * infinite value gives an infinity or, where a part is 0, NaN.)
  * The order of a sum follows from the sizes, the lengths and the card's number of
  * compute units, never from values or from other calls.  Only tokens first .. n - 1
  * and the table's entries for them are read, whatever the other places hold.
@@ -129,10 +130,11 @@ arResult_t arCacheRead(const int64_t *slots, size_t tokens, const arCacheLayout_
  *               arUnsupported; arGateQuant quantises other outputs).
  *  lse          host array of nranks device pointers [seqs][heads], or NULL.
  *  workspace    device memory of at least the bytes that arCacheAttentionWorkspace
- *               names for this dim, zeros before its first use; every call leaves it
- *               fit for the next.  One call at a time may use it: calls that may run
+ *               names for this dim and heads / cache->heads, zeros before its first
+ *               use; every call leaves it fit for the next.  One call at a time may use it: calls that may run
  *               at once, in graphs as well, need one each.
- *  seqs         at most 65536 (else arUnsupported).
+ *  seqs         at most 65536, and seqs * heads * nranks at most 2^30 (else
+ *               arUnsupported).
  * Rules (arInvalidArgument when broken): no NULL pointer but those named; every
  * pointer 16-byte aligned, pageTable and lengths 4-byte aligned; tablePages >= 1;
  * no written range (the workspace's is one) overlaps another. */
@@ -147,8 +149,9 @@ arResult_t arCacheAttention(const void *const *queries, size_t queryStride,
                             arStream_t stream);
 
 /* Bytes of workspace that arCacheAttention needs on the communicator's device for
- * heads of `dim`, whatever its other arguments. */
-arResult_t arCacheAttentionWorkspace(size_t dim, arComm_t comm, size_t *bytes);
+ * heads of `dim` and `group` query heads to a key-value head (1 .. 4096), whatever its
+ * other arguments.  One that is large enough for several calls may serve them in turn. */
+arResult_t arCacheAttentionWorkspace(size_t dim, size_t group, arComm_t comm, size_t *bytes);
 
 #ifdef __cplusplus
 }

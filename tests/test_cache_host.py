@@ -35,7 +35,7 @@ def test_constants_and_layout_match_the_header():
 def test_header_is_c99(tmp_path):
     src = tmp_path / "t.c"
     src.write_text('#include "ar_cache.h"\narCacheLayout_t layout = {4, 16, 2, 128, 4096, 2048, 128};\n'
-                   'arResult_t (*const call)(size_t, arComm_t, size_t *) = arCacheAttentionWorkspace;\n')
+                   'arResult_t (*const call)(size_t, size_t, arComm_t, size_t *) = arCacheAttentionWorkspace;\n')
     res = subprocess.run(["gcc", "-std=c99", "-Wall", "-Wextra", "-Werror", "-c", str(src),
                           f"-I{ROOT / 'include'}", "-o", str(tmp_path / "t.o")],
                          capture_output=True, text=True)
@@ -162,6 +162,7 @@ CASES = [
     ("attend scale nan", T, dict(ATTEND, scale=float("nan")), "arInvalidArgument", "scale"),
     ("attend scale inf", T, dict(ATTEND, scale=float("inf")), "arInvalidArgument", "scale"),
     ("attend 65537 sequences", T, dict(ATTEND, seqs=65537), "arUnsupported", "65536"),
+    ("attend too many units", T, dict(ATTEND, seqs=65536, heads=4096, nranks=5), "arUnsupported", "2^30"),
     ("attend no table", T, dict(ATTEND, table_pages=0), "arInvalidArgument", "tablePages"),
     ("attend table huge", T, dict(ATTEND, table_pages=1 << 31), "arInvalidArgument", "tablePages"),
     ("attend query rows closer than a row", T, dict(ATTEND, query_stride=1016), "arInvalidArgument", "row stride"),
@@ -222,5 +223,6 @@ def test_validation(results, label, name, kw, code, why):
 
 
 def test_workspace_query_refusals():
-    assert ar.arCacheAttentionWorkspace(100, None)[0] == ar.arResult.arUnsupported
-    assert ar.arCacheAttentionWorkspace(128, None)[0] == ar.arResult.arInvalidArgument
+    assert ar.arCacheAttentionWorkspace(100, 8, None)[0] == ar.arResult.arUnsupported
+    assert ar.arCacheAttentionWorkspace(128, 0, None)[0] == ar.arResult.arUnsupported
+    assert ar.arCacheAttentionWorkspace(128, 8, None)[0] == ar.arResult.arInvalidArgument

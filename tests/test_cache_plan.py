@@ -11,38 +11,45 @@ import all_reduce_amd as ar
 SZ, U32, I32, I64 = ctypes.c_size_t, ctypes.c_uint32, ctypes.c_int32, ctypes.c_int64
 
 
-def pieces_of(lengths, capacity, window, step, units, grid, block):
+def pieces_of(lengths, capacity, window, tokens, ranks, heads, group, grid, block, team):
     lib = ar.library()
     fn = lib.ar_cache_attention_share
     fn.restype = SZ
-    fn.argtypes = [ctypes.POINTER(I32), SZ, SZ, SZ, U32, U32, U32, U32, ctypes.c_void_p, SZ]
-    most = len(lengths) * units + 2
-    out = np.zeros((most, 12), dtype=np.uint64)
-    n = fn((I32 * len(lengths))(*lengths), len(lengths), capacity, window, step, units, grid, block,
+    fn.argtypes = [ctypes.POINTER(I32), SZ, SZ, SZ, U32, U32, U32, U32, U32, U32, U32, ctypes.POINTER(U32), ctypes.c_void_p,
+                   SZ]
+    teams = (U32 * 5)()
+    most = 1 << 12
+    out = np.zeros((most, 13), dtype=np.uint32)
+    n = fn(lengths, len(lengths), capacity, window, tokens, ranks, heads, group, grid, block, team, teams,
            out.ctypes.data, most)
     assert n <= most
-    return out[:n].astype(np.int64).tolist()
+    return list(teams), out[:n].astype(np.int64).tolist()
 
 
-def check_plan(lengths, capacity, window, step, units, grid):
+def check_plan(lengths, capacity, window, tokens, ranks, heads, group, grid):
     """Every token of every unit is in one piece; a unit's pieces meet in slots and
-    counters of their own, in the numbers that the workgroups wait for; equal shares."""
-    covered, partial, sizes = {}, {}, []
-    slots = set()
+    counters of their own, in the numbers that the teams wait for; equal shares."""
+    covered, partial, sizes, slots = {}, {}, [], set()
+    array = (I32 * len(lengths))(*lengths)
+    (waves, side, tiles, a_pass, step), _ = pieces_of(array, capacity, window, tokens, ranks, heads, group, grid, 0, 0)
+    assert waves in (1, 4) and side <= waves and a_pass == waves // side << tokens and step >= a_pass and step % a_pass == 0
+    assert (tiles - 1) * side * 16 < group <= tiles * side * 16
+    teams = grid * 4 // waves
     for block in range(grid):
-        pieces = pieces_of(lengths, capacity, window, step, units, grid, block)
-        sizes.append(sum(p[3] - p[2] for p in pieces))
-        for unit, seq, s0, s1, steps, t0, t1, slot, gc, gn, uc, groups in pieces:
-            assert 0 <= unit < units and 0 <= seq < len(lengths) and 0 <= s0 < s1 <= steps
-            covered.setdefault((unit, seq), []).append((s0, s1, t0, t1))
-            if s0 == 0 and s1 == steps:
-                continue
-            assert slot < 2 * grid and gc < 4 * grid and uc < 4 * grid
-            assert slot not in slots
-            slots.add(slot)
-            partial.setdefault((unit, seq), []).append((gc, gn, uc, groups))
-    assert set(covered) == {(u, s) for u in range(units) for s in range(len(lengths))}
-    for (unit, seq), got in covered.items():
+        for team in range(4 // waves):
+            _, pieces = pieces_of(array, capacity, window, tokens, ranks, heads, group, grid, block, team)
+            sizes.append(sum(p[4] - p[3] for p in pieces))
+            for rank, seq, unit, s0, s1, steps, t0, t1, slot, gc, gn, uc, groups in pieces:
+                assert 0 <= rank < ranks and 0 <= seq < len(lengths) and 0 <= unit < tiles * heads and 0 <= s0 < s1 <= steps
+                covered.setdefault((rank, seq, unit), []).append((s0, s1, t0, t1))
+                if s0 == 0 and s1 == steps:
+                    continue
+                assert slot < 2 * teams and gc < 4 * teams and uc < 4 * teams
+                assert slot not in slots
+                slots.add(slot)
+                partial.setdefault((rank, seq, unit), []).append((gc, gn, uc, groups))
+    assert len(covered) == ranks * heads * len(lengths) * tiles
+    for (_, seq, _), got in covered.items():
         n = lengths[seq]
         first = end = 0
         if 0 <= n <= capacity:
@@ -62,6 +69,7 @@ def check_plan(lengths, capacity, window, step, units, grid):
             members.setdefault(gc, []).append(gn)
         for gc, sizes_of in members.items():
             assert all(x == len(sizes_of) for x in sizes_of), (key, gc, sizes_of)
+            assert len(sizes_of) <= 16
         uc, groups = unit_counter.pop()
         assert groups == len(members)
         for c in (*members, uc):
@@ -69,31 +77,58 @@ def check_plan(lengths, capacity, window, step, units, grid):
         assert len({*members, uc}) == len(members) + 1
     busy = [x for x in sizes if x]
     assert max(busy) - min(busy) <= 1
-    assert len(busy) == grid or max(busy) == 1
+    assert len(busy) == teams or max(busy) == 1
+    return waves, side
 
 
 PLANS = [
-    ([0], 128, 0, 128, 1, 8), ([1], 128, 0, 128, 1, 512), ([5000], 1 << 20, 0, 128, 1, 512),
-    ([131072], 1 << 20, 0, 128, 8, 512), ([70001] * 3, 1 << 17, 0, 64, 1, 256), ([0] * 700, 1024, 0, 128, 3, 512),
-    ([-1, 5, 2000, 1025, 0, 1024], 1024, 0, 128, 2, 16), ([2 ** 31 - 1], 2 ** 31 - 1, 0, 128, 1, 512),
-    ([2 ** 31 - 1, 7], 2 ** 31 - 1, 129, 128, 5, 64), ([100000, 3], 1 << 17, 50000, 128, 4, 512),
+    ([0], 128, 0, 5, 1, 1, 1, 8), ([1], 128, 0, 5, 1, 1, 8, 512), ([5000], 1 << 20, 0, 5, 1, 1, 16, 512),
+    ([131072], 1 << 20, 0, 5, 8, 1, 17, 512), ([70001] * 3, 1 << 17, 0, 4, 1, 1, 33, 256),
+    ([0] * 700, 1024, 0, 5, 1, 3, 64, 512), ([-1, 5, 2000, 1025, 0, 1024], 1024, 0, 5, 2, 1, 65, 16),
+    ([2 ** 31 - 1], 2 ** 31 - 1, 0, 5, 1, 1, 8, 512), ([2 ** 31 - 1, 7], 2 ** 31 - 1, 129, 5, 1, 5, 200, 64),
+    ([2 ** 31 - 1] * 9, 2 ** 31 - 1, 0, 5, 8, 4, 16, 512), ([3, 2 ** 31 - 1, 0], 2 ** 31 - 1, 0, 4, 2, 250, 64, 256),
+    ([100000, 3], 1 << 17, 50000, 5, 2, 2, 8, 512), ([20] * 700 + [32768], 1 << 16, 0, 5, 1, 2, 8, 512),
+    ([2 ** 31 - 1] + [1] * 600, 2 ** 31 - 1, 0, 5, 1, 2, 8, 512),
 ]
 
 
-@pytest.mark.parametrize("lengths,capacity,window,step,units,grid", PLANS, ids=[str(i) for i in range(len(PLANS))])
-def test_shares(lengths, capacity, window, step, units, grid):
-    check_plan(lengths, capacity, window, step, units, grid)
+@pytest.mark.parametrize("lengths,capacity,window,tokens,ranks,heads,group,grid", PLANS,
+                         ids=[str(i) for i in range(len(PLANS))])
+def test_shares(lengths, capacity, window, tokens, ranks, heads, group, grid):
+    check_plan(lengths, capacity, window, tokens, ranks, heads, group, grid)
 
 
 def test_drawn_shares():
     rng = random.Random(4)
-    for _ in range(150):
+    seen = set()
+    for _ in range(200):
         seqs = rng.choice([1, 1, 2, 3, 9, 40, 130])
-        longest = rng.choice([1, 130, 2000, 30000])
+        longest = rng.choice([1, 130, 600, 2000, 30000])
         lengths = [int(longest * rng.random() ** 2) for _ in range(seqs)]
         lengths[rng.randrange(seqs)] = longest
-        check_plan(lengths, 32768, rng.choice([0, 0, 1, 100, 5000]), rng.choice([64, 128]), rng.choice([1, 2, 8, 24]),
-                   rng.choice([8, 16, 64, 256, 512]))
+        seen.add(check_plan(lengths, 32768, rng.choice([0, 0, 1, 100, 5000]), rng.choice([4, 5]),
+                            rng.choice([1, 2, 8]), rng.choice([1, 1, 3]), rng.choice([1, 8, 16, 17, 40, 100]),
+                            rng.choice([8, 16, 64, 256])))
+    assert seen == {(1, 1), (4, 1), (4, 2), (4, 4)}
+
+
+def test_parts():
+    """What a group's and a unit's last team reads: every team's slot once, then the
+    slot of every group's first."""
+    fn = ar.library().ar_cache_attention_part
+    fn.restype = U32
+    fn.argtypes = [U32] * 5
+    for w0, w1 in ((0, 1), (3, 5), (15, 16), (0, 511), (7, 40), (16, 31), (31, 32), (5, 2047)):
+        def slot(w):
+            return 2 * w + (w == w0)
+        starts = []
+        for b in range(w0 // 16, w1 // 16 + 1):
+            members = list(range(max(w0, 16 * b), min(w1, 16 * b + 15) + 1))
+            starts.append(members[0])
+            for w in members:
+                assert [fn(w0, w1, w, 1, i) for i in range(len(members))] == [slot(m) for m in members]
+        for w in (w0, w1, (w0 + w1) // 2):
+            assert [fn(w0, w1, w, 2, i) for i in range(len(starts))] == [slot(m) for m in starts]
 
 
 def test_places():
