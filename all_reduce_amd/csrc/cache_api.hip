@@ -293,29 +293,41 @@ arResult_t arCacheAttentionWorkspace(size_t dim, size_t group, arComm_t comm, si
 
 // For tests, on the host: the pieces of the share of team `team` of workgroup `block`
 // of an attention whose lengths are known, as the kernel walks them (cache_plan.hpp).
-// 2^tokens: of a wave's tile.  Thirteen numbers a piece: rank, sequence, key-value head
+// 2^queries and 2^tokens are a wave's.  Thirteen numbers a piece: rank, sequence, key-value head
 // and tile of query heads, first step, step after the last, steps of the unit, first
 // token, token after the last, slot of partial sums, counter of the group and teams in
 // it, counter of the unit and groups in it.  `teams`: waves of a team, waves that take
 // the same tokens, tiles of query heads, tokens of a pass and of a step.  Returns the
 // number of pieces, of which `most` are written.
 size_t ar_cache_attention_share(const int32_t *lengths, size_t seqs, size_t capacity, size_t window,
-                                uint32_t tokens, uint32_t ranks, uint32_t heads, uint32_t group,
-                                uint32_t grid, uint32_t block, uint32_t team, uint32_t teams[5],
-                                uint32_t (*pieces)[13], size_t most)
+                                uint32_t queries, uint32_t tokens, uint32_t ranks,
+                                uint32_t heads, uint32_t group, uint32_t grid, uint32_t block,
+                                uint32_t team, uint32_t teams[5], uint32_t (*pieces)[13], size_t most)
 {
     uint32_t first, end;
     const uint32_t passes = passes_of_a_step(seqs, ranks, heads, group, tokens,
                                              window != 0 && window < capacity ? window : capacity);
-    uint32_t of_all = 0;
-    for (size_t i = 0; i < seqs; ++i) {
-        attended(lengths[i], capacity, window, &first, &end);
-        of_all += tiles_of(first, end, tokens);
+    CacheTeams t(group, queries, tokens, passes, false);
+    auto sum_up = [&](uint32_t shift, uint32_t of_one) {
+        uint32_t all = 0;
+        for (size_t i = 0; i < seqs; ++i) {
+            attended(lengths[i], capacity, window, &first, &end);
+            all += std::min(steps_of(first, end, shift), of_one);
+        }
+        return all;
+    };
+    const uint32_t per = ranks * heads * t.tiles;
+    bool alone = false;
+    if ((uint32_t)seqs * per > grid) {
+        const uint32_t tiles = sum_up(tokens, 1u << 12);
+        alone = waves_alone(tiles, (uint32_t)seqs);
+        if (alone)
+            t = CacheTeams(group, queries, tokens, passes + passes_alone(tiles, (uint32_t)seqs), true);
+    } else {
+        const uint32_t more = passes_to_try(sum_up(t.shift, ~0u), (uint32_t)seqs, per, grid);
+        if (more != 0 && sum_up(t.shift + more, ~0u) * per <= grid)
+            t.shift += more;
     }
-    CacheTeams t(group, tokens, passes, false);
-    const bool alone = waves_alone((uint32_t)seqs * ranks * heads * t.tiles, grid, of_all, (uint32_t)seqs);
-    if (alone)
-        t = CacheTeams(group, tokens, passes + passes_alone(of_all, (uint32_t)seqs), true);
     const uint32_t across = heads * t.tiles;
     auto steps_at = [&](size_t i) {
         attended(lengths[i], capacity, window, &first, &end);

@@ -43,9 +43,6 @@ constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kLn2 = 0.693147180559945309f;
 constexpr uint32_t kAttendWaves = 4, kAttendThreads = 64 * kAttendWaves;
 
-// Queries a workgroup takes at once.
-constexpr uint32_t kTileQueries = 16;
-
 // A slot of partial sums: [queries][DP] sums, then as many pairs of reference and sum
 // of weights.
 
@@ -106,14 +103,14 @@ __device__ inline uint32_t widen_pair(uint32_t w)
 }
 
 // What a wave holds of a tile.  T: the queries' and outputs' type; EIGHT: the
-// cache is e4m3; DP: dim rounded up to 64, 128 or 256.
+// cache is e4m3; DP: dim rounded up to 64, 128 or 256; QT: tiles of 16 queries.
 //
 // 16-bit caches multiply in their own type.  An e4m3 cache is widened (exactly) to
 // the queries' 16-bit type for the scores, to bfloat16 for a float32's, which is
 // split in three parts of 8 bits, and to bfloat16 for the values, whose scale goes
 // into the weight: float16 might not hold the product.  float32 caches use the
 // binary32 instruction.
-template <typename T, bool EIGHT, int DP>
+template <typename T, bool EIGHT, int DP, int QT>
 struct Tile {
     static constexpr bool kWide = !EIGHT && T::kBytes == 4;
     static constexpr int kBytes = EIGHT ? 1 : T::kBytes;      // of a cached value
@@ -137,21 +134,22 @@ struct Tile {
     static constexpr float kBias = ValueType::kId == Fp16::kId ? 8.0f : 0.0f;
     static constexpr float kRoom = ValueType::kId == Fp16::kId ? 15.0f : 8.0f;
     // Workgroups of a compute unit: registers of a wave.
-    static constexpr int kPerCu = DP == 256 || (kWide && DP == 128) ? 1 : 2;
+    static constexpr int kPerCu = DP == 256 || (DP == 128 && (kWide || QT == 2)) ? 1 : 2;
+    static constexpr uint32_t kQueries = 16 * QT, kQueryShift = QT == 1 ? 4 : 5;
 
     // query: dims of the lane's k index, for the wide instruction one a register
     static constexpr int kQueryRegs = kWide ? DP / 16 : DP / 32;
-    u32x4 q[kQueryParts][kQueryRegs];
+    u32x4 q[QT][kQueryParts][kQueryRegs];
     u32x4 k[kGroups][kKeyLoads];
     uint32_t v[kGroups][4][kVH][kVW];
-    f32x4 o[DP / 16];
+    f32x4 o[QT][DP / 16];
 
     // The first dim of the lane's 16 bytes (8-bit: of either half) of load s.
     static __device__ uint32_t key_dim(int s, uint32_t g) { return (s * 4 + g) * kE; }
     static __device__ uint32_t value_dim(int h, uint32_t n) { return h * 16 * kVE + n * kVE; }
 
     template <bool EXACT>
-    __device__ void load_query(const char *row, bool there, uint32_t g, uint32_t dim)
+    __device__ void load_query(int tile, const char *row, bool there, uint32_t g, uint32_t dim)
     {
 #pragma unroll
         for (int s = 0; s < kQueryRegs; ++s) {
@@ -171,7 +169,7 @@ struct Tile {
                     x[1] = load_piece<false>(row + (uint64_t)d * T::kBytes + 16);
             }
             if constexpr (kQueryParts == 1) {
-                q[0][s] = x[0];
+                q[tile][0][s] = x[0];
             } else {
                 // Cut, not rounded, so that the largest values stay finite: three
                 // parts of 8 bits hold all of a float32.
@@ -182,7 +180,7 @@ struct Tile {
                     for (int t = 0; t < kQueryParts; ++t) {
                         const uint32_t ua = __builtin_bit_cast(uint32_t, a) & 0xffff0000u;
                         const uint32_t ub = __builtin_bit_cast(uint32_t, b) & 0xffff0000u;
-                        q[t][s][i] = ua >> 16 | ub;
+                        q[tile][t][s][i] = ua >> 16 | ub;
                         a = __builtin_isfinite(a) ? a - as_float(ua) : 0.0f;
                         b = __builtin_isfinite(b) ? b - as_float(ub) : 0.0f;
                     }
@@ -223,11 +221,13 @@ struct Tile {
                 }
     }
 
-    __device__ void scores(f32x4 (&s)[kGroups]) const
+    __device__ void scores(f32x4 (&s)[QT][kGroups]) const
     {
 #pragma unroll
-        for (int gr = 0; gr < kGroups; ++gr)
-            s[gr] = f32x4{0, 0, 0, 0};
+        for (int t = 0; t < QT; ++t)
+#pragma unroll
+            for (int gr = 0; gr < kGroups; ++gr)
+                s[t][gr] = f32x4{0, 0, 0, 0};
 #pragma unroll
         for (int l = 0; l < kKeyLoads; ++l)
 #pragma unroll
@@ -235,8 +235,10 @@ struct Tile {
                 if constexpr (kWide) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        s[gr] = __builtin_amdgcn_mfma_f32_16x16x4f32(
-                            as_float(k[gr][l][e]), as_float(q[0][l][e]), s[gr], 0, 0, 0);
+#pragma unroll
+                        for (int t = 0; t < QT; ++t)
+                            s[t][gr] = __builtin_amdgcn_mfma_f32_16x16x4f32(
+                                as_float(k[gr][l][e]), as_float(q[t][0][l][e]), s[t][gr], 0, 0, 0);
                 } else if constexpr (EIGHT) {
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
@@ -248,11 +250,15 @@ struct Tile {
                         }
                         // the small parts first
 #pragma unroll
-                        for (int t = kQueryParts - 1; t >= 0; --t)
-                            s[gr] = multiply<KeyType>(a, q[t][2 * l + half], s[gr]);
+                        for (int part = kQueryParts - 1; part >= 0; --part)
+#pragma unroll
+                            for (int t = 0; t < QT; ++t)
+                                s[t][gr] = multiply<KeyType>(a, q[t][part][2 * l + half], s[t][gr]);
                     }
                 } else {
-                    s[gr] = multiply<KeyType>(k[gr][l], q[0][l], s[gr]);
+#pragma unroll
+                    for (int t = 0; t < QT; ++t)
+                        s[t][gr] = multiply<KeyType>(k[gr][l], q[t][0][l], s[t][gr]);
                 }
             }
     }
@@ -268,7 +274,7 @@ struct Tile {
     }
 
     // o += V^T P^T; `p`: weights (8-bit values: times their scales) of the lane's tokens.
-    __device__ void accumulate(const float (&p)[kGroups][4])
+    __device__ void accumulate(const float (&p)[QT][kGroups][4])
     {
         if constexpr (kWide) {
 #pragma unroll
@@ -279,15 +285,20 @@ struct Tile {
                     for (int h = 0; h < kVH; ++h)
 #pragma unroll
                         for (int j = 0; j < kVE; ++j)
-                            o[h * kVE + j] = __builtin_amdgcn_mfma_f32_16x16x4f32(
-                                as_float(v[gr][i][h][j]), p[gr][i], o[h * kVE + j], 0, 0, 0);
-        } else {
-            float x[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                x[e] = p[e / 4][e % 4];
-            u32x4 w[kWeightParts];
-            split8<ValueType, kWeightParts>(x, w);
+                            for (int t = 0; t < QT; ++t)
+                                o[t][h * kVE + j] = __builtin_amdgcn_mfma_f32_16x16x4f32(
+                                    as_float(v[gr][i][h][j]), p[t][gr][i], o[t][h * kVE + j], 0, 0, 0);
+        } else {
+            u32x4 w[QT][kWeightParts];
+#pragma unroll
+            for (int t = 0; t < QT; ++t) {
+                float x[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    x[e] = p[t][e / 4][e % 4];
+                split8<ValueType, kWeightParts>(x, w[t]);
+            }
 #pragma unroll
             for (int h = 0; h < kVH; ++h)
 #pragma unroll
@@ -306,7 +317,7 @@ struct Tile {
                         }
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
-                            add_parts(o[h * kVE + 4 * c + j], a[j], w);
+                            add_parts(h * kVE + 4 * c + j, a[j], w);
                     } else {
                         u32x4 a[2];
 #pragma unroll
@@ -317,17 +328,19 @@ struct Tile {
                         }
 #pragma unroll
                         for (int j = 0; j < 2; ++j)
-                            add_parts(o[h * kVE + 2 * c + j], a[j], w);
+                            add_parts(h * kVE + 2 * c + j, a[j], w);
                     }
                 }
         }
     }
 
-    static __device__ void add_parts(f32x4 &c, u32x4 a, const u32x4 (&w)[kWeightParts])
+    __device__ void add_parts(int c, u32x4 a, const u32x4 (&w)[QT][kWeightParts])
     {
 #pragma unroll
-        for (int t = kWeightParts - 1; t >= 0; --t)
-            c = multiply<ValueType>(a, w[t], c);
+        for (int part = kWeightParts - 1; part >= 0; --part)
+#pragma unroll
+            for (int t = 0; t < QT; ++t)
+                o[t][c] = multiply<ValueType>(a, w[t][part], o[t][c]);
     }
 
     // The dim of value i of accumulator t.
@@ -348,14 +361,14 @@ __device__ inline void matrix_done()
     __builtin_amdgcn_sched_barrier(0);
 }
 
-template <int N>
-__device__ inline void matrix_done(f32x4 (&c)[N])
+template <int QT, int GROUPS>
+__device__ inline void matrix_done(f32x4 (&c)[QT][GROUPS])
 {
-    if constexpr (N == 1)
-        asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7" : "+v"(c[0]));
-    else
-        asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7" : "+v"(c[0]), "+v"(c[1]));
-    static_assert(N <= 2, "");
+    // (the last of them first; the others are older)
+    asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7" : "+v"(c[QT - 1][GROUPS - 1]));
+#pragma unroll
+    for (int i = 0; i < QT * GROUPS - 1; ++i)
+        asm volatile("" : "+v"(c[i / GROUPS][i % GROUPS]));
 }
 
 // A value that is the same in every lane, in a scalar register.
@@ -422,8 +435,8 @@ template <typename X, int DP>
 struct AttendShared {
     uint64_t rows[kAttendWaves][X::kTokens];      // a tile's rows: byte offsets in a pool
     float scales[kAttendWaves][2][X::kTokens];    // a tile's scales, of keys and of values
-    float sums[kAttendWaves][kTileQueries][DP + 4];
-    float refs[kAttendWaves][kTileQueries], weights[kAttendWaves][kTileQueries];
+    float sums[kAttendWaves][X::kQueries][DP + 4];
+    float refs[kAttendWaves][X::kQueries], weights[kAttendWaves][X::kQueries];
     uint32_t bad[kAttendWaves], last;
     uint32_t found[kAttendWaves][2];
 };
@@ -431,10 +444,10 @@ struct AttendShared {
 // (The code is kept short, with one copy of everything: a call of few tokens runs
 // through it once, from memory.  Loading eight parts of a sum at once, not four, is 1 KB
 // more and took 0.6 us longer where two are joined.)
-template <typename T, bool EIGHT, int DP, bool EXACT, bool EIGHT_OUT>
-__global__ __launch_bounds__(kAttendThreads, (Tile<T, EIGHT, DP>::kPerCu)) void cache_attend(CacheAttentionArgs p)
+template <typename T, bool EIGHT, int DP, int QT, bool EXACT, bool EIGHT_OUT>
+__global__ __launch_bounds__(kAttendThreads, (Tile<T, EIGHT, DP, QT>::kPerCu)) void cache_attend(CacheAttentionArgs p)
 {
-    typedef Tile<T, EIGHT, DP> X;
+    typedef Tile<T, EIGHT, DP, QT> X;
     __shared__ __align__(16) AttendShared<X, DP> lds;
     const uint32_t lane = threadIdx.x & 63u, wave = uniform(threadIdx.x >> 6);
     const uint32_t n = lane & 15u, g = lane >> 4;
@@ -464,13 +477,15 @@ __global__ __launch_bounds__(kAttendThreads, (Tile<T, EIGHT, DP>::kPerCu)) void 
     const uint32_t chunk = (p.seqs + kAttendThreads - 1u) / kAttendThreads;
     const uint32_t from = small ? lane : threadIdx.x * chunk;
     const uint32_t to = small ? lane + 1u : from + chunk;
-    // What `of` says of all sequences' tokens; `before`: of those before the lane's.
-    auto sum_up = [&](auto of, uint32_t &mine, uint32_t &before) {
+    uint32_t mine, before;  // steps of the lane's sequences (of one unit), and of those before
+    // The steps of 2^shift tokens, `most` of a sequence at most, of all sequences.
+    auto sum_up = [&](uint32_t shift, uint32_t most) {
         mine = 0;
         for (uint32_t s = from; s < to && s < p.seqs; ++s) {
             uint32_t first, end;
             attended(small ? lane_length : p.lengths[s], capacity, p.window, &first, &end);
-            mine += of(first, end);
+            const uint32_t steps = steps_of(first, end, shift);
+            mine += steps < most ? steps : most;
         }
         before = scan64(mine);
         uint32_t all = __builtin_amdgcn_readlane(before, 63);
@@ -489,16 +504,30 @@ __global__ __launch_bounds__(kAttendThreads, (Tile<T, EIGHT, DP>::kPerCu)) void 
         }
         return all;
     };
-    CacheTeams teams(group, X::kTokenShift, p.passes, false);
+    CacheTeams teams(group, X::kQueryShift, X::kTokenShift, p.passes, false);
+    const uint32_t per = p.nranks * p.cache.heads * teams.tiles;  // units of a sequence
     bool alone = false;
-    uint32_t mine, before;
-    const uint32_t units = p.seqs * p.nranks * p.cache.heads * teams.tiles;
-    if (units > gridDim.x) {
-        const uint32_t all = sum_up([&](uint32_t first, uint32_t end) { return tiles_of(first, end, X::kTokenShift); },
-                                    mine, before);
-        alone = waves_alone(units, gridDim.x, all, p.seqs);
+    uint32_t all;
+    if (p.seqs * per > gridDim.x) {
+        // (4096 tiles of a sequence say enough of how long it is)
+        all = sum_up(X::kTokenShift, 1u << 12);
+        alone = waves_alone(all, p.seqs);
         if (alone)
-            teams = CacheTeams(group, X::kTokenShift, p.passes + passes_alone(all, p.seqs), true);
+            teams = CacheTeams(group, X::kQueryShift, X::kTokenShift, p.passes + passes_alone(all, p.seqs), true);
+        all = sum_up(teams.shift, ~0u);
+    } else {
+        all = sum_up(teams.shift, ~0u);
+        const uint32_t more = passes_to_try(all, p.seqs, per, gridDim.x);
+        if (more != 0) {
+            const uint32_t mine0 = mine, before0 = before, fewer = sum_up(teams.shift + more, ~0u);
+            if (fewer * per <= gridDim.x) {
+                teams.shift += more;
+                all = fewer;
+            } else {
+                mine = mine0;
+                before = before0;
+            }
+        }
     }
     auto steps_in = [&](uint32_t first, uint32_t end) { return steps_of(first, end, teams.shift); };
     auto steps_at = [&](int32_t length) {
@@ -507,7 +536,7 @@ __global__ __launch_bounds__(kAttendThreads, (Tile<T, EIGHT, DP>::kPerCu)) void 
         return steps_in(first, end);
     };
     const uint32_t across = p.cache.heads * teams.tiles;  // units of a sequence and rank
-    const uint32_t row = sum_up(steps_in, mine, before) * across;  // steps of a rank
+    const uint32_t row = all * across;  // steps of a rank
     mine *= across;
     before *= across;
     // Non-temporal loads where all keys and values together are more than half of the
@@ -555,9 +584,9 @@ __global__ __launch_bounds__(kAttendThreads, (Tile<T, EIGHT, DP>::kPerCu)) void 
     const uint32_t member = alone ? lane : threadIdx.x;      // lane of the team
     const uint32_t beside = alone ? 0u : wave % teams.side;  // the wave's place among those on its tokens
     const uint32_t behind = alone ? 0u : wave / teams.side;
-    const uint32_t most_queries = kTileQueries * teams.side < group ? kTileQueries * teams.side : group;
+    const uint32_t most_queries = X::kQueries * teams.side < group ? X::kQueries * teams.side : group;
     const uint32_t waves_deep = teams.waves / teams.side;
-    const uint32_t mine0 = beside * kTileQueries;            // the wave's queries among the team's
+    const uint32_t mine0 = beside * X::kQueries;            // the wave's queries among the team's
     auto meet = [&] {
         if (alone)
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -565,84 +594,113 @@ __global__ __launch_bounds__(kAttendThreads, (Tile<T, EIGHT, DP>::kPerCu)) void 
             __syncthreads();
     };
 
-    for (;;) {
-        // ---- a piece: steps [step0, step1) of a unit ----------------------------
-        const uint32_t kv = teams.tiles == 1u ? unit : unit / teams.tiles, tile = unit - kv * teams.tiles;
-        uint32_t first, end;
-        const bool fine = attended(length, capacity, p.window, &first, &end);
-        const uint32_t steps = steps_in(first, end);
-        const uint32_t step1 = left < steps - step0 ? step0 + left : steps;
-        const uint32_t t1 = step1 == steps ? end : first + (step1 << teams.shift);
-        const uint32_t query0 = tile * kTileQueries * teams.side;  // of the group
-        const uint32_t queries = group - query0 < most_queries ? group - query0 : most_queries;
-        const uint32_t head0 = kv * group + query0;
+    auto pieces = [&](auto nt) {
+        constexpr bool NT = decltype(nt)::value;
+        for (;;) {
+            // ---- a piece: steps [step0, step1) of a unit ----------------------------
+            const uint32_t kv = teams.tiles == 1u ? unit : unit / teams.tiles, tile = unit - kv * teams.tiles;
+            uint32_t first, end;
+            const bool fine = attended(length, capacity, p.window, &first, &end);
+            const uint32_t steps = steps_in(first, end);
+            const uint32_t step1 = left < steps - step0 ? step0 + left : steps;
+            const uint32_t t1 = step1 == steps ? end : first + (step1 << teams.shift);
+            const uint32_t query0 = tile * X::kQueries * teams.side;  // of the group
+            const uint32_t queries = group - query0 < most_queries ? group - query0 : most_queries;
+            const uint32_t head0 = kv * group + query0;
 
-        X x;
-        x.template load_query<EXACT>(
-            p.q[rank] + (seq * p.q_stride + (uint64_t)(head0 + mine0 + n) * dim) * T::kBytes,
-            mine0 + n < queries, g, dim);
+            X x;
 #pragma unroll
-        for (int t = 0; t < DP / 16; ++t)
-            x.o[t] = f32x4{0, 0, 0, 0};
-        if constexpr (!EXACT)
+            for (int t = 0; t < QT; ++t)
+                x.template load_query<EXACT>(
+                    t, p.q[rank] + (seq * p.q_stride + (uint64_t)(head0 + mine0 + 16 * t + n) * dim) * T::kBytes,
+                    mine0 + 16 * t + n < queries, g, dim);
+            float ref[QT], sum[QT];
+#pragma unroll
+            for (int t = 0; t < QT; ++t) {
+                ref[t] = -__builtin_inff();
+                sum[t] = 0.0f;
+#pragma unroll
+                for (int c = 0; c < DP / 16; ++c)
+                    x.o[t][c] = f32x4{0, 0, 0, 0};
+            }
+            // (where dim is not DP some lanes load none)
 #pragma unroll
             for (int gr = 0; gr < X::kGroups; ++gr)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     x.drop_values(gr, i);
-        float ref = -__builtin_inff(), sum = 0.0f;
-        bool bad = !fine;
+            bool bad = !fine;
 
-        const char *keys = p.keys[rank], *values = p.values[rank];
-        const float *scales = EIGHT ? (lane < 32u ? p.key_scales[rank] : p.value_scales[rank]) : nullptr;
-        const int32_t *table = p.table + seq * p.table_pages;
-        const uint32_t mine_at = lane % X::kTokens;
-        const uint32_t kd = X::key_dim(0, g) * X::kBytes, vd = X::value_dim(0, n) * X::kBytes;
-        uint32_t t0 = first + (step0 << teams.shift) + behind * X::kTokens;
-        const uint32_t tend = mine0 < queries ? t1 : 0u;  // a wave without queries has no tokens
+            const char *keys = p.keys[rank], *values = p.values[rank];
+            const float *scales = EIGHT ? (lane < 32u ? p.key_scales[rank] : p.value_scales[rank]) : nullptr;
+            const int32_t *table = p.table + seq * p.table_pages;
+            const uint32_t mine_at = lane % X::kTokens;
+            const uint32_t kd = X::key_dim(0, g) * X::kBytes, vd = X::value_dim(0, n) * X::kBytes;
+            uint32_t t0 = first + (step0 << teams.shift) + behind * X::kTokens;
+            const uint32_t tend = mine0 < queries ? t1 : 0u;  // a wave without queries has no tokens
 
-        // page and place of the lane's token of the tile at t (past the end: none)
-        auto look = [&](uint32_t t, uint32_t &place) {
-            t += mine_at;
-            int32_t page = -1;
-            place = 0;
-            if (t < t1) {
-                const uint32_t i = p.cache.page_of(t);
-                place = t - i * p.cache.page_tokens;
-                page = table[i];
-            }
-            return page;
-        };
-        const char *krow[X::kGroups], *vrow[X::kGroups][4];
-        float scale_next = 0.0f;
-        // A token without a place stands for the cache's first one.
-        auto rows = [&](uint32_t t, int32_t page, uint32_t place) {
-            if ((uint32_t)page >= p.cache.pages) {
-                bad = bad || t + mine_at < t1;
-                page = 0;
+            // page and place of the lane's token of the tile at t (past the end: none)
+            auto look = [&](uint32_t t, uint32_t &place) {
+                t += mine_at;
+                int32_t page = -1;
                 place = 0;
-            }
-            lds.rows[wave][mine_at] = p.cache.at((uint32_t)page, place, kv) * X::kBytes;
-            if constexpr (EIGHT)
-                scale_next = scales[p.cache.scale_at((uint32_t)page, place, kv)];
-            __builtin_amdgcn_wave_barrier();
+                if (t < t1) {
+                    const uint32_t i = p.cache.page_of(t);
+                    place = t - i * p.cache.page_tokens;
+                    page = table[i];
+                }
+                return page;
+            };
+            float scale_next = 0.0f;
+            // The rows of the tile at t to LDS.  A token without a place stands for the cache's
+            // first one.
+            auto rows = [&](uint32_t t, int32_t page, uint32_t place) {
+                if ((uint32_t)page >= p.cache.pages) {
+                    bad = bad || t + mine_at < t1;
+                    page = 0;
+                    place = 0;
+                }
+                lds.rows[wave][mine_at] = p.cache.at((uint32_t)page, place, kv) * X::kBytes;
+                if constexpr (EIGHT)
+                        scale_next = scales[p.cache.scale_at((uint32_t)page, place, kv)];
+                __builtin_amdgcn_wave_barrier();
+            };
+            // Where the tile's rows are: read from LDS ahead of its loads where there are
+            // registers for that (QT 1: 64 x 8192 tokens x 8 ranks 314 in place of 322 us).
+            const char *krow[X::kGroups], *vrow[X::kGroups][4];
+            auto find_keys = [&] {
 #pragma unroll
-            for (int gr = 0; gr < X::kGroups; ++gr) {
-                krow[gr] = keys + lds.rows[wave][gr * 16 + n] + kd;
+                for (int gr = 0; gr < X::kGroups; ++gr)
+                    krow[gr] = keys + lds.rows[wave][gr * 16 + n] + kd;
+            };
+            auto find_values = [&] {
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    vrow[gr][i] = values + lds.rows[wave][gr * 16 + 4 * g + i] + vd;
-            }
-            __builtin_amdgcn_wave_barrier();
-        };
-        if (t0 < tend) {
-            uint32_t place, place_next;
-            int32_t page = look(t0, place), page_next = look(t0 + teams.pass, place_next);
-            rows(t0, page, place);
-            auto loop = [&](auto nt) {
-                constexpr bool NT = decltype(nt)::value;
+                for (int gr = 0; gr < X::kGroups; ++gr)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        vrow[gr][i] = values + lds.rows[wave][gr * 16 + 4 * g + i] + vd;
+            };
+            auto load_keys = [&] {
+                if constexpr (QT != 1)
+                    find_keys();
                 x.template load_keys<EXACT, NT>(krow, g, dim);
+            };
+            auto load_values = [&] {
+                if constexpr (QT != 1)
+                    find_values();
                 x.template load_values<EXACT, NT>(vrow, n, dim);
+                __builtin_amdgcn_wave_barrier();
+            };
+            if (t0 < tend) {
+                uint32_t place, place_next;
+                int32_t page = look(t0, place), page_next = look(t0 + teams.pass, place_next);
+                rows(t0, page, place);
+                if constexpr (QT == 1) {
+                    find_keys();
+                    find_values();
+                }
+                load_keys();
+                load_values();
                 for (; t0 < t1; t0 += teams.pass) {
                     float ks[X::kGroups][4], vs[X::kGroups][4];
                     if constexpr (EIGHT) {
@@ -658,283 +716,298 @@ __global__ __launch_bounds__(kAttendThreads, (Tile<T, EIGHT, DP>::kPerCu)) void 
                         __builtin_amdgcn_wave_barrier();
                     }
                     rows(t0 + teams.pass, page_next, place_next);
+                    if constexpr (QT == 1) {
+                        find_keys();
+                        find_values();
+                    }
                     page_next = look(t0 + 2 * teams.pass, place_next);
-                    f32x4 s[X::kGroups];
+                    f32x4 s[QT][X::kGroups];
                     x.scores(s);
                     matrix_done(s);
                     // (also behind the last tile, where there is nothing to load: behind a branch the
                     // compiler would wait for the keys where it needs the values)
-                    x.template load_keys<EXACT, NT>(krow, g, dim);
-                    float w[X::kGroups][4], most = -__builtin_inff();
+                    load_keys();
+                    float w[QT][X::kGroups][4];
 #pragma unroll
-                    for (int gr = 0; gr < X::kGroups; ++gr)
+                    for (int t = 0; t < QT; ++t)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            float f = factor;
-                            if constexpr (EIGHT)
-                                f = f * ks[gr][i];
-                            w[gr][i] = s[gr][i] * f;
-                        }
+                        for (int gr = 0; gr < X::kGroups; ++gr)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                float f = factor;
+                                if constexpr (EIGHT)
+                                    f = f * ks[gr][i];
+                                w[t][gr][i] = s[t][gr][i] * f;
+                            }
                     if (t0 + X::kTokens > t1) {
 #pragma unroll
                         for (int gr = 0; gr < X::kGroups; ++gr)
 #pragma unroll
                             for (int i = 0; i < 4; ++i)
                                 if (t0 + gr * 16 + 4 * g + i >= t1) {
-                                    w[gr][i] = -__builtin_inff();
+#pragma unroll
+                                    for (int t = 0; t < QT; ++t)
+                                        w[t][gr][i] = -__builtin_inff();
                                     if constexpr (EIGHT)
                                         vs[gr][i] = 0.0f;
                                     x.drop_values(gr, i);
                                 }
                     }
 #pragma unroll
-                    for (int gr = 0; gr < X::kGroups; ++gr)
+                    for (int t = 0; t < QT; ++t) {
+                        float most = -__builtin_inff();
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            most = w[gr][i] > most ? w[gr][i] : most;
-                    if (__ballot(most > ref + (X::kRoom - X::kBias)) != 0) {
-                        // (a NaN raises nothing; it reaches the sums by its own weight)
-                        most = max_query(most);
-                        const float next = most > ref ? most : ref;
-                        const float shift = next == -__builtin_inff() ? 0.0f : next;
-                        const float keep = __builtin_amdgcn_exp2f(ref - shift);
-                        sum = sum * keep;
+                        for (int gr = 0; gr < X::kGroups; ++gr)
 #pragma unroll
-                        for (int t = 0; t < DP / 16; ++t)
-                            x.o[t] = x.o[t] * keep;
-                        ref = next;
-                    }
-                    const float shift = (ref == -__builtin_inff() ? 0.0f : ref) - X::kBias;
+                            for (int i = 0; i < 4; ++i)
+                                most = w[t][gr][i] > most ? w[t][gr][i] : most;
+                        if (__ballot(most > ref[t] + (X::kRoom - X::kBias)) != 0) {
+                            // (a NaN raises nothing; it reaches the sums by its own weight)
+                            most = max_query(most);
+                            const float next = most > ref[t] ? most : ref[t];
+                            const float shift = next == -__builtin_inff() ? 0.0f : next;
+                            const float keep = __builtin_amdgcn_exp2f(ref[t] - shift);
+                            sum[t] = sum[t] * keep;
 #pragma unroll
-                    for (int gr = 0; gr < X::kGroups; ++gr)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            w[gr][i] = __builtin_amdgcn_exp2f(w[gr][i] - shift);
-                            sum += w[gr][i];
-                            if constexpr (EIGHT)
-                                w[gr][i] = w[gr][i] * vs[gr][i];
+                            for (int c = 0; c < DP / 16; ++c)
+                                x.o[t][c] = x.o[t][c] * keep;
+                            ref[t] = next;
                         }
+                        const float shift = (ref[t] == -__builtin_inff() ? 0.0f : ref[t]) - X::kBias;
+#pragma unroll
+                        for (int gr = 0; gr < X::kGroups; ++gr)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                w[t][gr][i] = __builtin_amdgcn_exp2f(w[t][gr][i] - shift);
+                                sum[t] += w[t][gr][i];
+                                if constexpr (EIGHT)
+                                    w[t][gr][i] = w[t][gr][i] * vs[gr][i];
+                            }
+                    }
                     x.accumulate(w);
-                    x.template load_values<EXACT, NT>(vrow, n, dim);
+                    load_values();
                     matrix_done();
                 }
-            };
-            if (stream)
-                loop(std::true_type{});
-            else
-                loop(std::false_type{});
-        }
+            }
 
-        // ---- the waves' sums to LDS -----------------------------------------------
-        sum = sum_query(sum);
-        if (g == 0) {
-            lds.refs[wave][n] = ref;
-            lds.weights[wave][n] = sum;
-        }
-        const bool any_bad = __ballot(bad) != 0;
-        if (lane == 0)
-            lds.bad[wave] = any_bad;
+            // ---- the waves' sums to LDS -----------------------------------------------
+            const bool any_bad = __ballot(bad) != 0;
+            if (lane == 0)
+                lds.bad[wave] = any_bad;
 #pragma unroll
-        for (int t = 0; t < DP / 16; ++t)
+            for (int t = 0; t < QT; ++t) {
+                sum[t] = sum_query(sum[t]);
+                if (g == 0) {
+                    lds.refs[wave][16 * t + n] = ref[t];
+                    lds.weights[wave][16 * t + n] = sum[t];
+                }
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                lds.sums[wave][n][X::result_dim(t, g, i)] = x.o[t][i];
-        meet();
+                for (int c = 0; c < DP / 16; ++c)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        lds.sums[wave][16 * t + n][X::result_dim(c, g, i)] = x.o[t][c][i];
+            }
+            meet();
 
-        // ---- and together: the waves', then, where several teams share the unit, those of
-        // a group of teams, then those of the groups; by the last team to arrive ---------
-        // A lane of the team takes eight dims of a query, then of another.
-        constexpr uint32_t kPieces = DP / 8;
-        const uint32_t d0 = member % kPieces * 8u;
-        const uint32_t slot_floats = most_queries * (DP + 2u);
-        const bool whole = step0 == 0 && step1 == steps;
-        const CacheJoin join = {whole ? share : plan.owner(here), whole ? share : plan.owner(here + steps - 1u)};
-        uint32_t stage = 0, parts = 0;  // slots of a sum
-        for (;;) {
-            const CacheJoin::Parts from_slots = join.parts(share, stage);
-            const bool done = stage == 0 ? whole : stage == 2 || join.groups() == 1u;
-            for (uint32_t q = member / kPieces; q < queries; q += 64u * teams.waves / kPieces) {
-                float top = -__builtin_inff(), total = 0.0f, y[8] = {};
-                // `count` parts of references r, sums of weights l and sums f
-                auto add = [&](auto parts_at_once, uint32_t count, const float *r, const float *l, const float (*f)[8]) {
-                    constexpr uint32_t N = decltype(parts_at_once)::value;
-                    const float last = top;
+            // ---- and together: the waves', then, where several teams share the unit, those of
+            // a group of teams, then those of the groups; by the last team to arrive ---------
+            // A lane of the team takes eight dims of a query, then of another.
+            constexpr uint32_t kPieces = DP / 8;
+            const uint32_t d0 = member % kPieces * 8u;
+            const uint32_t slot_floats = most_queries * (DP + 2u);
+            const bool whole = step0 == 0 && step1 == steps;
+            const CacheJoin join = {whole ? share : plan.owner(here), whole ? share : plan.owner(here + steps - 1u)};
+            uint32_t stage = 0, parts = 0;  // slots of a sum
+            for (;;) {
+                const CacheJoin::Parts from_slots = join.parts(share, stage);
+                const bool done = stage == 0 ? whole : stage == 2 || join.groups() == 1u;
+                for (uint32_t q = member / kPieces; q < queries; q += 64u * teams.waves / kPieces) {
+                    float top = -__builtin_inff(), total = 0.0f, y[8] = {};
+                    // `count` parts of references r, sums of weights l and sums f
+                    auto add = [&](auto parts_at_once, uint32_t count, const float *r, const float *l, const float (*f)[8]) {
+                        constexpr uint32_t N = decltype(parts_at_once)::value;
+                        const float last = top;
 #pragma unroll
-                    for (uint32_t j = 0; j < N; ++j)
-                        top = r[j] > top ? r[j] : top;
-                    const float shift = top == -__builtin_inff() ? 0.0f : top;
-                    const float a = __builtin_amdgcn_exp2f(last - shift);
-                    total = total * a;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        y[e] = y[e] * a;
-#pragma unroll
-                    for (uint32_t j = 0; j < N; ++j)
-                        if (j < count) {
-                            const float b = __builtin_amdgcn_exp2f(r[j] - shift);
-                            total += l[j] * b;
-#pragma unroll
-                            for (int e = 0; e < 8; ++e)
-                                y[e] += f[j][e] * b;
-                        }
-                };
-                // All loads are under way at once; past the last part the last again, left out.
-                if (stage == 0) {
-                    float r[kAttendWaves], l[kAttendWaves], f[kAttendWaves][8];
-#pragma unroll
-                    for (uint32_t j = 0; j < kAttendWaves; ++j) {
-                        const uint32_t w = wave0 + q / kTileQueries + (j < waves_deep ? j : waves_deep - 1u) * teams.side;
-                        const uint32_t k = q % kTileQueries;
-                        r[j] = lds.refs[w][k];
-                        l[j] = lds.bad[w] != 0 ? __builtin_nanf("") : lds.weights[w][k];
+                        for (uint32_t j = 0; j < N; ++j)
+                            top = r[j] > top ? r[j] : top;
+                        const float shift = top == -__builtin_inff() ? 0.0f : top;
+                        const float a = __builtin_amdgcn_exp2f(last - shift);
+                        total = total * a;
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
-                            f[j][e] = lds.sums[w][k][d0 + e];
-                    }
-                    add(std::integral_constant<uint32_t, kAttendWaves>{}, waves_deep, r, l, f);
-                } else {
-                    for (uint32_t i = 0; i < parts; i += kJoinLoads) {
-                        float r[kJoinLoads], l[kJoinLoads], f[kJoinLoads][8];
+                            y[e] = y[e] * a;
 #pragma unroll
-                        for (uint32_t j = 0; j < kJoinLoads; ++j) {
-                            const uint32_t at = i + j < parts ? i + j : parts - 1u;
-                            const uint32_t part = at == 0 ? from_slots.first : from_slots.next + (at - 1u) * from_slots.by;
-                            const float *slot = p.slots + (uint64_t)part * slot_floats;
-                            const f32x2 s = shared_pair(slot + most_queries * DP + 2 * q);
-                            r[j] = s[0];
-                            l[j] = s[1];
+                        for (uint32_t j = 0; j < N; ++j)
+                            if (j < count) {
+                                const float b = __builtin_amdgcn_exp2f(r[j] - shift);
+                                total += l[j] * b;
 #pragma unroll
-                            for (int e = 0; e < 8; e += 2) {
-                                const f32x2 v = shared_pair(slot + q * DP + d0 + e);
-                                f[j][e] = v[0];
-                                f[j][e + 1] = v[1];
+                                for (int e = 0; e < 8; ++e)
+                                    y[e] += f[j][e] * b;
                             }
+                    };
+                    // All loads are under way at once; past the last part the last again, left out.
+                    if (stage == 0) {
+                        float r[kAttendWaves], l[kAttendWaves], f[kAttendWaves][8];
+#pragma unroll
+                        for (uint32_t j = 0; j < kAttendWaves; ++j) {
+                            const uint32_t w = wave0 + q / X::kQueries + (j < waves_deep ? j : waves_deep - 1u) * teams.side;
+                            const uint32_t k = q % X::kQueries;
+                            r[j] = lds.refs[w][k];
+                            l[j] = lds.bad[w] != 0 ? __builtin_nanf("") : lds.weights[w][k];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                f[j][e] = lds.sums[w][k][d0 + e];
                         }
-                        add(std::integral_constant<uint32_t, kJoinLoads>{}, parts - i, r, l, f);
+                        add(std::integral_constant<uint32_t, kAttendWaves>{}, waves_deep, r, l, f);
+                    } else {
+                        for (uint32_t i = 0; i < parts; i += kJoinLoads) {
+                            float r[kJoinLoads], l[kJoinLoads], f[kJoinLoads][8];
+#pragma unroll
+                            for (uint32_t j = 0; j < kJoinLoads; ++j) {
+                                const uint32_t at = i + j < parts ? i + j : parts - 1u;
+                                const uint32_t part = at == 0 ? from_slots.first : from_slots.next + (at - 1u) * from_slots.by;
+                                const float *slot = p.slots + (uint64_t)part * slot_floats;
+                                const f32x2 s = shared_pair(slot + most_queries * DP + 2 * q);
+                                r[j] = s[0];
+                                l[j] = s[1];
+#pragma unroll
+                                for (int e = 0; e < 8; e += 2) {
+                                    const f32x2 v = shared_pair(slot + q * DP + d0 + e);
+                                    f[j][e] = v[0];
+                                    f[j][e + 1] = v[1];
+                                }
+                            }
+                            add(std::integral_constant<uint32_t, kJoinLoads>{}, parts - i, r, l, f);
+                        }
+                    }
+                    if (!done) {
+                        // (a group's sums: in the place of its first, which this wave alone has read)
+                        float *slot = p.slots + (uint64_t)join.slot(stage == 0 ? share : join.first(share)) * slot_floats;
+#pragma unroll
+                        for (int e = 0; e < 8; e += 2)
+                            share_pair(slot + q * DP + d0 + e, y[e], y[e + 1]);
+                        if (d0 == 0)
+                            share_pair(slot + most_queries * DP + 2 * q, top, total);
+                        continue;
+                    }
+                    const bool empty = length == 0;
+                    const uint64_t out_row = (uint64_t)seq * p.heads + head0 + q;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        y[e] = empty ? 0.0f : y[e] / total;
+                    if (p.has_lse != 0 && d0 == 0)
+                        p.lse[rank][out_row] = empty ? -__builtin_inff()
+                                                     : ((top == -__builtin_inff() ? 0.0f : top) - X::kBias) * kLn2 +
+                                                           __builtin_logf(total);
+                    if constexpr (EIGHT_OUT) {
+                        // 16 neighbouring lanes hold the 128 columns of a scale
+                        const float s = scale_of(max16(max_bits(y)));
+                        store_eights<false>(p.out[rank] + out_row * dim + d0, to_eights(y, s));
+                        if (d0 % AR_SCALE_BLOCK == 0)
+                            p.out_scales[rank][((uint64_t)(head0 + q) * dim + d0) / AR_SCALE_BLOCK * p.seqs + seq] = s;
+                    } else if (EXACT || d0 < dim) {
+                        char *at = p.out[rank] + (out_row * dim + d0) * T::kBytes;
+                        constexpr int E = kPiece<T>;
+#pragma unroll
+                        for (int i = 0; i < 8 / E; ++i) {
+                            float f[E];
+#pragma unroll
+                            for (int e = 0; e < E; ++e)
+                                f[e] = y[i * E + e];
+                            store_piece<false>(at + i * 16, narrow_piece<T>(f));
+                        }
                     }
                 }
-                if (!done) {
-                    // (a group's sums: in the place of its first, which this wave alone has read)
-                    float *slot = p.slots + (uint64_t)join.slot(stage == 0 ? share : join.first(share)) * slot_floats;
-#pragma unroll
-                    for (int e = 0; e < 8; e += 2)
-                        share_pair(slot + q * DP + d0 + e, y[e], y[e + 1]);
-                    if (d0 == 0)
-                        share_pair(slot + most_queries * DP + 2 * q, top, total);
-                    continue;
+                if (done)
+                    break;
+                // Whether this team is the last to come here.
+                const uint32_t counter = stage == 0 ? join.group_counter(share) : join.unit_counter();
+                const uint32_t count = stage == 0 ? join.last(share) - join.first(share) + 1u : join.groups();
+                shared_stores_done();
+                meet();
+                uint32_t last = 0;
+                if (member == 0) {
+                    const uint32_t old = __hip_atomic_fetch_add(counters + counter, 1u, __ATOMIC_RELAXED,
+                                                                __HIP_MEMORY_SCOPE_AGENT);
+                    last = old + 1u == count;
+                    if (last != 0)
+                        __hip_atomic_store(counters + counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                    lds.last = last;
                 }
-                const bool empty = length == 0;
-                const uint64_t out_row = (uint64_t)seq * p.heads + head0 + q;
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    y[e] = empty ? 0.0f : y[e] / total;
-                if (p.has_lse != 0 && d0 == 0)
-                    p.lse[rank][out_row] = empty ? -__builtin_inff()
-                                                 : ((top == -__builtin_inff() ? 0.0f : top) - X::kBias) * kLn2 +
-                                                       __builtin_logf(total);
-                if constexpr (EIGHT_OUT) {
-                    // 16 neighbouring lanes hold the 128 columns of a scale
-                    const float s = scale_of(max16(max_bits(y)));
-                    store_eights<false>(p.out[rank] + out_row * dim + d0, to_eights(y, s));
-                    if (d0 % AR_SCALE_BLOCK == 0)
-                        p.out_scales[rank][((uint64_t)(head0 + q) * dim + d0) / AR_SCALE_BLOCK * p.seqs + seq] = s;
-                } else if (EXACT || d0 < dim) {
-                    char *at = p.out[rank] + (out_row * dim + d0) * T::kBytes;
-                    constexpr int E = kPiece<T>;
-#pragma unroll
-                    for (int i = 0; i < 8 / E; ++i) {
-                        float f[E];
-#pragma unroll
-                        for (int e = 0; e < E; ++e)
-                            f[e] = y[i * E + e];
-                        store_piece<false>(at + i * 16, narrow_piece<T>(f));
-                    }
-                }
+                meet();
+                if ((alone ? uniform(last) : uniform(lds.last)) == 0)
+                    break;
+                ++stage;
+                parts = count;
             }
-            if (done)
-                break;
-            // Whether this team is the last to come here.
-            const uint32_t counter = stage == 0 ? join.group_counter(share) : join.unit_counter();
-            const uint32_t count = stage == 0 ? join.last(share) - join.first(share) + 1u : join.groups();
-            shared_stores_done();
-            meet();
-            uint32_t last = 0;
-            if (member == 0) {
-                const uint32_t old = __hip_atomic_fetch_add(counters + counter, 1u, __ATOMIC_RELAXED,
-                                                            __HIP_MEMORY_SCOPE_AGENT);
-                last = old + 1u == count;
-                if (last != 0)
-                    __hip_atomic_store(counters + counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-                lds.last = last;
-            }
-            meet();
-            if ((alone ? uniform(last) : uniform(lds.last)) == 0)
-                break;
-            ++stage;
-            parts = count;
-        }
 
-        left -= step1 - step0;
-        if (left == 0)
-            return;
-        here += steps;
-        step0 = 0;
-        if (++unit == across) {
-            unit = 0;
-            if (++seq == p.seqs) {
-                seq = 0;
-                ++rank;
+            left -= step1 - step0;
+            if (left == 0)
+                return;
+            here += steps;
+            step0 = 0;
+            if (++unit == across) {
+                unit = 0;
+                if (++seq == p.seqs) {
+                    seq = 0;
+                    ++rank;
+                }
+                length = length_of(seq);
             }
-            length = length_of(seq);
+            meet();  // the sums in LDS are read before the next piece's are written
         }
-        meet();  // the sums in LDS are read before the next piece's are written
-    }
+    };
+    if (stream)
+        pieces(std::true_type{});
+    else
+        pieces(std::false_type{});
 }
 
 // Workgroups of a launch at most: what fits the compute units at once.
 inline uint32_t attend_most(int per_cu, int cu_count) { return (uint32_t)(per_cu * cu_count) / 8u * 8u; }
 
-template <typename T, bool EIGHT, int DP, bool EXACT, bool EIGHT_OUT>
+template <typename T, bool EIGHT, int DP, int QT, bool EXACT, bool EIGHT_OUT>
 hipError_t enqueue_attend(CacheAttentionArgs args, int cu_count, hipStream_t stream)
 {
-    typedef Tile<T, EIGHT, DP> X;
+    typedef Tile<T, EIGHT, DP, QT> X;
     const uint64_t capacity = args.table_pages * args.cache.page_tokens;
     const uint64_t tokens = args.window != 0 && args.window < capacity ? args.window : capacity;
     args.passes = passes_of_a_step(args.seqs, args.nranks, args.cache.heads, args.group, X::kTokenShift, tokens);
     // (a call of few steps has fewer workgroups)
-    const CacheTeams teams(args.group, X::kTokenShift, args.passes, false);
+    const CacheTeams teams(args.group, X::kQueryShift, X::kTokenShift, args.passes, false);
     const uint64_t units = (uint64_t)args.nranks * args.cache.heads * args.seqs * teams.tiles;
     const uint64_t steps = ((tokens - 1u) >> teams.shift) + 1u;
     uint64_t grid = attend_most(X::kPerCu, cu_count);
     if (steps < grid && units * steps < grid)
         grid = (units * steps + 7u) / 8u * 8u;
-    hipLaunchKernelGGL((cache_attend<T, EIGHT, DP, EXACT, EIGHT_OUT>), dim3((uint32_t)grid),
+    hipLaunchKernelGGL((cache_attend<T, EIGHT, DP, QT, EXACT, EIGHT_OUT>), dim3((uint32_t)grid),
                        dim3(kAttendThreads), 0, stream, args);
     return hipGetLastError();
 }
 
-template <typename T, bool EIGHT, int DP>
-hipError_t pick_attend(const CacheAttentionArgs &args, bool eight_out, int cu_count, hipStream_t stream)
-{
-    if (args.cache.dim != DP)
-        return enqueue_attend<T, EIGHT, DP, false, false>(args, cu_count, stream);
-    if constexpr (DP % AR_SCALE_BLOCK == 0)
-        if (eight_out)
-            return enqueue_attend<T, EIGHT, DP, true, true>(args, cu_count, stream);
-    return enqueue_attend<T, EIGHT, DP, true, false>(args, cu_count, stream);
-}
-
-// One of the six kernel families, each compiled in a file of its own.
-template <typename T, bool EIGHT>
+// One of the kernel families, each compiled in a file of its own.
+template <typename T, bool EIGHT, int QT>
 hipError_t launch_attend(const CacheAttentionArgs &args, bool eight_out, int cu_count,
                          hipStream_t stream)
 #ifdef AR_ATTEND_FAMILY
 {
+    auto pick = [&](auto padded) {
+        constexpr int DP = decltype(padded)::value;
+        if (args.cache.dim != DP)
+            return enqueue_attend<T, EIGHT, DP, QT, false, false>(args, cu_count, stream);
+        if constexpr (DP % AR_SCALE_BLOCK == 0)
+            if (eight_out)
+                return enqueue_attend<T, EIGHT, DP, QT, true, true>(args, cu_count, stream);
+        return enqueue_attend<T, EIGHT, DP, QT, true, false>(args, cu_count, stream);
+    };
     switch (padded_dim(args.cache.dim)) {
-    case 64: return pick_attend<T, EIGHT, 64>(args, eight_out, cu_count, stream);
-    case 128: return pick_attend<T, EIGHT, 128>(args, eight_out, cu_count, stream);
-    default: return pick_attend<T, EIGHT, 256>(args, eight_out, cu_count, stream);
+    case 64: return pick(std::integral_constant<int, 64>{});
+    case 128: return pick(std::integral_constant<int, 128>{});
     }
+    if constexpr (QT == 1 || T::kBytes == 2)
+        return pick(std::integral_constant<int, 256>{});
+    return hipErrorInvalidValue;
 }
 #else
     ;

@@ -1,10 +1,11 @@
-// cache_attention_fp32.hip -- the cached attention's kernels for float32 queries and a cache
-// of their type (cache_attention.hpp).
+// cache_attention_fp32.hip -- the cached attention's kernels for float32 queries, a cache
+// of their type and up to 16 query heads to a key-value head
+// (cache_attention.hpp).
 #define AR_ATTEND_FAMILY
 #include "cache_attention.hpp"
 
 namespace ar {
 
-template hipError_t launch_attend<Fp32, false>(const CacheAttentionArgs &, bool, int, hipStream_t);
+template hipError_t launch_attend<Fp32, false, 1>(const CacheAttentionArgs &, bool, int, hipStream_t);
 
 }  // namespace ar

@@ -3,8 +3,7 @@
 //
 // The host does not know the lengths (they change between replays of a graph),
 // so the grid is fixed and each team of waves finds its own share.  A unit is the
-// attention of up to 16 query heads (64 where a team's waves share the tokens' keys
-// and values) of one key-value head of one rank over one sequence; its work comes in
+// attention of up to 16 query heads (32 or more where there are more: CacheTeams) of one key-value head of one rank over one sequence; its work comes in
 // steps of `step` tokens, at least one, so that an empty sequence is visited too.
 // All units' steps stand in one row, by rank, then sequence, then key-value head and
 // tile of query heads (heads that lie side by side in memory are read side by side),
@@ -75,25 +74,24 @@ struct CachePlan {
     }
 };
 
-// How a launch's waves make teams.  Four waves of a workgroup share a unit's tokens;
-// with more than 16 query heads to a key-value head, two or all four of them take
-// the same tokens and 16 heads each, so that keys and values come from memory once
-// for 64.  Where there are more units than workgroups, and short ones, each wave is a
-// team, and its
-// steps are longer: a team's way into and out of a unit is a chain of loads that four
-// waves do not shorten.  On MI355X 2048 units of 33 tokens take 16 us that way and 25 with
-// four waves, of 133 tokens 37 and 44; of 333 tokens 110 and 79, so long sequences have
-// four.
+// How a launch's waves make teams.  A wave takes 16 query heads of a key-value head, or
+// 32 where there are more.  Four waves of a workgroup share a unit's tokens; with more
+// than 32 query heads, two or all four of them take the same tokens and 32 heads each.
+// Where there are more units than workgroups, and short ones, each wave is a team, with
+// longer steps: a team's way into and out of a unit is a chain of loads that four waves
+// do not shorten.  On MI355X 2048 units of 33 tokens take 16 us that way and 25 with four
+// waves, of 133 tokens 37 and 44; of 333 tokens 110 and 79.
 struct CacheTeams {
     uint32_t waves;  // of a team
     uint32_t side;   // waves that take the same tokens
-    uint32_t tiles;  // of 16 * side query heads: units of a sequence and key-value head
+    uint32_t tiles;  // of a team's query heads: units of a sequence and key-value head
     uint32_t pass;   // tokens that the team takes at once
     uint32_t shift;  // 2^shift tokens are a step
-    // `tokens`: 2^tokens are a wave's tile; 2^passes of a step.
-    __host__ __device__ CacheTeams(uint32_t group, uint32_t tokens, uint32_t passes, bool alone)
+    // 2^queries and 2^tokens are a wave's; 2^passes a step's.
+    __host__ __device__ CacheTeams(uint32_t group, uint32_t queries, uint32_t tokens, uint32_t passes,
+                                   bool alone)
     {
-        const uint32_t t = (group + 15u) / 16u;
+        const uint32_t t = (group + (1u << queries) - 1u) >> queries;
         const uint32_t beside = alone || t == 1u ? 0u : t == 2u ? 1u : 2u, behind = alone ? 0u : 2u - beside;
         waves = alone ? 1u : 4u;
         side = 1u << beside;
@@ -103,12 +101,12 @@ struct CacheTeams {
     }
 };
 
-// Whether each wave is to be a team, for units of a batch whose sequences have `tiles`
-// tiles of tokens together; and the passes of its step, for most sequences a power of
-// two that takes all of them.
-__host__ __device__ inline bool waves_alone(uint32_t units, uint32_t grid, uint32_t tiles, uint32_t seqs)
+// Whether each wave is to be a team, for a batch whose sequences have `tiles` tiles of
+// tokens together; and the passes of its step, a power of two that takes most sequences
+// whole.
+__host__ __device__ inline bool waves_alone(uint32_t tiles, uint32_t seqs)
 {
-    return units > grid && tiles <= 8u * seqs;
+    return tiles <= 8u * seqs;
 }
 
 __host__ __device__ inline uint32_t passes_alone(uint32_t tiles, uint32_t seqs)
@@ -116,11 +114,21 @@ __host__ __device__ inline uint32_t passes_alone(uint32_t tiles, uint32_t seqs)
     return tiles <= seqs ? 2u : tiles <= 2u * seqs ? 3u : tiles <= 4u * seqs ? 4u : 5u;
 }
 
-// A sequence's part of `tiles` (no more than counts).
-__host__ __device__ inline uint32_t tiles_of(uint32_t first, uint32_t end, uint32_t tokens)
+// How long a step of teams of four is: one pass where a team's share is many, else 2, 4
+// or 8, where that leaves no more steps than teams: splitting a unit costs a joining of
+// its parts (4 us on MI355X; a pass takes 1.2).  64 units of 200 tokens take 9.3 us whole
+// and 10.3 in two parts, 435 of 333 tokens on the average 17.7 and 22.0.  Few units that
+// are longer gain by more teams: 8 of 1000 tokens take 10.7 us in eight parts, 11.2 in four
+// and 12.6 in two.
+//
+// This is the exponent to try for `seqs` sequences of `per` units and `steps` steps of
+// one pass each; it is taken if there are no more steps than teams then.
+__host__ __device__ inline uint32_t passes_to_try(uint32_t steps, uint32_t seqs, uint32_t per, uint32_t teams)
 {
-    const uint32_t n = steps_of(first, end, tokens);
-    return n < 1u << 12 ? n : 1u << 12;
+    const uint32_t all = steps * per;
+    if (steps == seqs || (all <= teams && steps > 4u * seqs) || all > 8u * teams)
+        return 0;
+    return all > 4u * teams ? 3u : all > 2u * teams ? 2u : 1u;
 }
 
 // The smallest power of two of passes to a step (as its exponent) with which all steps

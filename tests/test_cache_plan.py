@@ -11,33 +11,34 @@ import all_reduce_amd as ar
 SZ, U32, I32, I64 = ctypes.c_size_t, ctypes.c_uint32, ctypes.c_int32, ctypes.c_int64
 
 
-def pieces_of(lengths, capacity, window, tokens, ranks, heads, group, grid, block, team):
+def pieces_of(lengths, capacity, window, queries, tokens, ranks, heads, group, grid, block, team):
     lib = ar.library()
     fn = lib.ar_cache_attention_share
     fn.restype = SZ
-    fn.argtypes = [ctypes.POINTER(I32), SZ, SZ, SZ, U32, U32, U32, U32, U32, U32, U32, ctypes.POINTER(U32), ctypes.c_void_p,
+    fn.argtypes = [ctypes.POINTER(I32), SZ, SZ, SZ, U32, U32, U32, U32, U32, U32, U32, U32, ctypes.POINTER(U32), ctypes.c_void_p,
                    SZ]
     teams = (U32 * 5)()
     most = 1 << 12
     out = np.zeros((most, 13), dtype=np.uint32)
-    n = fn(lengths, len(lengths), capacity, window, tokens, ranks, heads, group, grid, block, team, teams,
+    n = fn(lengths, len(lengths), capacity, window, queries, tokens, ranks, heads, group, grid, block, team, teams,
            out.ctypes.data, most)
     assert n <= most
     return list(teams), out[:n].astype(np.int64).tolist()
 
 
-def check_plan(lengths, capacity, window, tokens, ranks, heads, group, grid):
+def check_plan(lengths, capacity, window, tokens, ranks, heads, group, grid, queries):
     """Every token of every unit is in one piece; a unit's pieces meet in slots and
     counters of their own, in the numbers that the teams wait for; equal shares."""
     covered, partial, sizes, slots = {}, {}, [], set()
     array = (I32 * len(lengths))(*lengths)
-    (waves, side, tiles, a_pass, step), _ = pieces_of(array, capacity, window, tokens, ranks, heads, group, grid, 0, 0)
+    (waves, side, tiles, a_pass, step), _ = pieces_of(array, capacity, window, queries, tokens, ranks, heads, group, grid, 0, 0)
     assert waves in (1, 4) and side <= waves and a_pass == waves // side << tokens and step >= a_pass and step % a_pass == 0
-    assert (tiles - 1) * side * 16 < group <= tiles * side * 16
+    wide = 1 << queries
+    assert (tiles - 1) * side * wide < group <= tiles * side * wide
     teams = grid * 4 // waves
     for block in range(grid):
         for team in range(4 // waves):
-            _, pieces = pieces_of(array, capacity, window, tokens, ranks, heads, group, grid, block, team)
+            _, pieces = pieces_of(array, capacity, window, queries, tokens, ranks, heads, group, grid, block, team)
             sizes.append(sum(p[4] - p[3] for p in pieces))
             for rank, seq, unit, s0, s1, steps, t0, t1, slot, gc, gn, uc, groups in pieces:
                 assert 0 <= rank < ranks and 0 <= seq < len(lengths) and 0 <= unit < tiles * heads and 0 <= s0 < s1 <= steps
@@ -95,7 +96,8 @@ PLANS = [
 @pytest.mark.parametrize("lengths,capacity,window,tokens,ranks,heads,group,grid", PLANS,
                          ids=[str(i) for i in range(len(PLANS))])
 def test_shares(lengths, capacity, window, tokens, ranks, heads, group, grid):
-    check_plan(lengths, capacity, window, tokens, ranks, heads, group, grid)
+    for queries in (4, 5):
+        check_plan(lengths, capacity, window, tokens, ranks, heads, group, grid, queries)
 
 
 def test_drawn_shares():
@@ -108,7 +110,7 @@ def test_drawn_shares():
         lengths[rng.randrange(seqs)] = longest
         seen.add(check_plan(lengths, 32768, rng.choice([0, 0, 1, 100, 5000]), rng.choice([4, 5]),
                             rng.choice([1, 2, 8]), rng.choice([1, 1, 3]), rng.choice([1, 8, 16, 17, 40, 100]),
-                            rng.choice([8, 16, 64, 256])))
+                            rng.choice([8, 16, 64, 256]), rng.choice([4, 5])))
     assert seen == {(1, 1), (4, 1), (4, 2), (4, 4)}
 
 
