@@ -2,12 +2,13 @@
 the operators around it in a tensor-parallel layer, its key-value cache among them.
 
 The functions named ``ar*`` are the C ABI of ``include/ar_allreduce.h``,
-``include/ar_block.h`` and ``include/ar_cache.h``, one for one, over ctypes: arguments are marshalled and
-the result code is returned, nothing else happens here.  :class:`Comm` and :func:`rank_buffers`
-are conveniences on top for torch tensors; torch supplies device memory and
-streams only.  Every step of the all-reduce runs in the HIP kernels of
-``libar_allreduce.so``; there is no other implementation to fall back to, so a
-missing library raises instead of running anything.
+``include/ar_block.h`` and ``include/ar_cache.h``, one for one, over ctypes:
+arguments are marshalled and the result code is returned, nothing else happens
+here.  :class:`Comm` and :func:`rank_buffers` are conveniences on top for torch
+tensors; torch supplies device memory and streams only.  Every step of the
+all-reduce runs in the HIP kernels of ``libar_allreduce.so``; there is no other
+implementation to fall back to, so a missing library raises instead of running
+anything.
 """
 from __future__ import annotations
 
@@ -677,6 +678,8 @@ class Comm:
         layout = self._pages(key_pages, value_pages, key_scales, value_scales, n, dtype)
         if layout.dim != dim:
             raise ValueError(f"queries of {dim}, cache of {layout.dim}")
+        if window < 0:
+            raise ValueError(f"window must not be negative, got {window}")
         stride = self._strided("queries", queries, n, (seqs, heads, dim), dtype)
         self._check("out", out, n, (seqs, heads, dim), dtype if out_scales is None else torch.float8_e4m3fn)
         if out_scales is not None:

@@ -153,8 +153,8 @@ arResult_t copy(const Copy &c, bool write, size_t row_stride, const int64_t *slo
     args.slots = slots;
     args.row_stride = row_stride;
     args.tokens = (uint32_t)tokens;
-    return launched(write ? launch_cache_write(args, dtype, eight, nranks, comm->cu_count, (hipStream_t)stream)
-                          : launch_cache_read(args, dtype, eight, nranks, comm->cu_count, (hipStream_t)stream));
+    auto launch = write ? launch_cache_write : launch_cache_read;
+    return launched(launch(args, dtype, eight, nranks, comm->cu_count, (hipStream_t)stream));
 }
 
 }  // namespace
@@ -209,14 +209,14 @@ arResult_t arCacheAttention(const void *const *queries, size_t queryStride,
         return reject(arUnsupported, "heads must be a multiple of the cache's, at most 4096");
     if (eight_out && cache->dim % AR_SCALE_BLOCK != 0)
         return reject(arUnsupported, "8-bit outputs need heads of 128 or 256");
-    if (!isfinite(scale))
-        return reject(arInvalidArgument, "scale must be finite");
+    if (!(fabsf(scale) <= 0x1p126f))  // (the kernel takes it times log2 e)
+        return reject(arInvalidArgument, "scale must be at most 2^126 in magnitude");
     if (seqs == 0)
         return arSuccess;
     if (seqs > kMostSeqs)
         return reject(arUnsupported, "seqs must be at most 65536");
-    if (seqs * heads * (size_t)nranks > (size_t)1 << 30)
-        return reject(arUnsupported, "seqs * heads * nranks must be at most 2^30");
+    if (seqs * heads * (size_t)nranks > (size_t)1 << 24)
+        return reject(arUnsupported, "seqs * heads * nranks must be at most 2^24");
     if (tablePages < 1 || tablePages > INT32_MAX)
         return reject(arInvalidArgument, "tablePages must be in 1..2^31 - 1");
     const size_t row = heads * cache->dim;
@@ -293,10 +293,10 @@ arResult_t arCacheAttentionWorkspace(size_t dim, size_t group, arComm_t comm, si
 
 // For tests, on the host: the pieces of the share of team `team` of workgroup `block`
 // of an attention whose lengths are known, as the kernel walks them (cache_plan.hpp).
-// 2^queries and 2^tokens are a wave's.  Thirteen numbers a piece: rank, sequence, key-value head
-// and tile of query heads, first step, step after the last, steps of the unit, first
-// token, token after the last, slot of partial sums, counter of the group and teams in
-// it, counter of the unit and groups in it.  `teams`: waves of a team, waves that take
+// 2^queries and 2^tokens are a wave's.  Thirteen numbers a piece: rank, sequence,
+// key-value head and tile of query heads, first step, step after the last, steps of the
+// unit, first token, token after the last, slot of partial sums, counter of the group and
+// teams in it, counter of the unit and groups in it.  `teams`: waves of a team, waves that take
 // the same tokens, tiles of query heads, tokens of a pass and of a step.  Returns the
 // number of pieces, of which `most` are written.
 size_t ar_cache_attention_share(const int32_t *lengths, size_t seqs, size_t capacity, size_t window,
@@ -306,7 +306,7 @@ size_t ar_cache_attention_share(const int32_t *lengths, size_t seqs, size_t capa
 {
     uint32_t first, end;
     const uint32_t passes = passes_of_a_step(seqs, ranks, heads, group, tokens,
-                                             window != 0 && window < capacity ? window : capacity);
+                                             most_attended(capacity, window));
     CacheTeams t(group, queries, tokens, passes, false);
     auto sum_up = [&](uint32_t shift, uint32_t of_one) {
         uint32_t all = 0;

@@ -398,12 +398,14 @@ __device__ inline float max_query(float x)
 __device__ inline void share_pair(float *to, float a, float b)
 {
     const f32x2 v = {a, b};
-    __hip_atomic_store((uint64_t *)to, __builtin_bit_cast(uint64_t, v), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __hip_atomic_store((uint64_t *)to, __builtin_bit_cast(uint64_t, v), __ATOMIC_RELAXED,
+                       __HIP_MEMORY_SCOPE_AGENT);
 }
 
 __device__ inline f32x2 shared_pair(const float *from)
 {
-    return __builtin_bit_cast(f32x2, __hip_atomic_load((const uint64_t *)from, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+    const uint64_t v = __hip_atomic_load((const uint64_t *)from, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    return __builtin_bit_cast(f32x2, v);
 }
 
 __device__ inline void shared_stores_done()
@@ -445,7 +447,8 @@ struct AttendShared {
 // through it once, from memory.  Loading eight parts of a sum at once, not four, is 1 KB
 // more and took 0.6 us longer where two are joined.)
 template <typename T, bool EIGHT, int DP, int QT, bool EXACT, bool EIGHT_OUT>
-__global__ __launch_bounds__(kAttendThreads, (Tile<T, EIGHT, DP, QT>::kPerCu)) void cache_attend(CacheAttentionArgs p)
+__global__ __launch_bounds__(kAttendThreads, (Tile<T, EIGHT, DP, QT>::kPerCu))
+void cache_attend(CacheAttentionArgs p)
 {
     typedef Tile<T, EIGHT, DP, QT> X;
     __shared__ __align__(16) AttendShared<X, DP> lds;
@@ -513,7 +516,8 @@ __global__ __launch_bounds__(kAttendThreads, (Tile<T, EIGHT, DP, QT>::kPerCu)) v
         all = sum_up(X::kTokenShift, 1u << 12);
         alone = waves_alone(all, p.seqs);
         if (alone)
-            teams = CacheTeams(group, X::kQueryShift, X::kTokenShift, p.passes + passes_alone(all, p.seqs), true);
+            teams = CacheTeams(group, X::kQueryShift, X::kTokenShift,
+                               p.passes + passes_alone(all, p.seqs), true);
         all = sum_up(teams.shift, ~0u);
     } else {
         all = sum_up(teams.shift, ~0u);
@@ -544,7 +548,8 @@ __global__ __launch_bounds__(kAttendThreads, (Tile<T, EIGHT, DP, QT>::kPerCu)) v
     // in place of 355 us, but 256 of 67 tokens (70 MB, which the cache holds) 35 in place
     // of 31.  Not where waves read the same tokens: 136 in place of 117 us for 32 windows
     // of 4096 tokens x 4 ranks and 32 query heads of 256.
-    const bool stream = teams.side == 1u && ((uint64_t)row * p.nranks << teams.shift) * dim * (2u * X::kBytes) >= (uint64_t)128 << 20;
+    const uint64_t tokens = (uint64_t)row * p.nranks << teams.shift;
+    const bool stream = teams.side == 1u && tokens * dim * (2u * X::kBytes) >= (uint64_t)128 << 20;
     const CachePlan plan(row * p.nranks, alone ? gridDim.x * kAttendWaves : gridDim.x);
     const uint32_t team = alone ? wave : 0u;
     const uint32_t share = plan.share(blockIdx.x, team, gridDim.x);
@@ -610,10 +615,11 @@ __global__ __launch_bounds__(kAttendThreads, (Tile<T, EIGHT, DP, QT>::kPerCu)) v
 
             X x;
 #pragma unroll
-            for (int t = 0; t < QT; ++t)
-                x.template load_query<EXACT>(
-                    t, p.q[rank] + (seq * p.q_stride + (uint64_t)(head0 + mine0 + 16 * t + n) * dim) * T::kBytes,
-                    mine0 + 16 * t + n < queries, g, dim);
+            for (int t = 0; t < QT; ++t) {
+                const uint32_t q = mine0 + 16 * t + n;
+                const char *at = p.q[rank] + (seq * p.q_stride + (uint64_t)(head0 + q) * dim) * T::kBytes;
+                x.template load_query<EXACT>(t, at, q < queries, g, dim);
+            }
             float ref[QT], sum[QT];
 #pragma unroll
             for (int t = 0; t < QT; ++t) {
@@ -662,7 +668,7 @@ __global__ __launch_bounds__(kAttendThreads, (Tile<T, EIGHT, DP, QT>::kPerCu)) v
                 }
                 lds.rows[wave][mine_at] = p.cache.at((uint32_t)page, place, kv) * X::kBytes;
                 if constexpr (EIGHT)
-                        scale_next = scales[p.cache.scale_at((uint32_t)page, place, kv)];
+                    scale_next = scales[p.cache.scale_at((uint32_t)page, place, kv)];
                 __builtin_amdgcn_wave_barrier();
             };
             // Where the tile's rows are: read from LDS ahead of its loads where there are
@@ -816,7 +822,8 @@ __global__ __launch_bounds__(kAttendThreads, (Tile<T, EIGHT, DP, QT>::kPerCu)) v
             const uint32_t d0 = member % kPieces * 8u;
             const uint32_t slot_floats = most_queries * (DP + 2u);
             const bool whole = step0 == 0 && step1 == steps;
-            const CacheJoin join = {whole ? share : plan.owner(here), whole ? share : plan.owner(here + steps - 1u)};
+            const CacheJoin join = {whole ? share : plan.owner(here),
+                                    whole ? share : plan.owner(here + steps - 1u)};
             uint32_t stage = 0, parts = 0;  // slots of a sum
             for (;;) {
                 const CacheJoin::Parts from_slots = join.parts(share, stage);
@@ -824,7 +831,8 @@ __global__ __launch_bounds__(kAttendThreads, (Tile<T, EIGHT, DP, QT>::kPerCu)) v
                 for (uint32_t q = member / kPieces; q < queries; q += 64u * teams.waves / kPieces) {
                     float top = -__builtin_inff(), total = 0.0f, y[8] = {};
                     // `count` parts of references r, sums of weights l and sums f
-                    auto add = [&](auto parts_at_once, uint32_t count, const float *r, const float *l, const float (*f)[8]) {
+                    auto add = [&](auto parts_at_once, uint32_t count, const float *r, const float *l,
+                                   const float (*f)[8]) {
                         constexpr uint32_t N = decltype(parts_at_once)::value;
                         const float last = top;
 #pragma unroll
@@ -851,7 +859,8 @@ __global__ __launch_bounds__(kAttendThreads, (Tile<T, EIGHT, DP, QT>::kPerCu)) v
                         float r[kAttendWaves], l[kAttendWaves], f[kAttendWaves][8];
 #pragma unroll
                         for (uint32_t j = 0; j < kAttendWaves; ++j) {
-                            const uint32_t w = wave0 + q / X::kQueries + (j < waves_deep ? j : waves_deep - 1u) * teams.side;
+                            const uint32_t deep = j < waves_deep ? j : waves_deep - 1u;
+                            const uint32_t w = wave0 + q / X::kQueries + deep * teams.side;
                             const uint32_t k = q % X::kQueries;
                             r[j] = lds.refs[w][k];
                             l[j] = lds.bad[w] != 0 ? __builtin_nanf("") : lds.weights[w][k];
@@ -866,7 +875,8 @@ __global__ __launch_bounds__(kAttendThreads, (Tile<T, EIGHT, DP, QT>::kPerCu)) v
 #pragma unroll
                             for (uint32_t j = 0; j < kJoinLoads; ++j) {
                                 const uint32_t at = i + j < parts ? i + j : parts - 1u;
-                                const uint32_t part = at == 0 ? from_slots.first : from_slots.next + (at - 1u) * from_slots.by;
+                                const uint32_t part =
+                                    at == 0 ? from_slots.first : from_slots.next + (at - 1u) * from_slots.by;
                                 const float *slot = p.slots + (uint64_t)part * slot_floats;
                                 const f32x2 s = shared_pair(slot + most_queries * DP + 2 * q);
                                 r[j] = s[0];
@@ -883,7 +893,8 @@ __global__ __launch_bounds__(kAttendThreads, (Tile<T, EIGHT, DP, QT>::kPerCu)) v
                     }
                     if (!done) {
                         // (a group's sums: in the place of its first, which this wave alone has read)
-                        float *slot = p.slots + (uint64_t)join.slot(stage == 0 ? share : join.first(share)) * slot_floats;
+                        const uint32_t to_slot = join.slot(stage == 0 ? share : join.first(share));
+                        float *slot = p.slots + (uint64_t)to_slot * slot_floats;
 #pragma unroll
                         for (int e = 0; e < 8; e += 2)
                             share_pair(slot + q * DP + d0 + e, y[e], y[e + 1]);
@@ -896,16 +907,18 @@ __global__ __launch_bounds__(kAttendThreads, (Tile<T, EIGHT, DP, QT>::kPerCu)) v
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
                         y[e] = empty ? 0.0f : y[e] / total;
-                    if (p.has_lse != 0 && d0 == 0)
-                        p.lse[rank][out_row] = empty ? -__builtin_inff()
-                                                     : ((top == -__builtin_inff() ? 0.0f : top) - X::kBias) * kLn2 +
-                                                           __builtin_logf(total);
+                    if (p.has_lse != 0 && d0 == 0) {
+                        const float shift = (top == -__builtin_inff() ? 0.0f : top) - X::kBias;
+                        p.lse[rank][out_row] = empty ? -__builtin_inff() : shift * kLn2 + __builtin_logf(total);
+                    }
                     if constexpr (EIGHT_OUT) {
                         // 16 neighbouring lanes hold the 128 columns of a scale
                         const float s = scale_of(max16(max_bits(y)));
                         store_eights<false>(p.out[rank] + out_row * dim + d0, to_eights(y, s));
-                        if (d0 % AR_SCALE_BLOCK == 0)
-                            p.out_scales[rank][((uint64_t)(head0 + q) * dim + d0) / AR_SCALE_BLOCK * p.seqs + seq] = s;
+                        if (d0 % AR_SCALE_BLOCK == 0) {
+                            const uint64_t block = ((uint64_t)(head0 + q) * dim + d0) / AR_SCALE_BLOCK;
+                            p.out_scales[rank][block * p.seqs + seq] = s;
+                        }
                     } else if (EXACT || d0 < dim) {
                         char *at = p.out[rank] + (out_row * dim + d0) * T::kBytes;
                         constexpr int E = kPiece<T>;
@@ -971,9 +984,9 @@ template <typename T, bool EIGHT, int DP, int QT, bool EXACT, bool EIGHT_OUT>
 hipError_t enqueue_attend(CacheAttentionArgs args, int cu_count, hipStream_t stream)
 {
     typedef Tile<T, EIGHT, DP, QT> X;
-    const uint64_t capacity = args.table_pages * args.cache.page_tokens;
-    const uint64_t tokens = args.window != 0 && args.window < capacity ? args.window : capacity;
-    args.passes = passes_of_a_step(args.seqs, args.nranks, args.cache.heads, args.group, X::kTokenShift, tokens);
+    const uint64_t tokens = most_attended(args.table_pages * args.cache.page_tokens, args.window);
+    args.passes = passes_of_a_step(args.seqs, args.nranks, args.cache.heads, args.group,
+                                   X::kTokenShift, tokens);
     // (a call of few steps has fewer workgroups)
     const CacheTeams teams(args.group, X::kQueryShift, X::kTokenShift, args.passes, false);
     const uint64_t units = (uint64_t)args.nranks * args.cache.heads * args.seqs * teams.tiles;

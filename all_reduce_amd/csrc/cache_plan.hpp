@@ -3,8 +3,9 @@
 //
 // The host does not know the lengths (they change between replays of a graph),
 // so the grid is fixed and each team of waves finds its own share.  A unit is the
-// attention of up to 16 query heads (32 or more where there are more: CacheTeams) of one key-value head of one rank over one sequence; its work comes in
-// steps of `step` tokens, at least one, so that an empty sequence is visited too.
+// attention of up to 16 query heads of one key-value head of one rank over one sequence
+// (of up to 128 where there are more: CacheTeams); its work comes in steps of some
+// tokens, at least one, so that an empty sequence is visited too.
 // All units' steps stand in one row, by rank, then sequence, then key-value head and
 // tile of query heads (heads that lie side by side in memory are read side by side),
 // and are cut into equal shares of whole steps.  A share's first
@@ -31,6 +32,13 @@ __host__ __device__ inline bool attended(int32_t length, uint64_t capacity, uint
     if (window != 0 && (uint64_t)length > window)
         *first = (uint32_t)(length - (int64_t)window);
     return true;
+}
+
+// The tokens that no sequence attends to more than (lengths have 31 bits).
+inline uint64_t most_attended(uint64_t capacity, uint64_t window)
+{
+    const uint64_t most = capacity < INT32_MAX ? capacity : INT32_MAX;
+    return window != 0 && window < most ? window : most;
 }
 
 // Steps of 2^shift tokens.
@@ -133,13 +141,14 @@ __host__ __device__ inline uint32_t passes_to_try(uint32_t steps, uint32_t seqs,
 
 // The smallest power of two of passes to a step (as its exponent) with which all steps
 // of a call can be counted in 31 bits whatever its lengths are: 0, but for calls of
-// extreme sizes.
+// extreme sizes.  With at most 2^24 units it is at most 20, and no step more than 2^30
+// tokens.
 inline uint32_t passes_of_a_step(uint64_t seqs, uint64_t ranks, uint64_t heads, uint32_t group,
                                  uint32_t tokens, uint64_t most_tokens)
 {
     const uint64_t units = seqs * ranks * heads * ((group + 15u) / 16u);
     uint32_t passes = 0;
-    while (units * ((most_tokens >> (tokens + passes)) + 1u) >= (uint64_t)1 << 31 && passes < 24u)
+    while (units * ((most_tokens >> (tokens + passes)) + 1u) >= (uint64_t)1 << 31)
         ++passes;
     return passes;
 }

@@ -102,7 +102,8 @@ arResult_t arCacheRead(const int64_t *slots, size_t tokens, const arCacheLayout_
  *     out[i][j] = sum_t exp(x_t) v_t / sum_t exp(x_t)
  *     lse[i][j] = log(sum_t exp(x_t))
  *
- * Scores, exponentials, sums and accumulators are binary32.  (The products of the
+ * Scores, exponentials, sums and accumulators are binary32; the scores are taken times
+ * log2 e, those of 8-bit keys first without their scales.  (The products of the
  * exponentials with values of 16 and 8 bits take the exponentials in two parts of
  * that type, or three for a float32 output, which hold 16, 22 or 24 bits of them; an
  * infinite value gives an infinity or, where a part is 0, NaN.)
@@ -120,7 +121,7 @@ arResult_t arCacheRead(const int64_t *slots, size_t tokens, const arCacheLayout_
  *  pageTable    device pointer, [seqs][tablePages].
  *  lengths      device pointer, [seqs].
  *  heads        query heads of a rank, a multiple of cache->heads, at most 4096.
- *  scale        finite.
+ *  scale        at most 2^126 in magnitude.
  *  window       tokens that are attended to, the last ones; 0: all.
  *  outbufs      host array of nranks device pointers: [seqs][heads][dim] dense, of
  *               dtype, or 8-bit values when outScales is given.
@@ -131,9 +132,9 @@ arResult_t arCacheRead(const int64_t *slots, size_t tokens, const arCacheLayout_
  *  lse          host array of nranks device pointers [seqs][heads], or NULL.
  *  workspace    device memory of at least the bytes that arCacheAttentionWorkspace
  *               names for this dim and heads / cache->heads, zeros before its first
- *               use; every call leaves it fit for the next.  One call at a time may use it: calls that may run
- *               at once, in graphs as well, need one each.
- *  seqs         at most 65536, and seqs * heads * nranks at most 2^30 (else
+ *               use; every call leaves it fit for the next.  One call at a time may
+ *               use it: calls that may run at once, in graphs as well, need one each.
+ *  seqs         at most 65536, and seqs * heads * nranks at most 2^24 (else
  *               arUnsupported).
  * Rules (arInvalidArgument when broken): no NULL pointer but those named; every
  * pointer 16-byte aligned, pageTable and lengths 4-byte aligned; tablePages >= 1;

@@ -161,8 +161,9 @@ CASES = [
     ("attend dim 24", T, dict(ATTEND, cache=layout(dim=24)), "arUnsupported", "dim"),
     ("attend scale nan", T, dict(ATTEND, scale=float("nan")), "arInvalidArgument", "scale"),
     ("attend scale inf", T, dict(ATTEND, scale=float("inf")), "arInvalidArgument", "scale"),
+    ("attend scale that overflows", T, dict(ATTEND, scale=-1.7e38), "arInvalidArgument", "scale"),
     ("attend 65537 sequences", T, dict(ATTEND, seqs=65537), "arUnsupported", "65536"),
-    ("attend too many units", T, dict(ATTEND, seqs=65536, heads=4096, nranks=5), "arUnsupported", "2^30"),
+    ("attend too many units", T, dict(ATTEND, seqs=65536, heads=130), "arUnsupported", "2^24"),
     ("attend no table", T, dict(ATTEND, table_pages=0), "arInvalidArgument", "tablePages"),
     ("attend table huge", T, dict(ATTEND, table_pages=1 << 31), "arInvalidArgument", "tablePages"),
     ("attend query rows closer than a row", T, dict(ATTEND, query_stride=1016), "arInvalidArgument", "row stride"),

@@ -18,7 +18,7 @@ def pieces_of(lengths, capacity, window, queries, tokens, ranks, heads, group, g
     fn.argtypes = [ctypes.POINTER(I32), SZ, SZ, SZ, U32, U32, U32, U32, U32, U32, U32, U32, ctypes.POINTER(U32), ctypes.c_void_p,
                    SZ]
     teams = (U32 * 5)()
-    most = 1 << 12
+    most = 1 << 16
     out = np.zeros((most, 13), dtype=np.uint32)
     n = fn(lengths, len(lengths), capacity, window, queries, tokens, ranks, heads, group, grid, block, team, teams,
            out.ctypes.data, most)
@@ -89,7 +89,8 @@ PLANS = [
     ([2 ** 31 - 1], 2 ** 31 - 1, 0, 5, 1, 1, 8, 512), ([2 ** 31 - 1, 7], 2 ** 31 - 1, 129, 5, 1, 5, 200, 64),
     ([2 ** 31 - 1] * 9, 2 ** 31 - 1, 0, 5, 8, 4, 16, 512), ([3, 2 ** 31 - 1, 0], 2 ** 31 - 1, 0, 4, 2, 250, 64, 256),
     ([100000, 3], 1 << 17, 50000, 5, 2, 2, 8, 512), ([20] * 700 + [32768], 1 << 16, 0, 5, 1, 2, 8, 512),
-    ([2 ** 31 - 1] + [1] * 600, 2 ** 31 - 1, 0, 5, 1, 2, 8, 512),
+    ([2 ** 31 - 1] + [1] * 600, 2 ** 31 - 1, 0, 5, 1, 2, 8, 512), ([2 ** 31 - 1, 3], 2 ** 50, 0, 5, 1, 2, 8, 512),
+    ([2 ** 31 - 1, 100], 2 ** 50, 2 ** 40, 4, 32, 16, 4, 256), ([2 ** 31 - 1] * 3, 2 ** 62, 0, 5, 16, 8, 64, 512),
 ]
 
 
@@ -112,6 +113,17 @@ def test_drawn_shares():
                             rng.choice([1, 2, 8]), rng.choice([1, 1, 3]), rng.choice([1, 8, 16, 17, 40, 100]),
                             rng.choice([8, 16, 64, 256]), rng.choice([4, 5])))
     assert seen == {(1, 1), (4, 1), (4, 2), (4, 4)}
+
+
+def test_steps_of_extreme_calls():
+    """As many units as a call may have, of the longest sequences: steps are counted in
+    31 bits and shifts stay below 32."""
+    array = (I32 * 65536)(*[2 ** 31 - 1] * 65536)
+    (waves, _, tiles, _, step), pieces = pieces_of(array, 2 ** 31 - 1, 0, 4, 5, 32, 8, 1, 512, 511, 0)
+    units = 65536 * 32 * 8 * tiles
+    steps = -(-(2 ** 31 - 1) // step)
+    assert units == 2 ** 24 and units * steps < 2 ** 31 and step <= 2 ** 30 and waves == 4
+    assert pieces[-1][:5] == [31, 65535, 7, pieces[-1][3], steps]
 
 
 def test_parts():

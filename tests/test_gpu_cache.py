@@ -303,6 +303,13 @@ ATTENDS = [
     (1, [3000, 1, 0, 900], 2, 100, 64, 16, "fp16", "e4m3", "token", None, 700),
     (2, [2000, 40], 1, 48, 256, 16, "fp32", None, "head", None, 0),
     (1, [7000], 1, 32, 128, 64, "bf16", "e4m3", "pair", "e4m3", 0),
+    (1, [150, 3], 1, 300, 64, 16, "fp16", None, "head", None, 0),
+    (1, [700, 0, 41], 1, 100, 256, 16, "fp32", None, "head", None, 0),
+    (1, [70], 1, 4096, 32, 16, "bf16", "e4m3", "head", None, 0),
+    (1, [7, 0], 4096, 1, 16, 16, "bf16", None, "token", None, 0),
+    # a page that holds the whole sequence, and a table that holds far more
+    (1, [3333], 1, 4, 64, 100000, "bf16", None, "head", None, 0),
+    (1, [40, 700], 2, 4, 32, 3, "bf16", "e4m3", "head", None, 2 ** 40),
     (1, [64] * 64, 2, 8, 64, 16, "bf16", None, "head", None, 0),
     (1, [65] * 65, 2, 8, 64, 16, "bf16", None, "head", None, 0),
 ]
@@ -319,7 +326,7 @@ def test_attention(comm, ranks, lengths, heads, group, dim, page, dtype, cache, 
 
 @pytest.mark.parametrize("seqs,longest,ranks,group,dim", [
     (70, 300, 2, 4, 64), (300, 90, 1, 4, 64), (1500, 20, 1, 4, 64), (5000, 6, 1, 4, 64), (60, 200, 12, 3, 128),
-    (600, 300, 1, 20, 64), (700, 40, 2, 70, 64), (400, 50, 2, 1, 256), (64, 100, 16, 16, 80)])
+    (600, 300, 1, 20, 64), (700, 40, 2, 70, 64), (400, 50, 2, 1, 256), (64, 100, 16, 16, 80), (65536, 1, 1, 1, 16)])
 @pytest.mark.parametrize("dtype,cache", [("bf16", "bf16"), ("bf16", "e4m3"), ("fp32", "fp32")])
 def test_attention_of_many_sequences(comm, seqs, longest, ranks, group, dim, dtype, cache):
     """Short ones, and among them one that is far longer."""
@@ -638,7 +645,7 @@ def test_refusals_with_a_device(comm):
     for change in (dict(lengths=a.on[1].long()), dict(page_table=a.on[0][0]), dict(lengths=a.on[1].cpu()),
                    dict(queries=[a.queries[0].float()]), dict(out=[a.out[0][:, :, ::2]]),
                    dict(value_pages=[a.pools[0].values[:, :, :8]]), dict(key_scales=[a.lse[0]]),
-                   dict(lse=[a.lse[0].double()])):
+                   dict(lse=[a.lse[0].double()]), dict(window=-1)):
         with pytest.raises(ValueError):
             comm.cache_attention(**dict(a.args(), **change))
     with pytest.raises(ar.ArError, match="Unsupported"):
