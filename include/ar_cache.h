@@ -105,7 +105,8 @@ arResult_t arCacheRead(const int64_t *slots, size_t tokens, const arCacheLayout_
  * Scores, exponentials, sums and accumulators are binary32; the scores are taken times
  * log2 e, those of 8-bit keys first without their scales.  (The products of the
  * exponentials with values of 16 and 8 bits take the exponentials in two parts of
- * that type, or three for a float32 output, which hold 16, 22 or 24 bits of them; an
+ * that type, which hold 16 bits of them (bfloat16) or 22 (float16), or three, which hold
+ * 24, for a float32 output and of bfloat16 for an 8-bit one with its binary32 scales; an
  * infinite value gives an infinity or, where a part is 0, NaN.)
  * The order of a sum follows from the sizes, the lengths and the card's number of
  * compute units, never from values or from other calls.  Only tokens first .. n - 1

@@ -361,6 +361,39 @@ def test_attention_scales(comm, dtype, cache, scale):
 
 
 @pytest.mark.parametrize("dtype,cache", [("bf16", None), ("fp16", None), ("fp32", None), ("bf16", "e4m3"),
+                                         ("fp16", "e4m3")])
+@pytest.mark.parametrize("group", [4, 20])
+def test_scales_of_8_bit_outputs_are_binary32(comm, dtype, cache, group):
+    """Two tokens, the second with scores -q and values of 1, the first with scores and
+    values of 0: every output is w / (1 + w), w = e^-q.  In steps U = 2^-24: q times log2 e
+    2 |q| log2 e (the constant's and the product's rounding; |q| at most 1.5), which makes
+    3.1 of w, the exponential 2, the parts of w 1, three cut additions of them 6, the sum
+    of weights 1, the division 1, the scale 2: together at most 17 of 20."""
+    note(f"scales of 8-bit outputs {dtype} {cache} {group}")
+    a = Attend(1, [2] * 32, 1, group, 128, 16, dtype, cache, out="e4m3")
+    q = draw((32, group), 3).sigmoid().add(0.5).to(a.dtype)
+    a.rows.zero_()
+    a.queries[0][:, :, 0] = q.cuda()
+    pool, page = a.pools[0], a.table[:, 0].cuda().long()
+    if cache == "e4m3":
+        pool.key_scales[page] = 1.0
+        pool.value_scales[page] = 1.0
+    for which, first, second in (("keys", 0.0, -1.0), ("values", 0.0, 1.0)):
+        t = getattr(pool, which)
+        t = t.view(torch.uint8) if cache == "e4m3" else t
+        for place, value in ((0, first), (1, second)):
+            to = torch.full((32, 1, 128), value, device="cuda:0").to(DT[cache or dtype])
+            t[page, :, place] = to.view(torch.uint8) if cache == "e4m3" else to
+    comm.cache_attention(**a.args(scale=1.0))
+    torch.cuda.synchronize()
+    w = torch.exp(-q.double())
+    want = (w / (1 + w) / 448).t().contiguous()
+    off = (a.out_scales[0].double().cpu() - want).abs() / want
+    assert bool((off <= 20 * 2.0 ** -24).all()), float(off.max() * 2 ** 24)
+    assert bool((a.out[0].float() == 448).all())
+
+
+@pytest.mark.parametrize("dtype,cache", [("bf16", None), ("fp16", None), ("fp32", None), ("bf16", "e4m3"),
                                          ("fp32", "e4m3")])
 def test_scores_that_grow(comm, dtype, cache):
     """The largest score comes last, or first: every step moves the maximum, or none."""
