@@ -63,9 +63,10 @@ host threads and its own GB/s, parity.
 ``--only {sweep, prefill, copy, c5, c5b, hier, ll_variants, ceilings, layer}``
 runs one part alone (for profiler passes; c5b is the fp32 R = 16 / 32 workload
 at 112 MiB per rank, hier the same in the two-level order, fused and staged;
-layer the MLP half of a tensor-parallel layer, 8 ranks of hidden 8192 and a
-28672-wide MLP in 8-bit values, at 1 and 64 tokens: µs of each operator and of
-the pass, graph-replayed).
+layer the two halves of a tensor-parallel layer, 8 ranks of hidden 8192 and a
+28672-wide MLP in 8-bit values, 8 query heads of 128 to a rank's one key-value
+head and 8192 cached tokens a sequence in 8 bits, at 1 and 64 tokens: µs of each
+operator and of the pass, graph-replayed).
 """
 from __future__ import annotations
 
@@ -565,6 +566,7 @@ def main():
     # ---- the operators around the all-reduce, as a layer runs them ------------
     if args.only == "layer":
         result["layer"] = [run_layer(B, tokens) for tokens in (1, 64)]
+        result["attention"] = [run_attention(B, tokens) for tokens in (1, 64)]
 
     # ---- every named workload as one table ----------------------------------
     if args.configs and args.only == "all":
@@ -773,6 +775,94 @@ def run_c5(B, inputs, fp16=True):
     return rows
 
 
+def rank_tensors(B, ranks, *shape, dtype):
+    """One tensor a rank, in one allocation."""
+    return list(B.torch.empty((ranks, *shape), dtype=dtype, device=B.dev).unbind(0))
+
+
+def eight_bit_weights(B, ranks, n, k, gen):
+    """Synthetic 8-bit weights of n x k a rank and their scales, products of about 1."""
+    torch, ar = B.torch, B.ar
+    w = rank_tensors(B, ranks, n, k, dtype=torch.float8_e4m3fn)
+    s = rank_tensors(B, ranks, ar.scale_blocks(n), ar.scale_blocks(k), dtype=torch.float32)
+    for t, u in zip(w, s):
+        t.copy_(torch.randn((n, k), generator=gen, device=B.dev).mul_(110).clamp_(-448, 448))
+        u.fill_(1 / (110 * k ** 0.5))
+    return w, s
+
+
+def graph_us(B, call):
+    return round(statistics.median(B.graph_passes(None, None, 0, None, passes=MEDIAN_PASSES, call=call)), 2)
+
+
+def run_attention(B, seqs, cached=8192):
+    """The attention half of a tensor-parallel layer over 8 ranks in a decode step:
+    all-reduce of the MLP's partial sums with residual and norm into 8 bits, QKV
+    product, the new tokens' keys and values into the paged 8-bit cache, attention
+    of one token a sequence with an 8-bit output, output product; and the output
+    product with its all-reduce in one kernel.  Sequences of `cached` tokens, the
+    new one among them, in pages of 64 that lie anywhere; the last output is
+    checked to be finite and alike on every rank."""
+    torch, ar, c = B.torch, B.ar, B.comm
+    ranks, hidden, group, dim, page = 8, 8192, 8, 128, 64
+    e4m3, bf16, f32 = torch.float8_e4m3fn, torch.bfloat16, torch.float32
+    gen = torch.Generator("cuda").manual_seed(seqs)
+
+    def bufs(*shape, dtype):
+        return rank_tensors(B, ranks, *shape, dtype=dtype)
+
+    x, h, part, out = (bufs(seqs, hidden, dtype=bf16) for _ in range(4))
+    for t in x:
+        t.normal_(generator=gen)
+    res = torch.randn((seqs, hidden), generator=gen, device=B.dev).to(bf16)
+    norm = torch.ones(hidden, dtype=bf16, device=B.dev)
+    q8, qs = bufs(seqs, hidden, dtype=e4m3), bufs(ar.scale_blocks(hidden), seqs, dtype=f32)
+    w1, s1 = eight_bit_weights(B, ranks, (group + 2) * dim, hidden, gen)
+    w2, s2 = eight_bit_weights(B, ranks, hidden, group * dim, gen)
+    qkv = bufs(seqs, group + 2, dim, dtype=bf16)
+    queries, keys, values = ([t[:, a:b] for t in qkv]
+                             for a, b in ((0, group), (group, group + 1), (group + 1, group + 2)))
+    of_one = -(-cached // page)
+    pages = seqs * of_one
+    pools = [bufs(pages, 1, page, dim, dtype=e4m3) for _ in range(2)]
+    scales = [bufs(pages, 1, page, dtype=f32) for _ in range(2)]
+    for pool, scale in zip(pools, scales):
+        for t, s in zip(pool, scale):
+            t.copy_(torch.randn(t.shape, generator=gen, device=B.dev).mul_(110).clamp_(-448, 448))
+            s.fill_(1 / 110)
+    table = torch.randperm(pages, generator=gen, device=B.dev).int().view(seqs, of_one)
+    lengths = torch.full((seqs,), cached, dtype=torch.int32, device=B.dev)
+    slots = table[:, (cached - 1) // page].long() * page + (cached - 1) % page
+    att, att_s = bufs(seqs, group, dim, dtype=e4m3), bufs(group, seqs, dtype=f32)
+    flat = [t.view(seqs, -1) for t in att]
+    work = c.cache_workspace(dim, group)
+    calls = {
+        "all-reduce + norm, 8-bit": lambda: c.all_reduce_norm(x, norm, 1e-5, res, h, q8, qs),
+        "QKV product": lambda: c.matmul_scaled(q8, qs, w1, s1, [t.view(seqs, -1) for t in qkv]),
+        "cache write, 8-bit": lambda: c.cache_write(keys, values, slots, *pools, *scales),
+        "attention, 8-bit": lambda: c.cache_attention(queries, *pools, table, lengths, att, *scales,
+                                                      out_scales=att_s, workspace=work),
+        "output product": lambda: c.matmul_scaled(flat, att_s, w2, s2, part),
+    }
+
+    def half():
+        for call in calls.values():
+            call()
+
+    half()
+    row = {"ranks": ranks, "tokens": seqs, "hidden": hidden, "cached": cached,
+           "us": {name: graph_us(B, call) for name, call in calls.items()}, "half_us": graph_us(B, half)}
+    last = lambda: c.matmul_scaled(flat, att_s, w2, s2, out, reduce=True)
+    row["us"]["output product + all-reduce"] = graph_us(B, last)
+    half()
+    last()
+    torch.cuda.synchronize()
+    row["finite_and_alike"] = bool(out[0].isfinite().all()) and all(torch.equal(t, out[0]) for t in out)
+    log(f"attention half, {seqs} tokens: {row['half_us']} us; " +
+        "  ".join(f"{k} {v}" for k, v in row["us"].items()))
+    return row
+
+
 def run_layer(B, tokens):
     """The MLP half of a tensor-parallel layer over 8 ranks: all-reduce of the
     attention's partial sums with residual and norm into 8 bits, up product,
@@ -785,14 +875,7 @@ def run_layer(B, tokens):
     gen = torch.Generator("cuda").manual_seed(tokens)
 
     def bufs(rows, cols, dtype):
-        return list(torch.empty((ranks, rows, cols), dtype=dtype, device=B.dev).unbind(0))
-
-    def weights(n, k):
-        w, s = bufs(n, k, e4m3), bufs(ar.scale_blocks(n), ar.scale_blocks(k), torch.float32)
-        for t, u in zip(w, s):
-            t.copy_(torch.randn((n, k), generator=gen, device=B.dev).mul_(110).clamp_(-448, 448))
-            u.fill_(1 / (110 * k ** 0.5))
-        return w, s
+        return rank_tensors(B, ranks, rows, cols, dtype=dtype)
 
     x, h, h2, y = (bufs(tokens, hidden, bf16) for _ in range(4))
     for t in x:
@@ -802,8 +885,8 @@ def run_layer(B, tokens):
     q, qs = bufs(tokens, hidden, e4m3), bufs(ar.scale_blocks(hidden), tokens, torch.float32)
     up, part = bufs(tokens, 2 * inner, bf16), bufs(tokens, hidden, bf16)
     g, gs = bufs(tokens, inner, e4m3), bufs(ar.scale_blocks(inner), tokens, torch.float32)
-    w1, s1 = weights(2 * inner, hidden)
-    w2, s2 = weights(hidden, inner)
+    w1, s1 = eight_bit_weights(B, ranks, 2 * inner, hidden, gen)
+    w2, s2 = eight_bit_weights(B, ranks, hidden, inner, gen)
     c = B.comm
     # (streams are taken where a call is made: graph capture has its own)
     calls = {
@@ -819,8 +902,7 @@ def run_layer(B, tokens):
             call()
 
     def us(call):
-        return round(statistics.median(B.graph_passes(None, None, 0, None, passes=MEDIAN_PASSES,
-                                                      call=call)), 2)
+        return graph_us(B, call)
 
     layer()
     row = {"ranks": ranks, "tokens": tokens, "hidden": hidden, "mlp": 28672,
