@@ -351,7 +351,7 @@ size_t ar_cache_attention_share(const int32_t *lengths, size_t seqs, size_t capa
     for (;;) {
         const uint32_t steps = steps_at(seq);
         const uint32_t step1 = left < steps - step0 ? step0 + left : steps;
-        const CacheJoin join = {plan.owner(here), plan.owner(here + steps - 1u)};
+        const CacheJoin join(plan.owner(here), plan.owner(here + steps - 1u));
         const uint32_t piece[13] = {
             rank, seq, unit, step0, step1, steps, first + (step0 << t.shift),
             step1 == steps ? end : first + (step1 << t.shift), join.slot(share), join.group_counter(share),
@@ -378,7 +378,7 @@ size_t ar_cache_attention_share(const int32_t *lengths, size_t seqs, size_t capa
 // of teams w0 .. w1.
 uint32_t ar_cache_attention_part(uint32_t w0, uint32_t w1, uint32_t w, uint32_t stage, uint32_t i)
 {
-    const CacheJoin::Parts parts = CacheJoin{w0, w1}.parts(w, stage);
+    const CacheJoin::Parts parts = CacheJoin(w0, w1).parts(w, stage);
     return i == 0 ? parts.first : parts.next + (i - 1u) * parts.by;
 }
 

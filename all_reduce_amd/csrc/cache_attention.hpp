@@ -824,8 +824,8 @@ void cache_attend(CacheAttentionArgs p)
             const uint32_t d0 = member % kPieces * 8u;
             const uint32_t slot_floats = most_queries * (DP + 2u);
             const bool whole = step0 == 0 && step1 == steps;
-            const CacheJoin join = {whole ? share : plan.owner(here),
-                                    whole ? share : plan.owner(here + steps - 1u)};
+            const CacheJoin join(whole ? share : plan.owner(here),
+                                 whole ? share : plan.owner(here + steps - 1u));
             uint32_t stage = 0, parts = 0;  // slots of a sum
             for (;;) {
                 const CacheJoin::Parts from_slots = join.parts(share, stage);

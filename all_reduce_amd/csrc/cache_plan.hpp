@@ -155,26 +155,31 @@ inline uint32_t passes_of_a_step(uint64_t seqs, uint64_t ranks, uint64_t heads, 
 
 // The workspace: counters first, then two slots of partial sums a team, one for
 // the unit that its share begins inside, one for the unit that it ends inside.
-// Partial sums are joined in two steps, 16 consecutive teams first, so that one
-// long sequence is not joined by one team alone.
-constexpr uint32_t kJoinGroup = 16;
+// Partial sums of up to 16 teams are joined by the last of them; those of more in two
+// steps, by the last of groups of consecutive teams and then by the last of the groups,
+// so that one long sequence is not joined by one team alone.  (On MI355X: 8 sequences of
+// 4000 tokens, 32 teams each, 13.9 us by eights, 15.4 by 16, 16.9 by one team; 128
+// windows of 4096, 2 or 3 teams each, 113.5 in one step, 116.5 where groups began at
+// multiples of 16 and some took two.)
 struct CacheJoin {
     uint32_t w0, w1;  // the unit's first and last team
+    uint32_t shift;   // groups of 2^shift teams
+    __host__ __device__ CacheJoin(uint32_t first, uint32_t last) : w0(first), w1(last)
+    {
+        const uint32_t apart = last - first;
+        shift = apart < 16u ? 4u : apart < 64u ? 3u : apart < 256u ? 4u : 5u;
+    }
     __host__ __device__ uint32_t slot(uint32_t w) const { return 2u * w + (w == w0 ? 1u : 0u); }
     // The group of w: its first and last member.
-    __host__ __device__ uint32_t first(uint32_t w) const
-    {
-        const uint32_t g = w / kJoinGroup * kJoinGroup;
-        return g > w0 ? g : w0;
-    }
+    __host__ __device__ uint32_t first(uint32_t w) const { return w0 + ((w - w0) >> shift << shift); }
     __host__ __device__ uint32_t last(uint32_t w) const
     {
-        const uint32_t g = w / kJoinGroup * kJoinGroup + kJoinGroup - 1u;
-        return g < w1 ? g : w1;
+        const uint32_t l = first(w) + (1u << shift) - 1u;
+        return l < w1 ? l : w1;
     }
-    __host__ __device__ uint32_t groups() const { return w1 / kJoinGroup - w0 / kJoinGroup + 1u; }
-    // A team begins at most one group inside its share (its last piece's unit starts
-    // there) and one as the first of 16; and at most one unit.
+    __host__ __device__ uint32_t groups() const { return ((w1 - w0) >> shift) + 1u; }
+    // A team is the first of a group of the unit that its share begins inside, and of
+    // the unit that it ends inside, which has its counter there too.
     __host__ __device__ uint32_t group_counter(uint32_t w) const
     {
         const uint32_t f = first(w);
@@ -188,9 +193,8 @@ struct CacheJoin {
     };
     __host__ __device__ Parts parts(uint32_t w, uint32_t stage) const
     {
-        const uint32_t f = stage == 1u ? first(w) : w0;
-        return {slot(f), 2u * (stage == 1u ? f + 1u : (w0 / kJoinGroup + 1u) * kJoinGroup),
-                stage == 1u ? 2u : 2u * kJoinGroup};
+        const uint32_t f = stage == 1u ? first(w) : w0, by = stage == 1u ? 1u : 1u << shift;
+        return {slot(f), 2u * (f + by), 2u * by};
     }
 };
 

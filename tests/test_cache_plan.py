@@ -70,7 +70,7 @@ def check_plan(lengths, capacity, window, tokens, ranks, heads, group, grid, que
             members.setdefault(gc, []).append(gn)
         for gc, sizes_of in members.items():
             assert all(x == len(sizes_of) for x in sizes_of), (key, gc, sizes_of)
-            assert len(sizes_of) <= 16
+            assert len(sizes_of) <= 32
         uc, groups = unit_counter.pop()
         assert groups == len(members)
         for c in (*members, uc):
@@ -132,12 +132,14 @@ def test_parts():
     fn = ar.library().ar_cache_attention_part
     fn.restype = U32
     fn.argtypes = [U32] * 5
-    for w0, w1 in ((0, 1), (3, 5), (15, 16), (0, 511), (7, 40), (16, 31), (31, 32), (5, 2047)):
+    for w0, w1 in ((0, 1), (3, 5), (15, 16), (0, 511), (7, 40), (16, 31), (31, 32), (5, 2047), (3, 18), (3, 19), (9, 72), (9, 73), (0, 255), (0, 256)):
         def slot(w):
             return 2 * w + (w == w0)
         starts = []
-        for b in range(w0 // 16, w1 // 16 + 1):
-            members = list(range(max(w0, 16 * b), min(w1, 16 * b + 15) + 1))
+        n = w1 - w0 + 1
+        each = 16 if n <= 16 else 8 if n <= 64 else 16 if n <= 256 else 32
+        for b in range(w0, w1 + 1, each):
+            members = list(range(b, min(w1, b + each - 1) + 1))
             starts.append(members[0])
             for w in members:
                 assert [fn(w0, w1, w, 1, i) for i in range(len(members))] == [slot(m) for m in members]
