@@ -157,10 +157,10 @@ inline uint32_t passes_of_a_step(uint64_t seqs, uint64_t ranks, uint64_t heads, 
 // the unit that its share begins inside, one for the unit that it ends inside.
 // Partial sums of up to 16 teams are joined by the last of them; those of more in two
 // steps, by the last of groups of consecutive teams and then by the last of the groups,
-// so that one long sequence is not joined by one team alone.  (On MI355X: 8 sequences of
-// 4000 tokens, 32 teams each, 13.9 us by eights, 15.4 by 16, 16.9 by one team; 128
-// windows of 4096, 2 or 3 teams each, 113.5 in one step, 116.5 where groups began at
-// multiples of 16 and some took two.)
+// so that one long sequence is not joined by one team alone.  (On MI355X: 8 units of
+// 4000 tokens, 32 teams each, 12.7 us by eights and 15.3 by one team, 8 of 8192 in 8 bits,
+// 64 teams each, 16.3 by eights and 17.3 by 16; 128 windows of 4096, 2 or 3 teams each,
+// 113.5 in one step, 116.5 where groups began at multiples of 16 and some took two.)
 struct CacheJoin {
     uint32_t w0, w1;  // the unit's first and last team
     uint32_t shift;   // groups of 2^shift teams
