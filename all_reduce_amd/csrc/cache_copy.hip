@@ -63,7 +63,8 @@ __global__ __launch_bounds__(256) void cache_write(CacheCopyArgs p)
                 head[t] = (uint32_t)(r - (uint64_t)token * p.cache.heads);
                 slot[t] = p.slots[token];
                 if (d < p.cache.dim)
-                    x[t] = load_piece<NT>(rows + (token * p.row_stride + head[t] * p.cache.dim + d) * T::kBytes);
+                    x[t] = load_piece<NT>(
+                        rows + (token * p.row_stride + head[t] * p.cache.dim + d) * T::kBytes);
             }
         }
 #pragma unroll
