@@ -30,7 +30,7 @@
 // That is rare, so the loop has no reductions across lanes.
 //
 // Measured on MI355X, where reading alone reaches 7.1 TB/s: 64 x 8192 tokens x 8 ranks,
-// 8 query heads of 128, 323 us (6.7 TB/s of keys and values; 8 bits 172 us, 6.45);
+// 8 query heads of 128, 318 us (6.75 TB/s of keys and values; 8 bits 171 us, 6.5);
 // 4 ranks with heads of 256 316 us (6.8); heads of 64 165 us (6.5).  A call of few tokens
 // is one chain of loads (lengths, page, keys, queries), the waves' sums in LDS and, for a
 // unit of several teams, one or two joins through memory of 3 to 4 us: one sequence of
@@ -683,7 +683,8 @@ void cache_attend(CacheAttentionArgs p)
                 __builtin_amdgcn_wave_barrier();
             };
             // Where the tile's rows are: read from LDS ahead of its loads where there are
-            // registers for that (QT 1: 64 x 8192 tokens x 8 ranks 314 in place of 322 us).
+            // registers for that, beside the scores' instructions (QT 1: 64 x 8192 tokens x 8
+            // ranks 318 us; before those 324, each at its loads 322 where the rest took 314).
             const char *krow[X::kGroups], *vrow[X::kGroups][4];
             auto find_keys = [&] {
 #pragma unroll
@@ -733,13 +734,13 @@ void cache_attend(CacheAttentionArgs p)
                         __builtin_amdgcn_wave_barrier();
                     }
                     rows(t0 + teams.pass, page_next, place_next);
+                    page_next = look(t0 + 2 * teams.pass, place_next);
+                    f32x4 s[QT][X::kGroups];
+                    x.scores(s);
                     if constexpr (QT == 1) {
                         find_keys();
                         find_values();
                     }
-                    page_next = look(t0 + 2 * teams.pass, place_next);
-                    f32x4 s[QT][X::kGroups];
-                    x.scores(s);
                     matrix_done(s);
                     // (also behind the last tile, where there is nothing to load: behind a branch the
                     // compiler would wait for the keys where it needs the values)
