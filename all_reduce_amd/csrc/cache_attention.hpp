@@ -68,7 +68,7 @@ __device__ inline uint32_t pack2(float a, float b)
 }
 
 // The same of eight floats in PARTS words each: part i is the rounding of what
-// the parts before it leave.  An infinity or NaN stays in the first.
+// the parts before it leave.
 template <typename M, int PARTS>
 __device__ inline void split8(const float (&x)[8], u32x4 (&out)[PARTS])
 {
@@ -836,6 +836,37 @@ void cache_attend(CacheAttentionArgs p)
             const bool whole = step0 == 0 && step1 == steps;
             const CacheJoin join(whole ? share : plan.owner(here),
                                  whole ? share : plan.owner(here + steps - 1u));
+            // An infinite value times a later part of its weight, which is zero or negative as
+            // often as not, makes NaN of the infinity that it stands for.  A column that is NaN
+            // although its weights are not is the sum of the infinities and NaNs in it.
+            // (Looked for here, among the eight sums of a lane, it costs 1 x 1000 tokens 0.2 us of 10.2
+            // and windows with 32 heads of 256 1 of 106; among a wave's accumulators 4 of 106.)
+            auto infinities = [&](float (&y)[8]) {
+                float f[8] = {};
+#pragma unroll 1
+                for (uint32_t t = first + (step0 << teams.shift); t < t1; ++t) {
+                    const uint32_t i = p.cache.page_of(t), place = t - i * p.cache.page_tokens;
+                    const uint32_t page = (uint32_t)table[i];
+                    if (page >= p.cache.pages)
+                        continue;
+                    const char *at = values + (p.cache.at(page, place, kv) + d0) * X::kBytes;
+                    float v[8];
+                    if constexpr (EIGHT) {
+                        const float s = p.value_scales[rank][p.cache.scale_at(page, place, kv)];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            v[e] = __builtin_amdgcn_cvt_f32_fp8((int)((const uint8_t *)at)[e], 0) * s;
+                    } else if constexpr (!X::kWide) {
+                        widen_piece<T>(load_piece<false>(at), v);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        f[e] += __builtin_isfinite(v[e]) ? 0.0f : v[e];
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    y[e] = __builtin_isnan(y[e]) && !__builtin_isfinite(f[e]) ? f[e] : y[e];
+            };
             uint32_t stage = 0, parts = 0;  // slots of a sum
             for (;;) {
                 const CacheJoin::Parts from_slots = join.parts(share, stage);
@@ -882,6 +913,14 @@ void cache_attend(CacheAttentionArgs p)
                                 f[j][e] = lds.sums[w][k][d0 + e];
                         }
                         add(std::integral_constant<uint32_t, kAttendWaves>{}, waves_deep, r, l, f);
+                        if constexpr (!X::kWide) {
+                            float zero = 0.0f;  // NaN behind an infinity or NaN
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                zero = __builtin_fmaf(y[e], 0.0f, zero);
+                            if (__builtin_expect(__builtin_isnan(zero) && !__builtin_isnan(total), false))
+                                infinities(y);
+                        }
                     } else {
                         for (uint32_t i = 0; i < parts; i += kJoinLoads) {
                             float r[kJoinLoads], l[kJoinLoads], f[kJoinLoads][8];

@@ -458,6 +458,45 @@ def test_attention_special_values(comm, dtype):
     block_ref.assert_within(lse[0], l, l_tol, "their lse")
 
 
+@pytest.mark.parametrize("query", [1.0, 4.0])
+@pytest.mark.parametrize("dtype,cache,out,group,dim", [
+    ("bf16", None, None, 4, 64), ("fp16", None, None, 4, 128), ("fp32", None, None, 4, 64), ("bf16", None, "e4m3", 20, 128),
+    ("fp16", None, None, 40, 80), ("bf16", "e4m3", None, 4, 128), ("fp16", "e4m3", "e4m3", 8, 128), ("fp32", "e4m3", None, 20, 64)])
+def test_infinite_values(comm, dtype, cache, out, group, dim, query):
+    """An infinity among the values makes its column one, whatever its weight, in a sequence
+    of one token as in a joined one; two of both signs and a NaN make it NaN; the other columns
+    keep their values.  (8 bits: a value of zero times a scale of infinity is NaN.)"""
+    note(f"attention, infinite values {dtype} {cache} {out} {group} x {dim} {query}")
+    inf = float("inf")
+    a = Attend(1, [1, 300, 9000, 40], 1, group, dim, 16, dtype, cache, out=out, query=query)
+    pool = a.pools[0]
+
+    def put(i, t, column, value):
+        at = int(a.table[i, t // 16]), 0, t % 16
+        if cache == "e4m3":
+            pool.value_scales[at] = value
+        else:
+            pool.values[at][column] = value
+
+    put(0, 0, 3, inf)
+    put(1, 77, 9, -inf)
+    put(2, 0, dim - 1, inf)
+    if cache == "e4m3":
+        put(2, 8000, 0, inf)
+    else:
+        put(1, 5, 10, inf)
+        put(1, 20, 11, inf)
+        put(1, 250, 11, -inf)
+        put(1, 299, 12, float("nan"))
+        put(1, 100, 13, inf)
+        put(1, 101, 13, inf)
+        put(2, 8999, 0, -inf)
+    comm.cache_attention(**a.args())
+    a.check()
+    y = a.out[0][0].float() if out is None else a.out_scales[0][:, 0]
+    assert y.isinf().any()
+
+
 @pytest.mark.parametrize("dtype,cache,lowest", [
     ("bf16", None, None), ("fp16", None, None), ("fp32", None, None), ("bf16", None, torch.finfo(torch.bfloat16).min),
     ("fp16", None, torch.finfo(torch.float16).min), ("fp32", None, torch.finfo(torch.float32).min / 2), ("bf16", "e4m3", None)])
