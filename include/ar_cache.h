@@ -108,7 +108,8 @@ arResult_t arCacheRead(const int64_t *slots, size_t tokens, const arCacheLayout_
  * that type, which hold 16 bits of them (bfloat16) or 22 (float16), or three, which hold
  * 24, for a float32 output and of bfloat16 for an 8-bit one with its binary32 scales.)
  * An infinite value makes its column an infinity, or NaN beside a NaN or an infinity of the
- * other sign; of a token whose weight is less than binary32 holds, either.
+ * other sign; of a token whose weight is less than binary32 holds, either.  A score of
+ * infinity makes lse one, NaN beside a NaN, and out NaN.
  * The order of a sum follows from the sizes, the lengths and the card's number of
  * compute units, never from values or from other calls.  Only tokens first .. n - 1
  * and the table's entries for them are read, whatever the other places hold.

@@ -458,6 +458,54 @@ def test_attention_special_values(comm, dtype):
     block_ref.assert_within(lse[0], l, l_tol, "their lse")
 
 
+@pytest.mark.parametrize("dtype,cache,group", [("bf16", None, 4), ("fp16", None, 20), ("fp32", None, 4), ("bf16", "e4m3", 8),
+                                               ("fp32", "e4m3", 3)])
+def test_scores_of_plus_infinity(comm, dtype, cache, group):
+    """They make NaN of their query head's output and an infinity of its log-sum, NaN beside a
+    NaN score, in any piece of a joined sequence; where the same token's score is minus infinity
+    it has no weight."""
+    note(f"attention, scores of plus infinity {dtype} {cache} {group}")
+    inf = float("inf")
+    a = Attend(1, [1, 300, 9000, 9000, 50], 1, group, 64, 16, dtype, cache)
+    sign = torch.where(torch.arange(group) % 3 == 1, -1.0, 1.0).to(a.dtype)
+    a.rows[0][:, 1:1 + group, 0] = sign.cuda()
+    if cache == "e4m3":
+        a.rows[0][:, 1:1 + group, 1:] = 0.0
+    a.q = a.rows.cpu()
+    pool = a.pools[0]
+
+    def at(i, t):
+        return int(a.table[i, t // 16]), 0, t % 16
+
+    def set_key(i, t, value):
+        if cache == "e4m3":  # a one times the scale (a zero times infinity is NaN, so there only one dim has a query)
+            pool.bytes("key")[(*at(i, t), 0)] = torch.tensor(1.0).to(E4M3).view(torch.uint8).cuda()
+            pool.key_scales[at(i, t)] = value
+        else:
+            pool.keys[(*at(i, t), 0)] = value
+
+    infinite = {0: 0, 1: 130, 2: 8999, 3: 17}
+    for i, t in infinite.items():
+        set_key(i, t, inf)
+    set_key(3, 6000, float("nan"))
+    comm.cache_attention(**a.args())
+    torch.cuda.synchronize()
+    out, lse = a.out[0].cpu(), a.lse[0].cpu()
+    up = sign > 0
+    for i in (0, 1, 2):
+        assert out[i][up].isnan().all() and (lse[i][up] == inf).all(), (i, lse[i])
+    assert out[0][~up].isnan().all() and (lse[0][~up] == -inf).all()
+    assert out[3].isnan().all() and lse[3].isnan().all()
+    for i in (1, 2):
+        t = torch.tensor([t for t in range(int(a.lengths[i])) if t != infinite[i]])
+        page, place = a.table[i].long()[t // 16].cuda(), (t % 16).cuda()
+        k, v = (pool.rows(w, page, place)[:, 0] for w in ("key", "value"))
+        y, tol, l, l_tol = ref.attention(a.q[0, i, 1:1 + group].double(), k, v, 0.125, a.dtype, cache == "e4m3")
+        block_ref.assert_within(out[i][~up], y[~up], ref.round_up(y, tol, a.dtype)[~up], "beside a score of infinity")
+        block_ref.assert_within(lse[i][~up], l[~up], l_tol[~up], "their lse")
+    a.check(seqs=[4])
+
+
 @pytest.mark.parametrize("query", [1.0, 4.0])
 @pytest.mark.parametrize("dtype,cache,out,group,dim", [
     ("bf16", None, None, 4, 64), ("fp16", None, None, 4, 128), ("fp32", None, None, 4, 64), ("bf16", None, "e4m3", 20, 128),
