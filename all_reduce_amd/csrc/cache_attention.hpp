@@ -118,7 +118,7 @@ __device__ inline uint32_t widen_pair(uint32_t w)
 // split in three parts of 8 bits, and to bfloat16 for the values, whose scale goes
 // into the weight: float16 might not hold the product.  float32 caches use the
 // binary32 instruction.
-template <typename T, bool EIGHT, int DP, int QT, bool EIGHT_OUT = false>
+template <typename T, bool EIGHT, int DP, int QT>
 struct Tile {
     static constexpr bool kWide = !EIGHT && T::kBytes == 4;
     static constexpr int kBytes = EIGHT ? 1 : T::kBytes;      // of a cached value
@@ -136,9 +136,12 @@ struct Tile {
     using KeyType = std::conditional_t<T::kId == Fp16::kId, Fp16, Bf16>;
     using ValueType = std::conditional_t<!EIGHT && T::kId == Fp16::kId, Fp16, Bf16>;
     static constexpr int kQueryParts = EIGHT && T::kBytes == 4 ? 3 : 1;
-    // Two parts hold 22 bits of a weight in float16 and 16 in bfloat16, which is enough
-    // for 16-bit outputs; three for binary32 ones, which the scales of 8-bit outputs are.
-    static constexpr int kWeightParts = T::kBytes == 4 || (EIGHT_OUT && ValueType::kId != Fp16::kId) ? 3 : 2;
+    // The parts of a weight, each the rounding of what is left, hold a binary32's bits:
+    // three of bfloat16 all, two of float16 all but 2^-23 of the weight or 2^-33 of the
+    // largest.  (Two of bfloat16, 2^-18 off, took 64 x 8192 tokens x 8 ranks in 318.0 us in
+    // place of 318.4, 8-bit heads of 64 in 91 in place of 94.5, one rank's 64 query heads
+    // in 72 in place of 75.)
+    static constexpr int kWeightParts = ValueType::kId == Fp16::kId ? 2 : 3;
     // Weights are at most 2^kRoom, and the largest of those that set the reference
     // 2^kBias: float16 keeps more of the small ones that way.
     static constexpr float kBias = ValueType::kId == Fp16::kId ? 8.0f : 0.0f;
@@ -461,7 +464,7 @@ template <typename T, bool EIGHT, int DP, int QT, bool EXACT, bool EIGHT_OUT>
 __global__ __launch_bounds__(kAttendThreads, (Tile<T, EIGHT, DP, QT>::kPerCu))
 void cache_attend(CacheAttentionArgs p)
 {
-    typedef Tile<T, EIGHT, DP, QT, EIGHT_OUT> X;
+    typedef Tile<T, EIGHT, DP, QT> X;
     __shared__ __align__(16) AttendShared<X, DP> lds;
     const uint32_t lane = threadIdx.x & 63u, wave = uniform(threadIdx.x >> 6);
     const uint32_t n = lane & 15u, g = lane >> 4;

@@ -104,9 +104,9 @@ arResult_t arCacheRead(const int64_t *slots, size_t tokens, const arCacheLayout_
  *
  * Scores, exponentials, sums and accumulators are binary32; the scores are taken times
  * log2 e, those of 8-bit keys first without their scales.  (The products of the
- * exponentials with values of 16 and 8 bits take the exponentials in two parts of
- * that type, which hold 16 bits of them (bfloat16) or 22 (float16), or three, which hold
- * 24, for a float32 output and of bfloat16 for an 8-bit one with its binary32 scales.)
+ * exponentials with values of 16 and 8 bits take the exponentials in three parts of bfloat16,
+ * which hold all of their 24 bits, or, for values of float16, in two parts of that, which are
+ * within 2^-23 of an exponential or 2^-33 of the largest.)
  * An infinite value makes its column an infinity, or NaN beside a NaN or an infinity of the
  * other sign; of a token whose weight is less than binary32 holds, either.  A score of
  * infinity makes lse one, NaN beside a NaN, and out NaN.

@@ -393,6 +393,54 @@ def test_scales_of_8_bit_outputs_are_binary32(comm, dtype, cache, group):
     assert bool((a.out[0].float() == 448).all())
 
 
+@pytest.mark.parametrize("dtype,cache,out", [("bf16", None, None), ("fp16", None, None), ("fp32", None, None), ("bf16", None, "e4m3"),
+                                             ("bf16", "e4m3", None), ("fp16", "e4m3", None), ("fp32", "e4m3", None)])
+@pytest.mark.parametrize("group", [4, 20])
+def test_weights_are_binary32(comm, dtype, cache, out, group):
+    """Three tokens whose values cancel the first 16 bits of a weight: two of score 0 with
+    values -a and -b, one of score -q with value 1, w = e^-q, a the rounding of w to the
+    cache's bits (8, or 11), b that of w - a: every output is (w - a - b) / (2 + w).
+    In steps U = 2^-24 of 1: q times log2 e and its factor 2 |q| (|q| at most 0.65), the shift of
+    8 of float16 6, the exponential 2, the parts of a weight 2, its product with a scale 2, three
+    instructions' sums of magnitudes up to 2, cut inside and at their end, 24: together at
+    most 38 of 40.  (Two parts of 8 bits would be up to 64 off.)"""
+    note(f"weights are binary32 {dtype} {cache} {out} {group}")
+    a = Attend(1, [3] * 64, 1, group, 128, 16, dtype, cache, out=out)
+    q = (0.05 + 0.6 * torch.rand(64, generator=torch.Generator().manual_seed(4))).to(a.dtype)
+    a.rows.zero_()
+    a.queries[0][:, :, 0] = q[:, None].cuda()
+    w = torch.exp(-q.double())
+    bits = torch.float16 if dtype == "fp16" else torch.bfloat16
+    first = w.to(bits)
+    second = (w - first.double()).to(bits)
+    pool, page = a.pools[0], a.table[:, 0].cuda().long()
+    keys = torch.zeros((64, 3, 128))
+    keys[:, 2] = -1.0
+    values = torch.stack([-first.float(), -second.float(), torch.ones(64)], 1)
+    for place in range(3):
+        if cache == "e4m3":
+            for which, x in (("key", keys[:, place].sign()), ("value", values[:, place, None].sign().expand(64, 128))):
+                pool.bytes(which)[page, 0, place] = x.to(E4M3).view(torch.uint8).cuda()
+            pool.key_scales[page, 0, place] = 1.0
+            pool.value_scales[page, 0, place] = values[:, place].abs().cuda()
+        else:
+            pool.keys[page, 0, place] = keys[:, place].to(pool.dtype).cuda()
+            pool.values[page, 0, place] = values[:, place, None].to(pool.dtype).cuda().expand(64, 128)
+    comm.cache_attention(**a.args(scale=1.0))
+    torch.cuda.synchronize()
+    want = ((w - first.double() - second.double()) / (2 + w))[:, None]
+    off = 40 * 2.0 ** -24 / (2 + w)[:, None] + torch.zeros((64, group * 128))
+    got = a.out[0].cpu().flatten(1)
+    if out == "e4m3":  # one value a block: the largest, which is 448 scales
+        got = got.double().sign() * 448 * a.out_scales[0].cpu().double().t().repeat_interleave(128, 1)
+        off = off + 2.0 ** -24 * want.abs()
+    else:
+        off = off + block_ref.HALF_STEP[a.dtype] * (want.abs() + off) + block_ref.HALF_LEAST[a.dtype]
+    bad = (got.double() - want).abs() > off
+    worst = float(((got.double() - want).abs() * (2 + w)[:, None]).max() * 2 ** 24)
+    assert not bad.any(), f"{int(bad.sum())} of {bad.numel()} off, the most {worst:.1f} steps"
+
+
 @pytest.mark.parametrize("dtype,cache", [("bf16", None), ("fp16", None), ("fp32", None), ("bf16", "e4m3"),
                                          ("fp32", "e4m3")])
 def test_scores_that_grow(comm, dtype, cache):
