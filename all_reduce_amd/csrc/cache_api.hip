@@ -83,6 +83,22 @@ bool add_pair(Ranges *mem, const void *a, const void *b, size_t bytes, size_t in
     return mem->add(a, bytes, true) && mem->add(b, bytes, true);
 }
 
+// The steps of 2^shift tokens of sequences whose lengths are known, for `choose`.
+struct TotalSteps {
+    uint32_t all;
+};
+TotalSteps total_steps(const int32_t *lengths, size_t seqs, size_t capacity, size_t window, uint32_t shift,
+                       uint32_t most)
+{
+    TotalSteps t = {0};
+    for (size_t i = 0; i < seqs; ++i) {
+        uint32_t first, end;
+        attended(lengths[i], capacity, window, &first, &end);
+        t.all += std::min(steps_of(first, end, shift), most);
+    }
+    return t;
+}
+
 struct Copy {
     const void *const *rows[2];
     const void *const *pages[2];
@@ -291,6 +307,20 @@ arResult_t arCacheAttentionWorkspace(size_t dim, size_t group, arComm_t comm, si
     return arSuccess;
 }
 
+// For tests, on the host: whether a call whose lengths are known loads keys and values past the
+// caches.
+int ar_cache_attention_streams(const int32_t *lengths, size_t seqs, size_t capacity, size_t window,
+                               uint32_t queries, uint32_t tokens, uint32_t ranks, uint32_t heads,
+                               uint32_t group, uint32_t grid, uint32_t token_bytes)
+{
+    const uint32_t passes = passes_of_a_step(seqs, ranks, heads, group, tokens,
+                                             most_attended(capacity, window));
+    const CacheCall call = {(uint32_t)seqs, ranks, heads, group, queries, tokens, passes, grid, token_bytes};
+    TotalSteps steps;
+    return choose(call, [&](uint32_t shift, uint32_t most) { return total_steps(lengths, seqs, capacity, window, shift, most); },
+                  &steps).stream;
+}
+
 // For tests, on the host: the pieces of the share of team `team` of workgroup `block`
 // of an attention whose lengths are known, as the kernel walks them (cache_plan.hpp).
 // 2^queries and 2^tokens are a wave's.  Thirteen numbers a piece: rank, sequence,
@@ -307,27 +337,13 @@ size_t ar_cache_attention_share(const int32_t *lengths, size_t seqs, size_t capa
     uint32_t first, end;
     const uint32_t passes = passes_of_a_step(seqs, ranks, heads, group, tokens,
                                              most_attended(capacity, window));
-    CacheTeams t(group, queries, tokens, passes, false);
-    auto sum_up = [&](uint32_t shift, uint32_t of_one) {
-        uint32_t all = 0;
-        for (size_t i = 0; i < seqs; ++i) {
-            attended(lengths[i], capacity, window, &first, &end);
-            all += std::min(steps_of(first, end, shift), of_one);
-        }
-        return all;
-    };
-    const uint32_t per = ranks * heads * t.tiles;
-    bool alone = false;
-    if ((uint32_t)seqs * per > grid) {
-        const uint32_t tiles = sum_up(tokens, 1u << 12);
-        alone = waves_alone(tiles, (uint32_t)seqs);
-        if (alone)
-            t = CacheTeams(group, queries, tokens, passes + passes_alone(tiles, (uint32_t)seqs), true);
-    } else {
-        const uint32_t more = passes_to_try(sum_up(t.shift, ~0u), (uint32_t)seqs, per, grid);
-        if (more != 0 && sum_up(t.shift + more, ~0u) * per <= grid)
-            t.shift += more;
-    }
+    const CacheCall call = {(uint32_t)seqs, ranks, heads, group, queries, tokens, passes, grid, 0};
+    TotalSteps steps_of_all;
+    const CacheChoice choice =
+        choose(call, [&](uint32_t shift, uint32_t most) { return total_steps(lengths, seqs, capacity, window, shift, most); },
+               &steps_of_all);
+    const CacheTeams &t = choice.teams;
+    const bool alone = choice.alone;
     const uint32_t across = heads * t.tiles;
     auto steps_at = [&](size_t i) {
         attended(lengths[i], capacity, window, &first, &end);

@@ -494,17 +494,19 @@ void cache_attend(CacheAttentionArgs p)
     const uint32_t chunk = (p.seqs + kAttendThreads - 1u) / kAttendThreads;
     const uint32_t from = small ? lane : threadIdx.x * chunk;
     const uint32_t to = small ? lane + 1u : from + chunk;
-    uint32_t mine, before;  // steps of the lane's sequences (of one unit), and of those before
-    // The steps of 2^shift tokens, `most` of a sequence at most, of all sequences.
-    auto sum_up = [&](uint32_t shift, uint32_t most) {
-        mine = 0;
+    // Steps of all sequences (of one unit each), of the lane's, and of those before.
+    struct Steps {
+        uint32_t all, mine, before;
+    };
+    auto sum_up = [&](uint32_t shift, uint32_t most) {  // of 2^shift tokens, `most` of a sequence at most
+        uint32_t mine = 0;
         for (uint32_t s = from; s < to && s < p.seqs; ++s) {
             uint32_t first, end;
             attended(small ? lane_length : p.lengths[s], capacity, p.window, &first, &end);
             const uint32_t steps = steps_of(first, end, shift);
             mine += steps < most ? steps : most;
         }
-        before = scan64(mine);
+        uint32_t before = scan64(mine);
         uint32_t all = __builtin_amdgcn_readlane(before, 63);
         before -= mine;
         if (!small) {
@@ -519,34 +521,14 @@ void cache_attend(CacheAttentionArgs p)
             }
             all = uniform(all);
         }
-        return all;
+        return Steps{all, mine, before};
     };
-    CacheTeams teams(group, X::kQueryShift, X::kTokenShift, p.passes, false);
-    const uint32_t per = p.nranks * p.cache.heads * teams.tiles;  // units of a sequence
-    bool alone = false;
-    uint32_t all;
-    if (p.seqs * per > gridDim.x) {
-        // (4096 tiles of a sequence say enough of how long it is)
-        all = sum_up(X::kTokenShift, 1u << 12);
-        alone = waves_alone(all, p.seqs);
-        if (alone)
-            teams = CacheTeams(group, X::kQueryShift, X::kTokenShift,
-                               p.passes + passes_alone(all, p.seqs), true);
-        all = sum_up(teams.shift, ~0u);
-    } else {
-        all = sum_up(teams.shift, ~0u);
-        const uint32_t more = passes_to_try(all, p.seqs, per, gridDim.x);
-        if (more != 0) {
-            const uint32_t mine0 = mine, before0 = before, fewer = sum_up(teams.shift + more, ~0u);
-            if (fewer * per <= gridDim.x) {
-                teams.shift += more;
-                all = fewer;
-            } else {
-                mine = mine0;
-                before = before0;
-            }
-        }
-    }
+    const CacheCall call = {p.seqs,          p.nranks,       p.cache.heads, group, X::kQueryShift, X::kTokenShift,
+                            p.passes, gridDim.x, dim * 2u * X::kBytes};
+    Steps sums;
+    const CacheChoice choice = choose(call, sum_up, &sums);
+    const CacheTeams &teams = choice.teams;
+    const bool alone = choice.alone;
     auto steps_in = [&](uint32_t first, uint32_t end) { return steps_of(first, end, teams.shift); };
     auto steps_at = [&](int32_t length) {
         uint32_t first, end;
@@ -554,16 +536,8 @@ void cache_attend(CacheAttentionArgs p)
         return steps_in(first, end);
     };
     const uint32_t across = p.cache.heads * teams.tiles;  // units of a sequence and rank
-    const uint32_t row = all * across;  // steps of a rank
-    mine *= across;
-    before *= across;
-    // Non-temporal loads where all keys and values together are more than half of the
-    // last-level cache, which would not keep them: 64 x 8192 tokens x 8 ranks take 321
-    // in place of 355 us, but 256 of 67 tokens (70 MB, which the cache holds) 35 in place
-    // of 31.  Not where waves read the same tokens: 136 in place of 117 us for 32 windows
-    // of 4096 tokens x 4 ranks and 32 query heads of 256.
-    const uint64_t tokens = (uint64_t)row * p.nranks << teams.shift;
-    const bool stream = teams.side == 1u && tokens * dim * (2u * X::kBytes) >= (uint64_t)128 << 20;
+    const uint32_t row = sums.all * across;  // steps of a rank
+    const uint32_t mine = sums.mine * across, before = sums.before * across;
     const CachePlan plan(row * p.nranks, alone ? gridDim.x * kAttendWaves : gridDim.x);
     const uint32_t team = alone ? wave : 0u;
     const uint32_t share = plan.share(blockIdx.x, team, gridDim.x);
@@ -1028,7 +1002,7 @@ void cache_attend(CacheAttentionArgs p)
             meet();  // the sums in LDS are read before the next piece's are written
         }
     };
-    if (stream)
+    if (choice.stream)
         pieces(std::true_type{});
     else
         pieces(std::false_type{});

@@ -139,6 +139,75 @@ __host__ __device__ inline uint32_t passes_to_try(uint32_t steps, uint32_t seqs,
     return all > 4u * teams ? 3u : all > 2u * teams ? 2u : 1u;
 }
 
+// What the teams' sharing depends on besides the lengths.
+struct CacheCall {
+    uint32_t seqs, ranks, heads, group;
+    uint32_t queries, tokens;  // 2^queries and 2^tokens are a wave's
+    uint32_t passes;           // of a step, at least (passes_of_a_step)
+    uint32_t grid;
+    uint32_t token_bytes;      // of a key and a value of a head
+};
+
+// Whether keys and values of `tokens` tokens of all sequences together are loaded past the
+// caches (non-temporal loads): where they are more than half of the last-level cache, which
+// would not keep them.  64 x 8192 tokens x 8 ranks, 8 query heads of 128, take 321 in place of
+// 355 us, but 256 of 67 tokens (70 MB, which the cache holds) 23.4 in place of 21.3, and 128 of
+// 200 (105 MB) 34.3 in place of 29.8.  Not where several waves or units read the same tokens
+// for other query heads: 136 in place of 117 us for 32 windows of 4096 tokens x 4 ranks and
+// 32 query heads of 256 as two waves, 120.5 in place of 118.2 for 256 of 200 tokens x 8 ranks
+// and 64 of 128 as two units.
+__host__ __device__ inline bool streamed(const CacheCall &c, const CacheTeams &teams, uint64_t tokens)
+{
+    return teams.side == 1u && teams.tiles == 1u &&
+           tokens * c.ranks * c.heads * c.token_bytes >= (uint64_t)128 << 20;
+}
+
+// How a call's waves share its work, from the lengths.  `sum_up(shift, most)` gives the steps of
+// 2^shift tokens of all sequences (of one unit each), `most` of a sequence at most, as its
+// member `all`, with whatever else it finds; that of the steps chosen is left in `steps`.
+struct CacheChoice {
+    CacheTeams teams;
+    bool alone;   // each wave is a team
+    bool stream;
+};
+
+template <typename SumUp, typename Steps>
+__host__ __device__ inline CacheChoice choose(const CacheCall &c, SumUp sum_up, Steps *steps)
+{
+    CacheTeams teams(c.group, c.queries, c.tokens, c.passes, false);
+    const uint32_t per = c.ranks * c.heads * teams.tiles;  // units of a sequence
+    // Whole steps and tiles bound the tokens, which are summed up only where that is not enough.
+    // (As many of a sequence as leave the sum 32 bits.)
+    auto stream_of = [&](uint64_t bound) {
+        uint32_t most = 0x80000000u;
+        for (uint32_t n = 1; n < c.seqs; n *= 2u)
+            most /= 2u;
+        return streamed(c, teams, bound) && streamed(c, teams, sum_up(0u, most).all);
+    };
+    bool alone = false, stream;
+    if (c.seqs * per > c.grid) {
+        // (so many tiles of a sequence say enough of how long it is)
+        const uint32_t tiles = sum_up(c.tokens, 0xffffu).all;
+        alone = waves_alone(tiles, c.seqs);
+        if (alone)
+            teams = CacheTeams(c.group, c.queries, c.tokens, c.passes + passes_alone(tiles, c.seqs), true);
+        stream = stream_of((uint64_t)tiles << c.tokens);
+        *steps = sum_up(teams.shift, ~0u);
+    } else {
+        *steps = sum_up(teams.shift, ~0u);
+        stream = stream_of((uint64_t)steps->all << teams.shift);
+        const uint32_t more = passes_to_try(steps->all, c.seqs, per, c.grid);
+        if (more != 0) {
+            const Steps fewer = sum_up(teams.shift + more, ~0u);
+            if (fewer.all * per <= c.grid) {
+                teams.shift += more;
+                *steps = fewer;
+            }
+        }
+    }
+    return {teams, alone, stream};
+}
+
 // The smallest power of two of passes to a step (as its exponent) with which all steps
 // of a call can be counted in 31 bits whatever its lengths are: 0, but for calls of
 // extreme sizes.  With at most 2^24 units it is at most 20, and no step more than 2^30

@@ -165,3 +165,47 @@ def test_places():
             assert (at[0], at[1]) == divmod(slot, page), (page, slot)
         for slot in (-1, -2 ** 40, pages * page, 2 ** 31, 2 ** 32 + 1, 2 ** 63 - 1):
             assert fn(pages, page, slot, at) == 0
+
+
+def streams(lengths, ranks, heads, group, token_bytes, queries=4, tokens=5, grid=512, window=0, capacity=2 ** 31 - 1):
+    fn = ar.library().ar_cache_attention_streams
+    fn.restype = ctypes.c_int
+    fn.argtypes = [ctypes.POINTER(I32), SZ, SZ, SZ] + [U32] * 7
+    return fn((I32 * len(lengths))(*lengths), len(lengths), capacity, window, queries, tokens, ranks, heads, group, grid,
+              token_bytes)
+
+
+def test_streamed_loads_go_by_the_cache_that_is_read():
+    """Loads past the caches from 128 MiB of keys and values on, whatever the length of a step
+    is: 512 bytes a token are heads of 128 in 16 bits."""
+    assert not streams([67] * 256, 8, 1, 8, 512)       # 67 MiB
+    assert not streams([33] * 256, 8, 1, 8, 512)
+    assert not streams([200] * 128, 8, 1, 8, 512)      # 100 MiB
+    assert not streams([1] * 4096, 8, 1, 8, 512)       # 16 MiB, in tiles of 32 tokens 512
+    assert streams([8192] * 64, 8, 1, 8, 512)
+    assert not streams([8192] * 64, 8, 1, 8, 512, window=127)
+    assert streams([8192] * 64, 8, 1, 8, 512, window=1024)
+    assert streams([131072], 8, 1, 8, 256) and not streams([131072], 1, 1, 8, 256)
+    assert streams([2 ** 31 - 1], 1, 1, 1, 32) and streams([2 ** 31 - 1] + [1] * 600, 1, 1, 1, 512)
+    assert not streams([5] * 65536, 1, 1, 1, 32)
+    # waves or units that read the same tokens for other query heads
+    assert streams([8192] * 64, 8, 1, 32, 512, queries=5) and not streams([8192] * 64, 8, 1, 33, 512, queries=5)
+    assert streams([250] * 600, 8, 1, 16, 512) and not streams([250] * 600, 8, 1, 17, 512)
+
+
+def test_drawn_streamed_loads():
+    """Tokens decide, on both sides of 128 MiB, for every choice of teams and steps."""
+    rng = random.Random(6)
+    seen = set()
+    for _ in range(400):
+        seqs, ranks, heads, tokens = rng.choice([1, 3, 20, 64, 65, 300, 2000]), rng.choice([1, 2, 8]), rng.choice([1, 4]), \
+            rng.choice([4, 5])
+        token_bytes = rng.choice([32, 256, 512, 1024, 2048])
+        limit = (1 << 27) / (token_bytes * ranks * heads)  # tokens
+        share = [rng.random() ** 2 + 0.01 for _ in range(seqs)]
+        share = [x / sum(share) for x in share]
+        lengths = [min(2 ** 21, max(1, int(x * limit * rng.choice([0.5, 0.9, 1.1, 2.0])))) for x in share]
+        want = sum(lengths) * ranks * heads * token_bytes >= 1 << 27
+        assert streams(lengths, ranks, heads, 8, token_bytes, tokens=tokens, grid=rng.choice([64, 256, 512])) == want
+        seen.add((want, seqs * ranks * heads > 512))
+    assert len(seen) == 4

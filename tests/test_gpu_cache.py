@@ -339,6 +339,27 @@ def test_attention_of_many_sequences(comm, seqs, longest, ranks, group, dim, dty
     a.check(seqs=sorted({0, 1, seqs // 3, seqs - 1, *torch.randint(seqs, (40 // ranks + 2,), generator=gen).tolist()}))
 
 
+@pytest.mark.parametrize("ranks,seqs,tokens,heads,group,dim,dtype,cache", [
+    # teams of four waves
+    (4, 30, 3001, 1, 8, 128, "bf16", None), (8, 30, 3001, 1, 8, 128, "fp16", "e4m3"), (1, 40, 3303, 4, 5, 80, "fp16", None),
+    (2, 30, 5501, 1, 20, 128, "bf16", None), (2, 70, 1201, 1, 16, 256, "bf16", None), (2, 70, 3001, 1, 7, 208, "bf16", "e4m3"),
+    (1, 20, 4001, 2, 3, 128, "fp32", None), (1, 17, 5003, 1, 2, 256, "fp32", None), (4, 30, 5501, 2, 24, 64, "fp32", "e4m3"),
+    (4, 30, 6001, 1, 9, 64, "bf16", None),
+    # waves alone
+    (8, 400, 100, 1, 8, 128, "bf16", None), (8, 300, 250, 2, 20, 128, "bf16", "e4m3"), (2, 700, 120, 2, 1, 128, "fp32", None),
+])
+def test_attention_of_more_than_the_caches_hold(comm, ranks, seqs, tokens, heads, group, dim, dtype, cache):
+    """More than 128 MiB of keys and values, which are loaded past the caches."""
+    gen = torch.Generator().manual_seed(tokens)
+    n = (tokens - (0.2 * tokens * torch.rand(seqs, generator=gen)).int()).tolist()
+    a = Attend(ranks, n, heads, group, dim, 64, dtype, cache)
+    bytes_ = 2 * ranks * sum(n) * heads * dim * DT[cache or dtype].itemsize
+    note(f"attention of {bytes_ >> 20} MiB R={ranks} {seqs} x {tokens} {heads} x {group} x {dim} {dtype} {cache}")
+    assert bytes_ >= 1 << 27
+    comm.cache_attention(**a.args())
+    a.check(ranks=[0, ranks - 1], seqs=sorted({0, seqs - 1, seqs // 2}))
+
+
 @pytest.mark.parametrize("dtype,cache", [("bf16", None), ("fp16", None), ("fp32", None), ("bf16", "e4m3"),
                                          ("fp32", "e4m3")])
 def test_attention_of_a_long_sequence(comm, dtype, cache):
