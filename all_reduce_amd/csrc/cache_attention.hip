@@ -5,17 +5,23 @@
 namespace ar {
 
 // Counters, in the same place whatever call uses the workspace, then two slots a team.
-// (A wave that is a team has at most 32 queries, four together at most 128.)
 uint64_t cache_attention_counters(int cu_count)
 {
     return (uint64_t)attend_most(2, cu_count) * kAttendWaves * 4u * sizeof(uint32_t);
 }
 
+// (A wave that is a team has at most 32 queries, four together at most 128.  Heads above 128
+// have half the workgroups, and a little less than twice as many floats a query.)
 uint64_t cache_attention_workspace(uint32_t dim, uint32_t group, int cu_count)
 {
     const uint32_t dp = padded_dim(dim), queries = group < 32u ? group : 32u;
-    const uint64_t teams = (uint64_t)attend_most(dp == 256 ? 1 : 2, cu_count) * kAttendWaves;
-    return cache_attention_counters(cu_count) + teams * 2u * queries * (dp + 2u) * sizeof(float);
+    auto floats = [&](int per_cu, uint32_t padded) {
+        return (uint64_t)attend_most(per_cu, cu_count) * kAttendWaves * 2u * queries * (padded + 2u);
+    };
+    uint64_t most = floats(2, dp < 128 ? dp : 128);
+    if (dp == 256 && floats(1, dp) > most)
+        most = floats(1, dp);
+    return cache_attention_counters(cu_count) + most * sizeof(float);
 }
 
 // 16 query heads a wave, or 32 where a key-value head has more: the keys and values in

@@ -763,6 +763,25 @@ def test_one_workspace_for_calls_in_order(comm):
         a.check(seqs=range(0, len(a.lengths), 1 + len(a.lengths) // 40))
 
 
+def test_a_workspace_serves_fewer_of_either(comm):
+    """Its size never falls as dim or group grows, and a call of a smaller dim runs in one that
+    was made for a larger."""
+    note("attention, workspaces of larger dims")
+    sizes = [[ar.arCacheAttentionWorkspace(dim, group, comm.handle) for group in (1, 2, 7, 8, 16, 17, 32, 33, 64, 4096)]
+             for dim in range(16, 257, 16)]
+    assert all(r == 0 for row in sizes for r, _ in row)
+    for row in sizes:
+        assert all(a <= b for (_, a), (_, b) in zip(row, row[1:]))
+    for row, following in zip(sizes, sizes[1:]):
+        assert all(a <= b for (_, a), (_, b) in zip(row, following))
+    for group in (8, 40):
+        work = comm.cache_workspace(256, group)
+        for dim in (64, 80, 128):
+            a = Attend(1, [9000, 5], 1, group, dim, 16, "bf16")
+            comm.cache_attention(**a.args(workspace=work))
+            a.check()
+
+
 def test_shared_pages(comm):
     """Sequences with a common prefix in the same pages, keys that are the values too."""
     note("attention over shared pages")
