@@ -12,6 +12,7 @@ anything.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from enum import IntEnum
 from pathlib import Path
@@ -76,6 +77,7 @@ class arActivation(IntEnum):
 AR_SCALE_BLOCK = 128
 AR_NORM_MAX_COLS = 32768
 AR_CACHE_MAX_DIM = 256
+AR_CACHE_WORKSPACE_ZEROS = 65536
 
 AR_MAX_RANKS = 32
 AR_NOALLOC_SCRATCH_BYTES = 64 << 20
@@ -713,8 +715,10 @@ class Comm:
         r, n = arCacheAttentionWorkspace(dim, group, self.handle)
         if r != 0:
             raise ArError(r, "arCacheAttentionWorkspace")
-        with torch.cuda.stream(torch.cuda.current_stream(self.device) if stream is None else stream):
-            return torch.zeros(n, dtype=torch.uint8, device=self.device)
+        with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+            work = torch.empty(n, dtype=torch.uint8, device=self.device)
+            work[:AR_CACHE_WORKSPACE_ZEROS].zero_()
+        return work
 
     @staticmethod
     def _rows(tensors, name):

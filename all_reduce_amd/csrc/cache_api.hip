@@ -282,7 +282,7 @@ arResult_t arCacheAttention(const void *const *queries, size_t queryStride,
     args.table_pages = tablePages;
     args.window = window;
     args.work = (char *)workspace;
-    args.slots = (float *)((char *)workspace + cache_attention_counters(comm->cu_count));
+    args.slots = (float *)((char *)workspace + AR_CACHE_WORKSPACE_ZEROS);
     args.seqs = (uint32_t)seqs;
     args.heads = (uint32_t)heads;
     args.group = (uint32_t)(heads / cache->heads);

@@ -5,11 +5,6 @@
 namespace ar {
 
 // Counters, in the same place whatever call uses the workspace, then two slots a team.
-uint64_t cache_attention_counters(int cu_count)
-{
-    return (uint64_t)attend_most(2, cu_count) * kAttendWaves * 4u * sizeof(uint32_t);
-}
-
 // (A wave that is a team has at most 32 queries, four together at most 128.  Heads above 128
 // have half the workgroups, and a little less than twice as many floats a query.)
 uint64_t cache_attention_workspace(uint32_t dim, uint32_t group, int cu_count)
@@ -21,7 +16,7 @@ uint64_t cache_attention_workspace(uint32_t dim, uint32_t group, int cu_count)
     uint64_t most = floats(2, dp < 128 ? dp : 128);
     if (dp == 256 && floats(1, dp) > most)
         most = floats(1, dp);
-    return cache_attention_counters(cu_count) + most * sizeof(float);
+    return AR_CACHE_WORKSPACE_ZEROS + most * sizeof(float);
 }
 
 // 16 query heads a wave, or 32 where a key-value head has more: the keys and values in

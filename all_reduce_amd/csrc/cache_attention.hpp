@@ -1008,8 +1008,13 @@ void cache_attend(CacheAttentionArgs p)
         pieces(std::false_type{});
 }
 
-// Workgroups of a launch at most: what fits the compute units at once.
-inline uint32_t attend_most(int per_cu, int cu_count) { return (uint32_t)(per_cu * cu_count) / 8u * 8u; }
+// Workgroups of a launch at most: what fits the compute units at once (of 512 at most: the
+// workspace's counters have room for so many).
+inline uint32_t attend_most(int per_cu, int cu_count)
+{
+    static_assert(2 * 512 * kAttendWaves * 4 * sizeof(uint32_t) <= AR_CACHE_WORKSPACE_ZEROS, "four counters a team");
+    return (uint32_t)(per_cu * (cu_count < 512 ? cu_count : 512)) / 8u * 8u;
+}
 
 template <typename T, bool EIGHT, int DP, int QT, bool EXACT, bool EIGHT_OUT>
 hipError_t enqueue_attend(CacheAttentionArgs args, int cu_count, hipStream_t stream)

@@ -97,9 +97,8 @@ hipError_t launch_cache_read(const CacheCopyArgs &args, int dtype, bool eight, i
                              int cu_count, hipStream_t stream);
 hipError_t launch_cache_attention(const CacheAttentionArgs &args, int dtype, bool eight,
                                   bool eight_out, int cu_count, hipStream_t stream);
-// Bytes of workspace for heads of `dim`, `group` query heads to a key-value head, and
-// of the counters it begins with.
+// Bytes of workspace for heads of `dim`, `group` query heads to a key-value head: counters
+// (AR_CACHE_WORKSPACE_ZEROS), then partial sums.
 uint64_t cache_attention_workspace(uint32_t dim, uint32_t group, int cu_count);
-uint64_t cache_attention_counters(int cu_count);
 
 }  // namespace ar

@@ -42,6 +42,8 @@ extern "C" {
 
 /* The widest head. */
 #define AR_CACHE_MAX_DIM 256
+/* What has to be zero of a workspace before its first use: its first bytes. */
+#define AR_CACHE_WORKSPACE_ZEROS 65536
 
 /* How keys and values lie in their pages: element (p, h, o, d) of page p, head
  * h, place o is at p * pageStride + h * headStride + o * tokenStride + d.  The
@@ -134,9 +136,10 @@ arResult_t arCacheRead(const int64_t *slots, size_t tokens, const arCacheLayout_
  *               arUnsupported; arGateQuant quantises other outputs).
  *  lse          host array of nranks device pointers [seqs][heads], or NULL.
  *  workspace    device memory of at least the bytes that arCacheAttentionWorkspace
- *               names for this dim and heads / cache->heads, zeros before its first
- *               use; every call leaves it fit for the next.  One call at a time may
- *               use it: calls that may run at once, in graphs as well, need one each.
+ *               names for this dim and heads / cache->heads, its first
+ *               AR_CACHE_WORKSPACE_ZEROS zero before its first use; every call leaves it
+ *               fit for the next.  One call at a time may use it: calls that may run at
+ *               once, in graphs as well, need one each.
  *  seqs         at most 65536, and seqs * heads * nranks at most 2^24 (else
  *               arUnsupported).
  * Rules (arInvalidArgument when broken): no NULL pointer but those named; every

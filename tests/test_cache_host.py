@@ -227,3 +227,7 @@ def test_workspace_query_refusals():
     assert ar.arCacheAttentionWorkspace(100, 8, None)[0] == ar.arResult.arUnsupported
     assert ar.arCacheAttentionWorkspace(128, 0, None)[0] == ar.arResult.arUnsupported
     assert ar.arCacheAttentionWorkspace(128, 8, None)[0] == ar.arResult.arInvalidArgument
+
+
+def test_zeros_of_a_workspace_match_the_header():
+    assert int(re.search(r"#define AR_CACHE_WORKSPACE_ZEROS (\d+)", HEADER).group(1)) == ar.AR_CACHE_WORKSPACE_ZEROS

@@ -782,6 +782,19 @@ def test_a_workspace_serves_fewer_of_either(comm):
             a.check()
 
 
+@pytest.mark.parametrize("dtype,cache,group,dim", [("bf16", None, 8, 128), ("fp32", "e4m3", 40, 64), ("fp16", None, 3, 256)])
+def test_only_the_first_bytes_of_a_workspace_are_zero(comm, dtype, cache, group, dim):
+    """The rest is NaN: partial sums are read where a team of the same call has written."""
+    note(f"attention, a workspace of NaN behind its zeros {dtype} {cache} {group} x {dim}")
+    work = torch.full((ar.arCacheAttentionWorkspace(dim, group, comm.handle)[1],), 0xFF, dtype=torch.uint8, device="cuda:0")
+    work[:ar.AR_CACHE_WORKSPACE_ZEROS] = 0
+    for lengths in ([70000], [5, 900, 9000, 0, 33], [200] * 300, [9000]):
+        a = Attend(1, lengths, 1, group, dim, 16, dtype, cache)
+        comm.cache_attention(**a.args(workspace=work))
+        a.check(seqs=range(0, len(lengths), 1 + len(lengths) // 10))
+        assert not work[:ar.AR_CACHE_WORKSPACE_ZEROS].any()
+
+
 def test_shared_pages(comm):
     """Sequences with a common prefix in the same pages, keys that are the values too."""
     note("attention over shared pages")
