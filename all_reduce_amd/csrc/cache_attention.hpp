@@ -633,24 +633,19 @@ void cache_attend(CacheAttentionArgs p)
             uint32_t t0 = first + (step0 << teams.shift) + behind * X::kTokens;
             const uint32_t tend = mine0 < queries ? t1 : 0u;  // a wave without queries has no tokens
 
-            // page and place of the lane's token of the tile at t (past the end: none)
+            // page and place of the lane's token of the tile at t (past the end: of the last one)
             auto look = [&](uint32_t t, uint32_t &place) {
                 t += mine_at;
-                int32_t page = -1;
-                place = 0;
-                if (t < t1) {
-                    const uint32_t i = p.cache.page_of(t);
-                    place = t - i * p.cache.page_tokens;
-                    page = table[i];
-                }
-                return page;
+                t = t < t1 ? t : t1 - 1u;
+                const uint32_t i = p.cache.page_of(t);
+                place = t - i * p.cache.page_tokens;
+                return table[i];
             };
             float scale_next = 0.0f;
-            // The rows of the tile at t to LDS.  A token without a place stands for the cache's
-            // first one.
-            auto rows = [&](uint32_t t, int32_t page, uint32_t place) {
+            // A tile's rows to LDS.  (A page that is none: the cache's first row, and NaN in the end.)
+            auto rows = [&](int32_t page, uint32_t place) {
                 if ((uint32_t)page >= p.cache.pages) {
-                    bad = bad || t + mine_at < t1;
+                    bad = true;
                     page = 0;
                     place = 0;
                 }
@@ -689,7 +684,7 @@ void cache_attend(CacheAttentionArgs p)
             if (t0 < tend) {
                 uint32_t place, place_next;
                 int32_t page = look(t0, place), page_next = look(t0 + teams.pass, place_next);
-                rows(t0, page, place);
+                rows(page, place);
                 if constexpr (QT == 1) {
                     find_keys();
                     find_values();
@@ -710,7 +705,7 @@ void cache_attend(CacheAttentionArgs p)
                             }
                         __builtin_amdgcn_wave_barrier();
                     }
-                    rows(t0 + teams.pass, page_next, place_next);
+                    rows(page_next, place_next);
                     page_next = look(t0 + 2 * teams.pass, place_next);
                     f32x4 s[QT][X::kGroups];
                     x.scores(s);

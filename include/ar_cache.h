@@ -114,7 +114,8 @@ arResult_t arCacheRead(const int64_t *slots, size_t tokens, const arCacheLayout_
  * infinity makes lse one, NaN beside a NaN, and out NaN.
  * The order of a sum follows from the sizes, the lengths and the card's number of
  * compute units, never from values or from other calls.  Only tokens first .. n - 1
- * and the table's entries for them are read, whatever the other places hold.
+ * and the table's entries for them are read, whatever the other places hold (and place 0
+ * of page 0, for a page number that is none).
  *
  * n = 0 gives zeros and lse -infinity.  A length that is negative or above
  * tablePages * pageTokens, and a page number of a token that is none of the
