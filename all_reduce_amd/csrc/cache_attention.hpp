@@ -366,7 +366,8 @@ struct Tile {
 // A matrix instruction's result is ready some issue slots after it, for which the
 // compiler fills in waits; of a branch that is taken in between it counts too few
 // (binary32 scores read behind one came out with old values in their last register).
-// So no branch follows such instructions before these waits.
+// So no branch follows such instructions before these waits.  (A test follows the paths
+// through the built code.)
 __device__ inline void matrix_done()
 {
     __builtin_amdgcn_sched_barrier(0);
@@ -776,8 +777,11 @@ void cache_attend(CacheAttentionArgs p)
                             }
                     }
                     x.accumulate(w);
+                    if constexpr (!EXACT)  // (whose loads have branches)
+                        matrix_done();
                     load_values();
-                    matrix_done();
+                    if constexpr (EXACT)
+                        matrix_done();
                 }
             }
 
