@@ -324,6 +324,23 @@ def test_attention(comm, ranks, lengths, heads, group, dim, page, dtype, cache, 
     a.check(window=window)
 
 
+# Heads that leave lanes without a part of the row, in every type and number of queries a wave.
+NARROWER = [(dtype, cache, dim, group, order)
+            for dtype, cache in (("bf16", None), ("fp16", None), ("fp32", None), ("bf16", "e4m3"), ("fp16", "e4m3"), ("fp32", "e4m3"))
+            for dim, group, order in ((144, 3, "head"), (176, 16, "token"), (208, 20, "pair"), (240, 40, "head"),
+                                      (240, 8, "token"), (144, 32, "head"), (112, 24, "token"), (16, 18, "head"),
+                                      (48, 5, "pair"))]
+
+
+@pytest.mark.parametrize("dtype,cache,dim,group,order", NARROWER)
+def test_attention_of_heads_between(comm, dtype, cache, dim, group, order):
+    note(f"attention of heads of {dim}, {group} {dtype} {cache} {order}")
+    for lengths, heads, window in ((EDGES, 1, 0), ([5000, 37, 1200], 2, 0), ([3000, 400], 1, 777)):
+        a = Attend(1, lengths, heads, group, dim, 20, dtype, cache, order)
+        comm.cache_attention(**a.args(window=window))
+        a.check(window=window)
+
+
 @pytest.mark.parametrize("seqs,longest,ranks,group,dim", [
     (70, 300, 2, 4, 64), (300, 90, 1, 4, 64), (1500, 20, 1, 4, 64), (5000, 6, 1, 4, 64), (60, 200, 12, 3, 128),
     (600, 300, 1, 20, 64), (700, 40, 2, 70, 64), (400, 50, 2, 1, 256), (64, 100, 16, 16, 80), (65536, 1, 1, 1, 16)])
