@@ -210,8 +210,8 @@ __host__ __device__ inline CacheChoice choose(const CacheCall &c, SumUp sum_up, 
 
 // The smallest power of two of passes to a step (as its exponent) with which all steps
 // of a call can be counted in 31 bits whatever its lengths are: 0, but for calls of
-// extreme sizes.  With at most 2^24 units it is at most 20, and no step more than 2^30
-// tokens.
+// extreme sizes.  With at most 2^24 units it is at most 20 for waves of 32 tokens and 21 for
+// waves of 16, and no step, at most 2^5 times longer, is more than 2^30 tokens.
 inline uint32_t passes_of_a_step(uint64_t seqs, uint64_t ranks, uint64_t heads, uint32_t group,
                                  uint32_t tokens, uint64_t most_tokens)
 {

@@ -126,6 +126,22 @@ def test_steps_of_extreme_calls():
     assert pieces[-1][:5] == [31, 65535, 7, pieces[-1][3], steps]
 
 
+@pytest.mark.parametrize("tokens,length", [(4, 0), (4, 16), (4, 60), (4, 100), (4, 2 ** 31 - 1), (5, 1), (5, 100), (5, 200), (5, 2 ** 31 - 1)])
+def test_longest_steps(tokens, length):
+    """The same number of units for waves of 16 and 32 tokens, and for single waves, whose steps
+    are the longest."""
+    array = (I32 * 65536)(*[length] * 65536)
+    (waves, _, tiles, _, step), pieces = pieces_of(array, 2 ** 31 - 1, 0, 4, tokens, 32, 8, 1, 512, 511, 3 if length <= 200 else 0)
+    units = 65536 * 32 * 8 * tiles
+    steps = max(1, -(-length // step))
+    assert units == 2 ** 24 and units * steps < 2 ** 31 and step <= 2 ** 30
+    assert waves == (4 if length > 200 else 1)
+    if (tokens, length) in ((4, 100), (5, 200)):
+        assert step == 2 ** 30
+    assert pieces[-1][:3] == [31, 65535, 7] and pieces[-1][4:6] == [steps, steps]
+    assert pieces[-1][7] == length
+
+
 def test_parts():
     """What a group's and a unit's last team reads: every team's slot once, then the
     slot of every group's first."""
