@@ -15,10 +15,16 @@ typedef unsigned __int128 u128;
 
 constexpr size_t kMostHeads = 4096, kMostSeqs = 65536;
 
-// The layout in the kernels' form, and the elements from a pool's first to its
-// last.  Strides of which there is only one step do not count.
+// A step of a layout: blocks of `inner` elements from their first to their last,
+// `stride` apart.
+struct Step {
+    size_t count, stride, inner;
+};
+
+// The layout in the kernels' form, its steps, the innermost first, and the elements
+// from a pool's first to its last.  Strides of which there is only one step do not count.
 arResult_t check_layout(const arCacheLayout_t *c, size_t page_bytes, CacheShape *shape,
-                        size_t *span)
+                        Step (&steps)[3], size_t *span)
 {
     if (c == nullptr)
         return reject(arInvalidArgument, "NULL cache layout");
@@ -29,12 +35,13 @@ arResult_t check_layout(const arCacheLayout_t *c, size_t page_bytes, CacheShape 
     if (c->pages < 1 || c->pageTokens < 1 || c->pages > INT32_MAX || c->pageTokens > INT32_MAX ||
         c->pages * c->pageTokens > INT32_MAX)
         return reject(arInvalidArgument, "pages * pageTokens must be in 1..2^31 - 1");
-    struct Step {
-        size_t count, stride;
-    } steps[3] = {{c->pages, c->pageStride}, {c->heads, c->headStride}, {c->pageTokens, c->tokenStride}};
+    steps[0] = {c->pages, c->pageStride, 0};
+    steps[1] = {c->heads, c->headStride, 0};
+    steps[2] = {c->pageTokens, c->tokenStride, 0};
     std::sort(steps, steps + 3, [](const Step &a, const Step &b) { return a.stride < b.stride; });
     u128 extent = c->dim;
-    for (const Step &s : steps) {
+    for (Step &s : steps) {
+        s.inner = (size_t)extent;
         if (s.count == 1)
             continue;
         if (s.stride % (16 / page_bytes) != 0)
@@ -70,15 +77,23 @@ arResult_t check_rows(size_t rows, size_t row, size_t stride, int dtype, size_t 
     return arSuccess;
 }
 
-// The ranges of a rank's keys and values, written both, which may be parts of
-// the same blocks: `inner` bytes of each of `count` blocks `stride` apart.
-bool add_pair(Ranges *mem, const void *a, const void *b, size_t bytes, size_t inner, size_t stride,
-              size_t count)
+// The ranges of a rank's keys and values, written both, `bytes` each, which may lie next to
+// each other inside the blocks of a step (elements of `es` bytes): the values' parts then lie
+// behind the keys' or the other way round, and neither's reach into the next block, here or
+// in the steps around it.
+template <size_t N>
+bool add_pair(Ranges *mem, const void *a, const void *b, size_t bytes, const Step (&steps)[N], size_t es)
 {
     const uintptr_t lo = std::min((uintptr_t)a, (uintptr_t)b), hi = std::max((uintptr_t)a, (uintptr_t)b);
     const size_t apart = hi - lo;
-    if (lo != 0 && count > 1 && (lo & 15u) == 0 && (hi & 15u) == 0 && apart < bytes &&
-        apart >= inner && apart + inner <= stride)
+    bool beside = false;
+    for (const Step &s : steps) {
+        if (s.count == 1)
+            continue;
+        const bool inside = apart < s.stride * es && s.inner * es <= s.stride * es - apart;
+        beside = inside && (beside || apart >= s.inner * es);
+    }
+    if (beside && lo != 0 && (lo & 15u) == 0 && (hi & 15u) == 0)
         return mem->add((const void *)lo, apart + bytes, true);
     return mem->add(a, bytes, true) && mem->add(b, bytes, true);
 }
@@ -120,8 +135,9 @@ arResult_t copy(const Copy &c, bool write, size_t row_stride, const int64_t *slo
         return reject(arInvalidArgument, "scales of keys and of values, or of neither");
     const size_t page_bytes = eight ? 1 : elem_bytes(dtype);
     CacheCopyArgs args = {};
+    Step steps[3];
     size_t span, row_span;
-    arResult_t r = check_layout(cache, page_bytes, &args.cache, &span);
+    arResult_t r = check_layout(cache, page_bytes, &args.cache, steps, &span);
     if (r != arSuccess)
         return r;
     if (tokens == 0)
@@ -137,20 +153,17 @@ arResult_t copy(const Copy &c, bool write, size_t row_stride, const int64_t *slo
             return reject(arInvalidArgument, "NULL buffer array");
     Ranges mem;
     const size_t places = cache->pages * cache->pageTokens * cache->heads;
-    // what keys take of a page, if pages are the outermost step
-    const size_t page_span = span - (cache->pages - 1) * args.cache.page_stride;
+    const Step rows[1] = {{tokens, row_stride, row}};
     bool ok = mem.add(slots, tokens * sizeof(int64_t), false, 8);
     for (int i = 0; i < nranks && ok; ++i) {
         if (write) {
             ok = mem.add(c.rows[0][i], row_span * es, false) &&
                  mem.add(c.rows[1][i], row_span * es, false) &&
-                 add_pair(&mem, c.pages[0][i], c.pages[1][i], span * page_bytes,
-                          page_span * page_bytes, cache->pageStride * page_bytes, cache->pages);
+                 add_pair(&mem, c.pages[0][i], c.pages[1][i], span * page_bytes, steps, page_bytes);
         } else {
             ok = mem.add(c.pages[0][i], span * page_bytes, false) &&
                  mem.add(c.pages[1][i], span * page_bytes, false) &&
-                 add_pair(&mem, c.rows[0][i], c.rows[1][i], row_span * es, row * es,
-                          row_stride * es, tokens);
+                 add_pair(&mem, c.rows[0][i], c.rows[1][i], row_span * es, rows, es);
         }
         for (int k = 0; k < 2 && eight && ok; ++k)
             ok = mem.add(c.scales[k][i], places * sizeof(float), write);
@@ -217,8 +230,9 @@ arResult_t arCacheAttention(const void *const *queries, size_t queryStride,
         return reject(arInvalidArgument, "scales of keys and of values, or of neither");
     const size_t es = elem_bytes(dtype), page_bytes = eight ? 1 : es;
     CacheAttentionArgs args = {};
+    Step steps[3];
     size_t span, q_span;
-    arResult_t r = check_layout(cache, page_bytes, &args.cache, &span);
+    arResult_t r = check_layout(cache, page_bytes, &args.cache, steps, &span);
     if (r != arSuccess)
         return r;
     if (heads < 1 || heads > kMostHeads || heads % cache->heads != 0)

@@ -48,7 +48,7 @@ extern "C" {
 /* How keys and values lie in their pages: element (p, h, o, d) of page p, head
  * h, place o is at p * pageStride + h * headStride + o * tokenStride + d.  The
  * same for keys and values and for every rank.  Keys and values may be in one
- * allocation, next to each other inside each page. */
+ * allocation, next to each other inside each page, head or token. */
 typedef struct {
     size_t pages;
     size_t pageTokens;  /* places of a page; pages * pageTokens < 2^31 */

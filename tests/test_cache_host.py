@@ -83,6 +83,24 @@ CASES = [
      "arInvalidArgument", "overlaps"),
     ("write pairs past the page", W, dict(WRITE, cache=layout(pageStride=8176), value_pages=[at(5) + 8192, at(8)]),
      "arInvalidArgument", "overlaps"),
+    ("write pairs of tokens", W, dict(WRITE, cache=layout(pageStride=8192, tokenStride=512, headStride=128),
+                                      value_pages=[at(5) + 512, at(6) + 512]), *OK),
+    ("write pairs of heads", W, dict(WRITE, cache=layout(pageStride=8192, headStride=4096), value_pages=[at(5) + 4096, at(6) + 4096]),
+     *OK),
+    ("write pairs of places", W, dict(WRITE, cache=layout(pageStride=8192, headStride=4096, tokenStride=256),
+                                      value_pages=[at(5) + 256, at(6) + 256]), *OK),
+    ("write pairs of one page's tokens", W, dict(WRITE, cache=layout(pages=1, tokenStride=512, headStride=128),
+                                                 value_pages=[at(5) + 512, at(6) + 512]), *OK),
+    ("write pairs of tokens that overlap", W, dict(WRITE, cache=layout(pageStride=8192, tokenStride=512, headStride=128),
+                                                   value_pages=[at(5) + 496, at(6) + 496]), "arInvalidArgument", "overlaps"),
+    ("write pairs of tokens past the token", W, dict(WRITE, cache=layout(pageStride=8192, tokenStride=512, headStride=128),
+                                                     value_pages=[at(5) + 528, at(6) + 528]), "arInvalidArgument", "overlaps"),
+    ("write pairs of tokens past the page", W, dict(WRITE, cache=layout(pageStride=8184, tokenStride=512, headStride=128),
+                                                    value_pages=[at(5) + 512, at(6) + 512]), "arInvalidArgument", "overlaps"),
+    ("write pairs of heads past the page", W, dict(WRITE, cache=layout(pageStride=6144, headStride=4096),
+                                                   value_pages=[at(5) + 4096, at(6) + 4096]), "arInvalidArgument", "overlaps"),
+    ("write pairs a token apart", W, dict(WRITE, cache=layout(pageStride=8192, tokenStride=512, headStride=128),
+                                          value_pages=[at(5) + 1024, at(6) + 1024]), "arInvalidArgument", "overlaps"),
     ("write pair over another rank's", W, dict(WRITE, cache=layout(pageStride=8192), key_pages=[at(5), at(5) + 8192],
                                                value_pages=[at(7), at(8)]), "arInvalidArgument", "overlaps"),
     ("write no tokens", W, dict(WRITE, tokens=0, keys=None, slots=None), "arSuccess", None),

@@ -133,6 +133,63 @@ def test_write_and_read(comm, ranks, tokens, heads, dim, page, dtype, cache, ord
         assert bool((raw(to[r].cpu()[gone]).view(torch.uint8) == ref.POISON).all()), "a row of no slot was written"
 
 
+class PairPool(ref.Pool):
+    """Keys and values next to each other inside each head or token of a page."""
+
+    def __init__(self, pages, heads, page_tokens, dim, dtype, inside):
+        super().__init__(pages, heads, page_tokens, dim, dtype, "pair")
+        both = self.raw[0][256:-256].view(dtype)
+        if inside == "head":
+            both = both.view(pages, heads, 2, page_tokens, dim)
+            self.keys, self.values = both[:, :, 0], both[:, :, 1]
+        elif inside == "token":
+            both = both.view(pages, page_tokens, 2, heads, dim).transpose(1, 3)
+            self.keys, self.values = both[:, :, 0], both[:, :, 1]
+        else:  # a token's head
+            both = both.view(pages, page_tokens, heads, 2, dim).transpose(1, 2)
+            self.keys, self.values = both[:, :, :, 0], both[:, :, :, 1]
+
+
+@pytest.mark.parametrize("inside", ["head", "token", "token's head"])
+@pytest.mark.parametrize("dtype,cache", [("bf16", "bf16"), ("fp32", "fp32"), ("fp16", "e4m3")])
+def test_pairs_inside_heads_and_tokens(comm, inside, dtype, cache):
+    note(f"cache with pairs inside a {inside} {dtype} {cache}")
+    heads, dim, page, group = 3, 80, 7, 4
+    a = Attend(2, [300, 41, 0, 1], heads, group, dim, page, dtype, cache)
+    for r, pool in enumerate(a.pools):
+        a.pools[r] = PairPool(*pool.keys.shape, DT[cache], inside)
+        ref.fill(a.pools[r], a.table, a.lengths, 50 + r)
+    comm.cache_attention(**a.args())
+    a.check()
+    # new tokens in, and back
+    slots = torch.randperm(a.pools[0].keys.shape[0] * page, generator=torch.Generator().manual_seed(3))[:100]
+    x = draw((2, 2, 100, heads, dim), 5, DT[dtype]).cuda()
+    back = torch.empty_like(x)
+    cached = pages_of(a.pools)
+    at = (slots // page).cuda(), (slots % page).cuda()
+    for p in a.pools:
+        p.raw[0][256:-256] = ref.POISON
+    comm.cache_write(list(x[0]), list(x[1]), slots.cuda(), **cached)
+    comm.cache_read(slots.cuda(), cached["key_pages"], cached["value_pages"], list(back[0]), list(back[1]),
+                    cached.get("key_scales"), cached.get("value_scales"))
+    torch.cuda.synchronize()
+    for r, p in enumerate(a.pools):
+        assert p.edges()
+        for i, which in enumerate(("key", "value")):
+            if p.eight:
+                want, tol, scale, scale_tol = ref.quantise(x[i, r].cpu())
+                s = p.key_scales if which == "key" else p.value_scales
+                block_ref.assert_within(s[at[0], :, at[1]], scale, scale_tol, "scales")
+                block_ref.assert_within(p.bytes(which)[at[0], :, at[1]].view(E4M3).float(), want, tol, "values")
+                stored = p.bytes(which)[at[0], :, at[1]].view(E4M3).float() * s[at[0], :, at[1]].unsqueeze(-1)
+                assert torch.equal(raw(back[i, r]), raw(stored.to(DT[dtype])))
+            else:
+                assert torch.equal(raw(back[i, r]), raw(x[i, r])) and torch.equal(raw(p.bytes(which)[at[0], :, at[1]]), raw(x[i, r]))
+            p.bytes(which)[at[0], :, at[1]] = torch.full((), ref.POISON, dtype=torch.uint8, device="cuda:0") if p.eight else \
+                torch.full((p.dtype.itemsize,), ref.POISON, dtype=torch.uint8, device="cuda:0").view(p.dtype)
+        assert bool((p.raw[0] == ref.POISON).all()), "a place of no token was written"
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
 def test_write_special_values(comm, dtype):
     """A token of zeros, with an infinity, with a NaN, of tiny and of the largest
