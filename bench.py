@@ -795,14 +795,26 @@ def graph_us(B, call):
     return round(statistics.median(B.graph_passes(None, None, 0, None, passes=MEDIAN_PASSES, call=call)), 2)
 
 
+def attention_off(q, keys, values, key_scales, value_scales, cached, got, got_scales):
+    """How far an 8-bit attention of q [heads, dim] over pages [n, tokens, dim] is from its
+    definition in 64 bits, in the 2-norm."""
+    k, v = ((t.double() * s.double().unsqueeze(-1)).flatten(0, 1)[:cached]
+            for t, s in ((keys, key_scales), (values, value_scales)))
+    want = (q.double() @ k.t().contiguous() / q.shape[-1] ** 0.5).softmax(-1) @ v
+    got = got.double() * got_scales.double().unsqueeze(-1)
+    return round(float((got - want).norm() / want.norm()), 5)
+
+
 def run_attention(B, seqs, cached=8192):
     """The attention half of a tensor-parallel layer over 8 ranks in a decode step:
     all-reduce of the MLP's partial sums with residual and norm into 8 bits, QKV
     product, the new tokens' keys and values into the paged 8-bit cache, attention
     of one token a sequence with an 8-bit output, output product; and the output
     product with its all-reduce in one kernel.  Sequences of `cached` tokens, the
-    new one among them, in pages of 64 that lie anywhere; the last output is
-    checked to be finite and alike on every rank."""
+    new one among them, in pages of 64 that lie anywhere.  (No position embedding: the
+    framework has none.)  The last output is checked to be finite and alike on every rank,
+    and the attention of the last sequence on the last rank against 64 bits: how far off it
+    is in the 2-norm, which is its rounding to 8 bits, 0.026."""
     torch, ar, c = B.torch, B.ar, B.comm
     ranks, hidden, group, dim, page = 8, 8192, 8, 128, 64
     e4m3, bf16, f32 = torch.float8_e4m3fn, torch.bfloat16, torch.float32
@@ -858,7 +870,9 @@ def run_attention(B, seqs, cached=8192):
     last()
     torch.cuda.synchronize()
     row["finite_and_alike"] = bool(out[0].isfinite().all()) and all(torch.equal(t, out[0]) for t in out)
-    log(f"attention half, {seqs} tokens: {row['half_us']} us; " +
+    row["attention_off"] = attention_off(queries[-1][-1], *(t[-1][table[-1].long(), 0] for t in (*pools, *scales)), cached,
+                                         att[-1][-1], att_s[-1][:, -1])
+    log(f"attention half, {seqs} tokens: {row['half_us']} us, attention {row['attention_off']} off; " +
         "  ".join(f"{k} {v}" for k, v in row["us"].items()))
     return row
 
