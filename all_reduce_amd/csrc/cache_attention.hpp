@@ -895,7 +895,10 @@ void cache_attend(CacheAttentionArgs p)
 #pragma unroll
                             for (int e = 0; e < 8; ++e)
                                 zero = __builtin_fmaf(y[e], 0.0f, zero);
-                            if (__builtin_expect(__builtin_isnan(zero) && __builtin_isfinite(total), false))
+                            // (columns past dim are no part of a row)
+                            if (__builtin_expect(__builtin_isnan(zero) && __builtin_isfinite(total) &&
+                                                     (EXACT || d0 < dim),
+                                                 false))
                                 infinities(y);
                         }
                     } else {

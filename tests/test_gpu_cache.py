@@ -652,7 +652,8 @@ def test_scores_of_plus_infinity(comm, dtype, cache, group):
 @pytest.mark.parametrize("query", [1.0, 4.0])
 @pytest.mark.parametrize("dtype,cache,out,group,dim", [
     ("bf16", None, None, 4, 64), ("fp16", None, None, 4, 128), ("fp32", None, None, 4, 64), ("bf16", None, "e4m3", 20, 128),
-    ("fp16", None, None, 40, 80), ("bf16", "e4m3", None, 4, 128), ("fp16", "e4m3", "e4m3", 8, 128), ("fp32", "e4m3", None, 20, 64)])
+    ("fp16", None, None, 40, 80), ("bf16", "e4m3", None, 5, 80), ("fp16", "e4m3", None, 20, 208), ("fp32", "e4m3", None, 3, 16),
+    ("bf16", "e4m3", None, 4, 128), ("fp16", "e4m3", "e4m3", 8, 128), ("fp32", "e4m3", None, 20, 64)])
 def test_infinite_values(comm, dtype, cache, out, group, dim, query):
     """An infinity among the values makes its column one, whatever its weight, in a sequence
     of one token as in a joined one; two of both signs and a NaN make it NaN; the other columns
