@@ -693,7 +693,7 @@ class Comm:
         self._check("page_table", [page_table], 1, (seqs, page_table.shape[1]), torch.int32)
         self._check("lengths", [lengths], 1, (seqs,), torch.int32)
         if workspace is None:
-            workspace = self.cache_workspace(dim, max(1, heads // layout.heads), stream)
+            workspace = self.cache_workspace(dim, max(1, heads // max(1, layout.heads)), stream)
         elif workspace.device != self.device or not workspace.is_contiguous():
             raise ValueError("the workspace must be a contiguous tensor on the communicator's device")
         return PreparedCall(self, "arCacheAttention", (

@@ -949,6 +949,17 @@ def test_refusals_with_a_device(comm):
         comm.cache_attention(**dict(a.args(), out=[eight], out_scales=[torch.empty((1, 1), device="cuda:0")]))
 
 
+def test_refusals_of_no_heads(comm):
+    """They are the library's, not a division by zero."""
+    note("attention of no heads")
+    a = Attend(1, [5], 2, 1, 64, 16, "bf16")
+    none = [t[:, :0] for t in (a.queries[0], a.pools[0].keys, a.pools[0].values)]
+    with pytest.raises(ar.ArError, match="Unsupported"):
+        comm.cache_attention(**dict(a.args(), key_pages=[none[1]], value_pages=[none[2]]))
+    with pytest.raises(ar.ArError, match="Unsupported"):
+        comm.cache_attention(**dict(a.args(), queries=[none[0]], out=[a.out[0][:, :0].contiguous()], lse=None))
+
+
 # ---- the attention half of a layer ---------------------------------------------
 @pytest.mark.parametrize("tokens,cache", [(1, "e4m3"), (5, "bf16"), (64, "e4m3")])
 def test_attention_half_of_a_layer(comm, tokens, cache):
