@@ -30,11 +30,11 @@
 // That is rare, so the loop has no reductions across lanes.
 //
 // Measured on MI355X, where reading alone reaches 7.1 TB/s: 64 x 8192 tokens x 8 ranks,
-// 8 query heads of 128, 318 us (6.75 TB/s of keys and values; 8 bits 171 us, 6.5);
-// 4 ranks with heads of 256 316 us (6.8); heads of 64 165 us (6.5).  A call of few tokens
+// 8 query heads of 128, 318 us (6.75 TB/s of keys and values; 8 bits 174 us, 6.4);
+// 4 ranks with heads of 256 315 us (6.8); heads of 64 163 us (6.6).  A call of few tokens
 // is one chain of loads (lengths, page, keys, queries), the waves' sums in LDS and, for a
 // unit of several teams, one or two joins through memory of 3 to 4 us: one sequence of
-// 20 tokens x 8 ranks 7.4 us, of 1000 10.6, of 8192 in 8 bits 14.9.
+// 20 tokens x 8 ranks 7.6 us, of 1000 10.6, of 8192 in 8 bits 16.0.
 #pragma once
 
 #include "block_device.hpp"

@@ -87,8 +87,11 @@ struct CachePlan {
 // than 32 query heads, two or all four of them take the same tokens and 32 heads each.
 // Where there are more units than workgroups, and short ones, each wave is a team, with
 // longer steps: a team's way into and out of a unit is a chain of loads that four waves
-// do not shorten.  On MI355X 2048 units of 33 tokens take 16 us that way and 25 with four
-// waves, of 133 tokens 37 and 44; of 333 tokens 110 and 79.
+// do not shorten.  On MI355X 2048 units of 33 tokens on the average (lengths from 1 to three
+// times as many) take 16 us that way and 26 with four waves, of 133 tokens 36 and 46, of 200
+// 51 and 60, of 333 81 and 85, but of 500 176 and 113, where a few waves have the longest
+// alone.  (Of equal lengths single waves are 4 to 10 % faster up to 1000 tokens; the rule
+// keeps clear of the loss.)
 struct CacheTeams {
     uint32_t waves;  // of a team
     uint32_t side;   // waves that take the same tokens

@@ -219,6 +219,25 @@ def test_write_special_values(comm, dtype):
         block_ref.assert_within(q[fine], want, tol, "values")
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+def test_written_8_bit_values_are_quotients(comm, dtype):
+    """Scales and values have the bits of binary32 divisions, ties among them: max / 448 and
+    y / s, rounded to nearest even.  (A product with a reciprocal, rounded, takes one value in
+    1000 to the other side of a tie.)"""
+    note(f"cache write, quotients {dtype}")
+    x = draw((20000, 2, 64), 11, DT[dtype]) * torch.rand((20000, 2, 1), generator=torch.Generator().manual_seed(3)).add(0.1).to(DT[dtype])
+    pool = ref.Pool(20000, 2, 1, 64, E4M3)
+    rows = x.cuda()
+    comm.cache_write([rows], [rows], torch.arange(20000, device="cuda:0"), **pages_of([pool]))
+    torch.cuda.synchronize()
+    y = x.float()
+    scale = y.abs().amax(-1) / torch.full((20000, 2), 448.0)
+    want = (y / scale.unsqueeze(-1).expand_as(y)).to(E4M3)
+    for which, s in (("key", pool.key_scales), ("value", pool.value_scales)):
+        assert torch.equal(raw(s[:, :, 0].cpu()), raw(scale))
+        assert torch.equal(pool.bytes(which)[:, :, 0].cpu(), raw(want))
+
+
 def test_write_of_no_tokens_and_one_row(comm):
     note("cache write of no tokens; a row of one token")
     pool = ref.Pool(1, 1, 1, 32, torch.bfloat16)
